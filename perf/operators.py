@@ -129,8 +129,9 @@ def _cache(case, g):
                   if page else None)
     if own:
         import block_sparse_attention_40_b200 as qsa
-        c = (qsa.PagedKVCache(B, cap, page, pages, s["table"], DEV, zero=False) if page
-             else qsa.KVCache(B, cap, DEV, zero=False))
+        dev = s["len"].device
+        c = (qsa.PagedKVCache(B, cap, page, pages, s["table"], dev, zero=False) if page
+             else qsa.KVCache(B, cap, dev, zero=False))
         c.k_blocks, c.v_blocks, c.kbar, c.len = s["k_blocks"], s["v_blocks"], s["kbar"], s["len"]
         c.h_len = list(lens)
         s["cache"] = c
