@@ -33,7 +33,10 @@ EXPORTS = ("qsa_status_string", "qsa_version", "qsa_launch_count", "qsa_workspac
            "qsa_decode_noalloc", "qsa_noalloc_last_device_error", "qsa_append_kv_paged",
            "qsa_decode_paged_workspace_size", "qsa_decode_paged",
            "qsa_decode_shard_workspace_size", "qsa_decode_shard_select", "qsa_merge_candidates",
-           "qsa_decode_shard_attend", "qsa_combine_partials", "qsa_gated_deltanet")
+           "qsa_decode_shard_attend", "qsa_combine_partials", "qsa_gated_deltanet",
+           "qsa_gated_deltanet_extend_workspace_size", "qsa_gated_deltanet_extend",
+           "qsa_gated_deltanet_step", "qsa_accumulate_weights", "qsa_accumulate_weights_paged",
+           "qsa_evict_workspace_size", "qsa_evict", "qsa_evict_paged")
 
 
 class QSAError(RuntimeError):
@@ -105,6 +108,15 @@ def load(build_if_needed: bool = True):
             "qsa_decode_shard_attend": ([P, P, I32, P, P, P, P, P, P, P, SZ, Params, P], st),
             "qsa_combine_partials": ([P, P, P, I32, I32, P, P], st),
             "qsa_gated_deltanet": ([P, P, P, P, P, P, P, I32, I32, P, P, P], st),
+            "qsa_gated_deltanet_extend_workspace_size": ([P, I32, I32, I32], SZ),
+            "qsa_gated_deltanet_extend": ([P, P, P, P, P, P, P, I32, I32, I32, P, I32, P, P, P, SZ,
+                                           P], st),
+            "qsa_gated_deltanet_step": ([P, P, P, P, P, I32, I32, P, I32, I32, P, I32, P, P, P], st),
+            "qsa_accumulate_weights": ([P, P, P, P, I32, P, P, SZ, P], st),
+            "qsa_accumulate_weights_paged": ([P, P, P, P, I32, P, P, SZ, P], st),
+            "qsa_evict_workspace_size": ([P, I32, I32, I32], SZ),
+            "qsa_evict": ([P, P, I32, I32, I32, P, P, SZ, P], st),
+            "qsa_evict_paged": ([P, P, I32, I32, I32, P, P, SZ, P], st),
         }
         for name, (args, res) in sig.items():
             fn = getattr(lib, name)
@@ -639,3 +651,184 @@ def gated_deltanet(q, k, v, log_alpha, beta, cu_seqlens, out=None, with_state=Fa
         _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta), _ptr(d),
         ctypes.c_void_p(h.data_ptr()), S, H, _ptr(out), _ptr(state), _stream(dev)))
     return (out, state) if with_state else out
+
+
+# --------------------------------------------------------------------------------------
+def _same_device(dev, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+
+
+def _delta_shapes(q, k, v, log_alpha, beta, states, slots, out, lead, rows):
+    """Checks of the tensors that extend and step share; `lead`: the leading dimensions of the
+    token tensors.  Returns (key_heads, heads)."""
+    nd = len(lead)
+    _need(v, "v", torch.bfloat16, (HEAD_DIM,), nd + 2)
+    _need(q, "q", torch.bfloat16, (HEAD_DIM,), nd + 2)
+    Hk, H = q.shape[nd], v.shape[nd]
+    _need(k, "k", torch.bfloat16, (Hk, HEAD_DIM), nd + 2)
+    _need(log_alpha, "log_alpha", torch.float32, (H,), nd + 1)
+    _need(beta, "beta", torch.float32, (H,), nd + 1)
+    for name, t in (("q", q), ("k", k), ("v", v), ("log_alpha", log_alpha), ("beta", beta)):
+        if tuple(t.shape[:nd]) != tuple(lead):
+            raise ValueError(f"{name} has leading dimensions {tuple(t.shape[:nd])}, expected "
+                             f"{tuple(lead)}")
+    if Hk < 1 or H % Hk:
+        raise ValueError(f"{H} heads do not divide over {Hk} key heads")
+    _need(states, "states", torch.float32, (H, HEAD_DIM, HEAD_DIM), 4)
+    if slots is not None:
+        _need(slots, "slots", torch.int32, (rows,), 1)
+    elif states.shape[0] < rows:
+        raise ValueError(f"{rows} rows need as many states, got {states.shape[0]}")
+    if out is not None:
+        _need(out, "out", torch.bfloat16, tuple(v.shape), nd + 2)
+    _same_device(v.device, q=q, k=k, log_alpha=log_alpha, beta=beta, states=states, slots=slots,
+                 out=out)
+    return Hk, H
+
+
+class DeltaExtend:
+    """Reusable context for running packed pieces of sequences through the gated delta rule:
+    holds the device cu_seqlens and the workspace.  One call of it at a time (calls on several
+    streams, or captured graphs that may replay together, take a context each)."""
+
+    def __init__(self, cu_seqlens, heads: int, device, key_heads: Optional[int] = None):
+        self.device = torch.device(device)
+        if self.device.type != "cuda":
+            raise ValueError(f"the device must be a CUDA device, got {self.device} (the library has "
+                             "no CPU path)")
+        if self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        self.heads, self.key_heads = int(heads), int(heads if key_heads is None else key_heads)
+        self.lib = load()
+        with torch.cuda.device(self.device):
+            self.h_cu, self.d_cu = _cu_pair(cu_seqlens, self.device)
+            self.num_seqs = self.h_cu.numel() - 1
+            n = self.lib.qsa_gated_deltanet_extend_workspace_size(
+                ctypes.c_void_p(self.h_cu.data_ptr()), self.num_seqs, self.key_heads, self.heads)
+            if n == 0:
+                raise QSAError("qsa_gated_deltanet_extend_workspace_size", 1)
+            self.T = int(self.h_cu[-1])
+            self.ws = new_workspace(n, self.device)
+
+    def run(self, q, k, v, log_alpha, beta, states, slots=None, out=None):
+        """q, k bf16 [T, key_heads, 128], v bf16 [T, heads, 128], log_alpha and beta fp32
+        [T, heads]; states fp32 [slots, heads, 128 (v), 128 (k)] is updated in place: sequence s
+        continues states[slots[s]] (int32 on the device; None: states[s]).  Returns out bf16
+        [T, heads, 128]."""
+        Hk, H = _delta_shapes(q, k, v, log_alpha, beta, states, slots, out, (self.T,),
+                              self.num_seqs)
+        if (Hk, H) != (self.key_heads, self.heads):
+            raise ValueError(f"{Hk} key heads and {H} heads, the context has {self.key_heads} and "
+                             f"{self.heads}")
+        _same_device(self.device, v=v)
+        if out is None:
+            out = torch.empty_like(v)
+        with torch.cuda.device(self.device):
+            _check("qsa_gated_deltanet_extend", self.lib.qsa_gated_deltanet_extend(
+                _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta), _ptr(self.d_cu),
+                ctypes.c_void_p(self.h_cu.data_ptr()), self.num_seqs, Hk, H, _ptr(states),
+                states.shape[0], _ptr(slots), _ptr(out), _ptr(self.ws), self.ws.numel(),
+                _stream(self.device)))
+        return out
+
+    def device_error(self):
+        with torch.cuda.device(self.device):
+            return last_device_error(self.ws)
+
+
+def gated_deltanet_extend(q, k, v, log_alpha, beta, cu_seqlens, states, slots=None, out=None):
+    """One DeltaExtend.run with a context of its own."""
+    ctx = DeltaExtend(cu_seqlens, v.shape[1], v.device, q.shape[1])
+    return ctx.run(q, k, v, log_alpha, beta, states, slots, out)
+
+
+def gated_deltanet_step(q, k, v, log_alpha, beta, states, slots=None, counts=None, out=None):
+    """The gated delta rule token by token for a decode batch: q, k bf16 [B, n, key_heads, 128],
+    v bf16 [B, n, heads, 128], log_alpha and beta fp32 [B, n, heads]; states as DeltaExtend.run
+    takes them, slots int32 [B] on the device (-1: an unused row) or None, counts int32 [B] on
+    the device (row b takes its first counts[b] tokens) or None.  Returns out bf16
+    [B, n, heads, 128]; rows that are not taken are left as they were (zero in a new tensor)."""
+    if not isinstance(v, torch.Tensor) or v.dim() != 4:
+        raise ValueError("v must be a [B, n, heads, 128] tensor")
+    B, n = v.shape[:2]
+    Hk, H = _delta_shapes(q, k, v, log_alpha, beta, states, slots, out, (B, n), B)
+    if counts is not None:
+        _need(counts, "counts", torch.int32, (B,), 1)
+        _same_device(v.device, counts=counts)
+    if out is None:
+        out = torch.empty_like(v) if slots is None and counts is None else torch.zeros_like(v)
+    with torch.cuda.device(v.device):
+        _check("qsa_gated_deltanet_step", load().qsa_gated_deltanet_step(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta), B, n, _ptr(counts), Hk, H,
+            _ptr(states), states.shape[0], _ptr(slots), _ptr(out), _stream(v.device)))
+    return out
+
+
+class Evictor:
+    """Eviction from a decode cache (contiguous or paged) by accumulated attention weight: holds
+    the running weights `mass` (fp32 [batch, capacity / 4], zero at first unless given) and the
+    workspace."""
+
+    def __init__(self, cache: KVCache, keep_blocks: int, sink_blocks: int = 0,
+                 recent_blocks: int = 0, mass: Optional[torch.Tensor] = None):
+        self.cache = cache
+        self.keep, self.sinks, self.recent = int(keep_blocks), int(sink_blocks), int(recent_blocks)
+        self.lib = load()
+        self._paged = isinstance(cache, PagedKVCache)
+        desc = cache.desc()
+        base = desc.base if self._paged else desc
+        n = self.lib.qsa_evict_workspace_size(ctypes.byref(base), self.keep, self.sinks,
+                                              self.recent)
+        if n == 0:
+            raise QSAError("qsa_evict_workspace_size", 1)
+        shape = (cache.batch, cache.capacity // BLOCK)
+        dev = cache.len.device
+        if mass is None:
+            mass = torch.zeros(shape, dtype=torch.float32, device=dev)
+        _need(mass, "mass", torch.float32, shape, 2)
+        _same_device(dev, mass=mass)
+        self.mass = mass
+        with torch.cuda.device(dev):
+            self.ws = new_workspace(n, dev)
+
+    def accumulate(self, q, sel_idx, sel_cnt):
+        """Add the attention weights of one decode step: its q [B, 24, 128] and the selection it
+        returned (Decoder.run(with_selection=True)).  Returns mass."""
+        B = self.cache.batch
+        _need(q, "q", torch.bfloat16, (B, NUM_HEADS, HEAD_DIM), 3)
+        _need(sel_idx, "sel_idx", torch.int32, ndim=2)
+        _need(sel_cnt, "sel_cnt", torch.int32, (B,), 1)
+        if sel_idx.shape[0] != B:
+            raise ValueError(f"sel_idx has {sel_idx.shape[0]} rows, the cache {B} sequences")
+        dev = self.mass.device
+        _same_device(dev, q=q, sel_idx=sel_idx, sel_cnt=sel_cnt)
+        desc = self.cache.desc()
+        name = "qsa_accumulate_weights" + ("_paged" if self._paged else "")
+        with torch.cuda.device(dev):
+            _check(name, getattr(self.lib, name)(
+                _ptr(q), ctypes.byref(desc), _ptr(sel_idx), _ptr(sel_cnt), sel_idx.shape[1],
+                _ptr(self.mass), _ptr(self.ws), self.ws.numel(), _stream(dev)))
+        return self.mass
+
+    def evict(self, with_kept: bool = False):
+        """Cut every sequence of more than keep_blocks complete blocks to keep_blocks (in place;
+        the cache's lengths follow).  With with_kept, returns the old indices of the blocks that
+        stay, int32 [B, keep_blocks] (-1 padded)."""
+        dev = self.mass.device
+        kept = (torch.empty((self.cache.batch, self.keep), dtype=torch.int32, device=dev)
+                if with_kept else None)
+        desc = self.cache.desc()
+        name = "qsa_evict" + ("_paged" if self._paged else "")
+        with torch.cuda.device(dev):
+            _check(name, getattr(self.lib, name)(
+                ctypes.byref(desc), _ptr(self.mass), self.keep, self.sinks, self.recent,
+                _ptr(kept), _ptr(self.ws), self.ws.numel(), _stream(dev)))
+        self.cache.h_len = [BLOCK * self.keep + n % BLOCK if n // BLOCK > self.keep else n
+                            for n in self.cache.h_len]
+        return kept
+
+    def device_error(self):
+        with torch.cuda.device(self.mass.device):
+            return last_device_error(self.ws)

@@ -11,6 +11,8 @@
 #include "../../include/qsa.h"
 #include "qsa_attn.cuh"
 #include "qsa_common.cuh"
+#include "qsa_delta.cuh"
+#include "qsa_evict.cuh"
 #include "qsa_gdn.cuh"
 #include "qsa_misc.cuh"
 #include "qsa_score.cuh"
@@ -1197,3 +1199,256 @@ extern "C" qsa_status qsa_gated_deltanet(const void* q, const void* k, const voi
   QSA_CHECK_LAUNCH();
   return QSA_OK;
 }
+
+// ---- the gated delta rule from and to a pool of states ---------------------------------------
+namespace {
+// Arguments that extend and step share.
+qsa_status delta_args(const void* q, const void* k, const void* v, const float* log_alpha,
+                      const float* beta, int32_t rows, int32_t key_heads, int32_t heads,
+                      float* states, int32_t num_slots, const int32_t* slots, void* out,
+                      DeltaArgs* a) {
+  for (const void* p : {q, k, v, static_cast<const void*>(states), static_cast<const void*>(out)}) {
+    if (!p) return QSA_ERR_INVALID_ARG;
+    if (!aligned16(p)) return QSA_ERR_ALIGNMENT;
+  }
+  if (!log_alpha || !beta) return QSA_ERR_INVALID_ARG;
+  for (const void* p : {static_cast<const void*>(log_alpha), static_cast<const void*>(beta),
+                        static_cast<const void*>(slots)})
+    if (reinterpret_cast<uintptr_t>(p) % 4 != 0) return QSA_ERR_ALIGNMENT;
+  if (rows < 1 || rows > 65535 || heads < 1 || heads > 256 || key_heads < 1 ||
+      heads % key_heads != 0 || num_slots < 1)
+    return QSA_ERR_INVALID_ARG;
+  if (!slots && num_slots < rows) return QSA_ERR_INVALID_ARG;
+  a->q = static_cast<const __nv_bfloat16*>(q);
+  a->k = static_cast<const __nv_bfloat16*>(k);
+  a->v = static_cast<const __nv_bfloat16*>(v);
+  a->log_alpha = log_alpha;
+  a->beta = beta;
+  a->slots = slots;
+  a->num_slots = num_slots;
+  a->rows = rows;
+  a->heads = heads;
+  a->key_heads = key_heads;
+  a->states = states;
+  a->out = static_cast<__nv_bfloat16*>(out);
+  return QSA_OK;
+}
+
+qsa_status launch_delta_step(const DeltaArgs& a, cudaStream_t s) {
+  k_delta_step<2><<<dim3(a.heads, a.rows, 4), kStepThreads, 0, s>>>(a);
+  QSA_CHECK_LAUNCH();
+  return QSA_OK;
+}
+
+qsa_status extend_check_cu(const int32_t* h_cu, int32_t num_seqs) {
+  if (!h_cu || num_seqs < 1 || num_seqs > 65535 || h_cu[0] != 0) return QSA_ERR_INVALID_ARG;
+  for (int32_t i = 0; i < num_seqs; ++i)
+    if (h_cu[i + 1] < h_cu[i]) return QSA_ERR_INVALID_ARG;
+  return QSA_OK;
+}
+}  // namespace
+
+extern "C" size_t qsa_gated_deltanet_extend_workspace_size(const int32_t* h_cu_seqlens,
+                                                           int32_t num_seqs, int32_t key_heads,
+                                                           int32_t heads) {
+  if (extend_check_cu(h_cu_seqlens, num_seqs) != QSA_OK || heads < 1 || heads > 256 ||
+      key_heads < 1 || heads % key_heads != 0)
+    return 0;
+  return QSA_WS_HEADER_BYTES;
+}
+
+extern "C" qsa_status qsa_gated_deltanet_extend(
+    const void* q, const void* k, const void* v, const float* log_alpha, const float* beta,
+    const int32_t* d_cu_seqlens, const int32_t* h_cu_seqlens, int32_t num_seqs, int32_t key_heads,
+    int32_t heads, float* states, int32_t num_slots, const int32_t* slots, void* out,
+    void* workspace, size_t ws_bytes, qsa_stream_t stream) {
+  DeltaArgs a{};
+  qsa_status st = extend_check_cu(h_cu_seqlens, num_seqs);
+  if (st == QSA_OK)
+    st = delta_args(q, k, v, log_alpha, beta, num_seqs, key_heads, heads, states, num_slots, slots,
+                    out, &a);
+  if (st != QSA_OK) return st;
+  if (!d_cu_seqlens || !workspace) return QSA_ERR_INVALID_ARG;
+  if (!aligned16(workspace) || reinterpret_cast<uintptr_t>(d_cu_seqlens) % 4 != 0)
+    return QSA_ERR_ALIGNMENT;
+  if (ws_bytes < qsa_gated_deltanet_extend_workspace_size(h_cu_seqlens, num_seqs, key_heads, heads))
+    return QSA_ERR_WORKSPACE;
+  a.cu = d_cu_seqlens;
+  a.tokens = h_cu_seqlens[num_seqs];
+  if (a.tokens == 0) return QSA_OK;
+  return launch_delta_step(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" qsa_status qsa_gated_deltanet_step(const void* q, const void* k, const void* v,
+                                              const float* log_alpha, const float* beta,
+                                              int32_t batch, int32_t n_new, const int32_t* counts,
+                                              int32_t key_heads, int32_t heads, float* states,
+                                              int32_t num_slots, const int32_t* slots, void* out,
+                                              qsa_stream_t stream) {
+  DeltaArgs a{};
+  const qsa_status st = delta_args(q, k, v, log_alpha, beta, batch, key_heads, heads, states,
+                                   num_slots, slots, out, &a);
+  if (st != QSA_OK) return st;
+  if (n_new < 0) return QSA_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(counts) % 4 != 0) return QSA_ERR_ALIGNMENT;
+  if (n_new == 0) return QSA_OK;
+  a.n_new = n_new;
+  a.counts = counts;
+  a.tokens = static_cast<int64_t>(batch) * n_new;
+  return launch_delta_step(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+// ---- eviction by accumulated attention weight --------------------------------------------------
+namespace {
+qsa_status check_cache_geom(const qsa_cache* c) {
+  if (!c || c->batch <= 0 || c->batch > 65535 || c->capacity <= 0 || c->capacity % 4 != 0 ||
+      c->capacity > QSA_MAX_SEQ_LEN)
+    return QSA_ERR_INVALID_ARG;
+  return QSA_OK;
+}
+
+qsa_status weights_impl(const void* q, const CacheView& view, const int32_t* sel_idx,
+                        const int32_t* sel_cnt, int32_t topk, float* mass, void* workspace,
+                        size_t ws_bytes, qsa_stream_t stream) {
+  const qsa_cache* c = view.c;
+  qsa_status st = check_cache_geom(c);
+  if (st != QSA_OK) return st;
+  st = check_prefill_ptrs({q, c->k_blocks, c->len, sel_idx, sel_cnt, mass, workspace});
+  if (st != QSA_OK) return st;
+  if (topk < 1 || topk > QSA_MAX_TOPK) return QSA_ERR_INVALID_ARG;
+  if (ws_bytes < QSA_WS_HEADER_BYTES) return QSA_ERR_WORKSPACE;
+  WeightArgs a{};
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.k_blocks = static_cast<const __nv_bfloat16*>(c->k_blocks);
+  a.len = c->len;
+  a.idx = sel_idx;
+  a.cnt = sel_cnt;
+  a.topk = topk;
+  a.cap_blocks = c->capacity / kBlock;
+  a.mass = mass;
+  a.pg = view.pg;
+  a.st = dev_status(workspace);
+  // as many CTAs to a sequence as keep the grid within two CTAs an SM
+  int cluster = 8;
+  while (cluster > 1 && int64_t(cluster) * c->batch > 2 * num_sms()) cluster /= 2;
+  const int smem = wt_smem_bytes(topk, cluster);
+  if (!set_smem(k_block_weights, smem)) return QSA_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(cluster, c->batch);
+  cfg.blockDim = dim3(kWtThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  QSA_CHECK_PDL(cudaLaunchKernelEx(&cfg, k_block_weights, a));
+  return QSA_OK;
+}
+
+struct EvictGeom {
+  size_t o_meta = 0, o_src = 0, total = 0;
+};
+
+qsa_status evict_geom(const qsa_cache* c, int32_t keep, int32_t sinks, int32_t recent,
+                      EvictGeom* g) {
+  const qsa_status st = check_cache_geom(c);
+  if (st != QSA_OK) return st;
+  if (keep < 1 || keep > QSA_MAX_SEQ_LEN / 4 || sinks < 0 || recent < 0 || sinks > keep ||
+      recent > keep - sinks)
+    return QSA_ERR_INVALID_ARG;
+  Carver cv;
+  g->o_meta = cv.take(static_cast<size_t>(c->batch) * sizeof(EvictMeta));
+  g->o_src = cv.take(static_cast<size_t>(c->batch) * (static_cast<size_t>(keep) + 1) * 4);
+  g->total = cv.off;
+  return QSA_OK;
+}
+
+qsa_status evict_impl(const CacheView& view, float* mass, int32_t keep, int32_t sinks,
+                      int32_t recent, int32_t* kept, void* workspace, size_t ws_bytes,
+                      qsa_stream_t stream) {
+  const qsa_cache* c = view.c;
+  EvictGeom g;
+  qsa_status st = evict_geom(c, keep, sinks, recent, &g);
+  if (st != QSA_OK) return st;
+  st = check_prefill_ptrs({c->k_blocks, c->v_blocks, c->kbar, c->len, mass, workspace});
+  if (st != QSA_OK) return st;
+  if (kept && !aligned16(kept)) return QSA_ERR_ALIGNMENT;
+  if (ws_bytes < g.total) return QSA_ERR_WORKSPACE;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  EvictArgs a{};
+  a.len = c->len;
+  a.mass = mass;
+  a.cap_blocks = c->capacity / kBlock;
+  a.batch = c->batch;
+  a.keep = keep;
+  a.sinks = sinks;
+  a.recent = recent;
+  a.kept = kept;
+  a.src = reinterpret_cast<int32_t*>(ws + g.o_src);
+  a.meta = reinterpret_cast<EvictMeta*>(ws + g.o_meta);
+  a.k_blocks = static_cast<uint4*>(c->k_blocks);
+  a.v_blocks = static_cast<uint4*>(c->v_blocks);
+  a.kbar = static_cast<uint4*>(c->kbar);
+  a.pg = view.pg;
+  a.st = dev_status(workspace);
+  k_evict_select<<<c->batch, kEvThreads, 0, s>>>(a);
+  QSA_CHECK_LAUNCH();
+  // enough column parts for two CTAs an SM
+  a.parts = 1;
+  while (a.parts < 16 && int64_t(4) * a.parts * c->batch < 2 * num_sms()) a.parts *= 2;
+  k_evict_move<<<dim3(4 * a.parts + 2, c->batch), kMvThreads, 0, s>>>(a);
+  QSA_CHECK_LAUNCH();
+  return QSA_OK;
+}
+}  // namespace
+
+extern "C" {
+
+qsa_status qsa_accumulate_weights(const void* q, const qsa_cache* cache, const int32_t* sel_idx,
+                                  const int32_t* sel_cnt, int32_t topk, float* mass,
+                                  void* workspace, size_t ws_bytes, qsa_stream_t stream) {
+  if (!cache) return QSA_ERR_INVALID_ARG;
+  return weights_impl(q, contiguous_view(cache), sel_idx, sel_cnt, topk, mass, workspace, ws_bytes,
+                      stream);
+}
+
+qsa_status qsa_accumulate_weights_paged(const void* q, const qsa_paged_cache* cache,
+                                        const int32_t* sel_idx, const int32_t* sel_cnt,
+                                        int32_t topk, float* mass, void* workspace,
+                                        size_t ws_bytes, qsa_stream_t stream) {
+  CacheView view;
+  const qsa_status st = paged_view(cache, &view);
+  if (st != QSA_OK) return st;
+  return weights_impl(q, view, sel_idx, sel_cnt, topk, mass, workspace, ws_bytes, stream);
+}
+
+size_t qsa_evict_workspace_size(const qsa_cache* cache, int32_t keep_blocks, int32_t sink_blocks,
+                                int32_t recent_blocks) {
+  EvictGeom g;
+  return evict_geom(cache, keep_blocks, sink_blocks, recent_blocks, &g) == QSA_OK ? g.total : 0;
+}
+
+qsa_status qsa_evict(const qsa_cache* cache, float* mass, int32_t keep_blocks, int32_t sink_blocks,
+                     int32_t recent_blocks, int32_t* kept, void* workspace, size_t ws_bytes,
+                     qsa_stream_t stream) {
+  if (!cache) return QSA_ERR_INVALID_ARG;
+  return evict_impl(contiguous_view(cache), mass, keep_blocks, sink_blocks, recent_blocks, kept,
+                    workspace, ws_bytes, stream);
+}
+
+qsa_status qsa_evict_paged(const qsa_paged_cache* cache, float* mass, int32_t keep_blocks,
+                           int32_t sink_blocks, int32_t recent_blocks, int32_t* kept,
+                           void* workspace, size_t ws_bytes, qsa_stream_t stream) {
+  CacheView view;
+  const qsa_status st = paged_view(cache, &view);
+  if (st != QSA_OK) return st;
+  return evict_impl(view, mass, keep_blocks, sink_blocks, recent_blocks, kept, workspace, ws_bytes,
+                    stream);
+}
+
+}  // extern "C"

@@ -412,6 +412,102 @@ QSA_API qsa_status qsa_gated_deltanet(const void *q, const void *k, const void *
                                       int32_t num_seqs, int32_t heads, void *out,
                                       float *final_state, qsa_stream_t stream);
 
+/* ---------------------------------------------------------------------------------- */
+/* The gated delta rule from and to a pool of states: prompts that arrive in pieces, and
+ * decoding.  The update and its gates are qsa_gated_deltanet's; the state of every sequence
+ * lives in a slot of a caller-owned pool, is read at the start of its tokens and written back
+ * after them:
+ *   states  fp32 [num_slots][heads][128 (v)][128 (k)], 16-byte aligned (zero a slot to start a
+ *           sequence)
+ *   slots   int32 on the device, the slot of each sequence (row); NULL: row r has slot r.  A
+ *           row whose slot lies outside 0 .. num_slots-1 (-1 marks the unused rows of a padded
+ *           batch) is skipped: neither a state nor its rows of out are written.  Of several
+ *           rows that name one slot the first takes it and the others are skipped.
+ *   q, k    bf16 [tokens][key_heads][128];  v, out  bf16 [tokens][heads][128] (16-byte aligned)
+ *   log_alpha, beta  fp32 [tokens][heads]
+ * heads 1..256, a multiple of key_heads: value head h reads key head h / (heads / key_heads).
+ * The arithmetic keeps about fp32 accuracy in the states; out is rounded once to bf16.
+ *
+ * qsa_gated_deltanet_extend takes packed sequences as qsa_gated_deltanet does (d_cu_seqlens,
+ * h_cu_seqlens, num_seqs; sequences may be empty), in chunks, with scratch space of
+ * qsa_gated_deltanet_extend_workspace_size bytes (0: bad arguments).  Calls that may run at the
+ * same time need workspaces (and slots) of their own, and so do captured graphs. */
+QSA_API size_t qsa_gated_deltanet_extend_workspace_size(const int32_t *h_cu_seqlens,
+                                                        int32_t num_seqs, int32_t key_heads,
+                                                        int32_t heads);
+
+QSA_API qsa_status qsa_gated_deltanet_extend(const void *q, const void *k, const void *v,
+                                             const float *log_alpha, const float *beta,
+                                             const int32_t *d_cu_seqlens,
+                                             const int32_t *h_cu_seqlens, int32_t num_seqs,
+                                             int32_t key_heads, int32_t heads, float *states,
+                                             int32_t num_slots, const int32_t *slots, void *out,
+                                             void *workspace, size_t ws_bytes,
+                                             qsa_stream_t stream);
+
+/* qsa_gated_deltanet_step takes n_new tokens of each of batch rows ([batch][n_new] in place of
+ * [tokens] above), token by token: one new token a row, or a short drafted run.  counts int32
+ * [batch] on the device (each clamped to 0..n_new) or NULL: row b takes its first counts[b]
+ * tokens, as qsa_append_kv does; the rest of its rows of out are left as they were.  No
+ * workspace. */
+QSA_API qsa_status qsa_gated_deltanet_step(const void *q, const void *k, const void *v,
+                                           const float *log_alpha, const float *beta,
+                                           int32_t batch, int32_t n_new, const int32_t *counts,
+                                           int32_t key_heads, int32_t heads, float *states,
+                                           int32_t num_slots, const int32_t *slots, void *out,
+                                           qsa_stream_t stream);
+
+/* ---------------------------------------------------------------------------------- */
+/* Eviction from a decode cache by accumulated attention weight.  The cache grows by every
+ * token, and a decode step's indexer reads the compressed key of every block; blocks that the
+ * queries never attend to can go.
+ *   mass  fp32 [batch][capacity/4], caller-owned: the running weight of every block of the cache
+ *         (zero it with len)
+ *
+ * qsa_accumulate_weights adds one decode step's attention weights: for the queries q (bf16
+ * [batch][24][128], at position len-1) and the selection sel_idx int32 [batch][topk] / sel_cnt
+ * int32 [batch] that the decode call returned for them,
+ *     mass[b][blk] += sum over the 24 heads and blk's tokens of the head's softmax weight
+ * for every selected block and the query's own block.  topk 1..QSA_MAX_TOPK.  The sums run in a
+ * fixed order.  A selected block that is not above the one before it in its row, or not before
+ * the own block, is left out and recorded as QSA_ERR_DEVICE, as are a count or a length out of
+ * range (nothing is added for that sequence) and a bad page (its keys read as zeros).
+ * workspace: at least QSA_WS_HEADER_BYTES (device status only). */
+QSA_API qsa_status qsa_accumulate_weights(const void *q, const qsa_cache *cache,
+                                          const int32_t *sel_idx, const int32_t *sel_cnt,
+                                          int32_t topk, float *mass, void *workspace,
+                                          size_t ws_bytes, qsa_stream_t stream);
+
+QSA_API qsa_status qsa_accumulate_weights_paged(const void *q, const qsa_paged_cache *cache,
+                                                const int32_t *sel_idx, const int32_t *sel_cnt,
+                                                int32_t topk, float *mass, void *workspace,
+                                                size_t ws_bytes, qsa_stream_t stream);
+
+/* qsa_evict cuts every sequence that holds more than keep_blocks complete blocks to exactly
+ * keep_blocks: its first sink_blocks, its last recent_blocks and, of the blocks between, those
+ * of largest mass (the lower block among equals; a NaN counts below every number).  The kept
+ * blocks (K, V, compressed key, mass) move together in place, in order; the incomplete last
+ * block and kbar_partial follow; the mass behind them is zeroed and len becomes 4 * keep_blocks
+ * plus the incomplete block's tokens.  Shorter sequences stay as they are.  keep_blocks >= 1,
+ * sink_blocks + recent_blocks <= keep_blocks.  The keys move as they are: a position that the
+ * caller rotated into a key stays in it.
+ *   kept  int32 [batch][keep_blocks] or NULL: the blocks that stay, by their old index, ascending
+ *         (-1 padded where a sequence holds fewer)
+ * A length out of range leaves its sequence alone and is recorded as QSA_ERR_DEVICE, as is a
+ * page table entry out of range (a block there reads as zeros and is not written).  A paged
+ * cache's table stays as it is: the pages behind the new length are the caller's to reuse.
+ * workspace: qsa_evict_workspace_size bytes (0: bad arguments; a paged cache passes its base). */
+QSA_API size_t qsa_evict_workspace_size(const qsa_cache *cache, int32_t keep_blocks,
+                                        int32_t sink_blocks, int32_t recent_blocks);
+
+QSA_API qsa_status qsa_evict(const qsa_cache *cache, float *mass, int32_t keep_blocks,
+                             int32_t sink_blocks, int32_t recent_blocks, int32_t *kept,
+                             void *workspace, size_t ws_bytes, qsa_stream_t stream);
+
+QSA_API qsa_status qsa_evict_paged(const qsa_paged_cache *cache, float *mass, int32_t keep_blocks,
+                                   int32_t sink_blocks, int32_t recent_blocks, int32_t *kept,
+                                   void *workspace, size_t ws_bytes, qsa_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

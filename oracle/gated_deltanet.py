@@ -55,3 +55,22 @@ def gated_deltanet(q, k, v, log_alpha, beta, cu_seqlens, with_state=False):
                 out[t, h] = S @ q[t, h]
             states[s, h] = S
     return (out, states) if with_state else out
+
+
+def gated_delta_rule(q, k, v, log_alpha, beta, state):
+    """The same recurrence for one sequence entered with `state`, value heads grouped over key
+    heads: q, k [T][Hk][d_k]; v [T][H][d_v]; log_alpha, beta [T][H]; state [H][d_v][d_k]; value
+    head h reads key head h // (H // Hk), and log_alpha below -87 counts as -87.  Returns the
+    outputs [T][H][d_v] and the state after the last token (fp64)."""
+    q, k, v, log_alpha, beta = (np.asarray(x, dtype=np.float64)
+                                for x in (q, k, v, log_alpha, beta))
+    S = np.array(state, dtype=np.float64)
+    rep = v.shape[1] // k.shape[1]
+    out = np.zeros(v.shape)
+    for t in range(v.shape[0]):
+        kt, qt = np.repeat(k[t], rep, axis=0), np.repeat(q[t], rep, axis=0)     # [H][d_k]
+        S = np.exp(np.maximum(log_alpha[t], -87.0))[:, None, None] * S
+        u = beta[t][:, None] * (v[t] - np.einsum("hvk,hk->hv", S, kt))
+        S = S + u[:, :, None] * kt[:, None, :]
+        out[t] = np.einsum("hvk,hk->hv", S, qt)
+    return out, S
