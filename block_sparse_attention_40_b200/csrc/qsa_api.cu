@@ -1246,6 +1246,65 @@ qsa_status extend_check_cu(const int32_t* h_cu, int32_t num_seqs) {
     if (h_cu[i + 1] < h_cu[i]) return QSA_ERR_INVALID_ARG;
   return QSA_OK;
 }
+
+// How a call of extend runs: heads in passes that keep the records within a budget, and long
+// sequences cut into segments of seg_chunks chunks where that fills the SMs better.
+struct ExtendPlan {
+  int64_t records = 0, max_chunks = 0, seg_slots = 0;
+  int32_t pass_heads = 1, seg_chunks = 1, segs = 1;
+  size_t o_rec = 0, o_state = 0, o_trans = 0, total = 0;
+};
+
+constexpr int64_t kRecordBudget = int64_t(5) << 29;   // 2.7 GB: every listed size in one pass
+
+void extend_plan(const int32_t* h_cu, int32_t num_seqs, int32_t heads, ExtendPlan* p) {
+  const int64_t tokens = h_cu[num_seqs];
+  p->records = tokens / kGdnChunk + num_seqs;
+  const int64_t per_head = p->records * kRecBytes;
+  int64_t hp = std::max<int64_t>(1, std::min<int64_t>(heads, kRecordBudget / per_head));
+  const int64_t passes = (heads + hp - 1) / hp;
+  hp = (heads + passes - 1) / passes;
+  p->pass_heads = static_cast<int32_t>(hp);
+  int64_t total = 0;
+  for (int32_t i = 0; i < num_seqs; ++i) {
+    const int64_t nc = (int64_t(h_cu[i + 1]) - h_cu[i] + kGdnChunk - 1) / kGdnChunk;
+    p->max_chunks = std::max(p->max_chunks, nc);
+    total += nc;
+  }
+  // Time of a launch, in chunks: its longest walk, or all walks over the SMs.  Cut, the walks
+  // but the last segment's run twice more without outputs (states and transitions, about 0.8
+  // of a chunk's time each), and the join takes about half a chunk's time per segment.
+  const double sms = num_sms();
+  auto spread = [&](double longest, double all) { return std::max(longest, all / sms); };
+  double best = spread(double(p->max_chunks), double(total) * hp);
+  int64_t L = std::max<int64_t>(1, p->max_chunks);
+  for (int64_t k = 3; k <= 256 && k <= p->max_chunks / 2; k += 1 + k / 16) {
+    const int64_t l = (p->max_chunks + k - 1) / k;
+    double inner = 0;
+    for (int32_t i = 0; i < num_seqs; ++i) {
+      const int64_t nc = (int64_t(h_cu[i + 1]) - h_cu[i] + kGdnChunk - 1) / kGdnChunk;
+      const int64_t segs = (nc + l - 1) / l;
+      if (segs > 1) inner += double((2 * segs - 3) * l);
+    }
+    const double t = 0.8 * spread(double(l), inner * hp) + 0.5 * double(k) + 4 +
+                     spread(double(l), double(total) * hp);
+    if (t < 0.9 * best) {
+      best = t;
+      L = l;
+    }
+  }
+  p->seg_chunks = static_cast<int32_t>(L);
+  p->segs = static_cast<int32_t>((p->max_chunks + L - 1) / L);
+  Carver cv;
+  p->o_rec = cv.take(static_cast<size_t>(per_head * hp));
+  if (p->segs > 1) {
+    p->seg_slots = p->records / L + num_seqs;
+    const size_t bytes = static_cast<size_t>(p->seg_slots) * hp * kGdnDim * kGdnDim * 4;
+    p->o_state = cv.take(bytes);
+    p->o_trans = cv.take(bytes);
+  }
+  p->total = cv.off;
+}
 }  // namespace
 
 extern "C" size_t qsa_gated_deltanet_extend_workspace_size(const int32_t* h_cu_seqlens,
@@ -1254,7 +1313,9 @@ extern "C" size_t qsa_gated_deltanet_extend_workspace_size(const int32_t* h_cu_s
   if (extend_check_cu(h_cu_seqlens, num_seqs) != QSA_OK || heads < 1 || heads > 256 ||
       key_heads < 1 || heads % key_heads != 0)
     return 0;
-  return QSA_WS_HEADER_BYTES;
+  ExtendPlan p;
+  extend_plan(h_cu_seqlens, num_seqs, heads, &p);
+  return p.total;
 }
 
 extern "C" qsa_status qsa_gated_deltanet_extend(
@@ -1262,21 +1323,54 @@ extern "C" qsa_status qsa_gated_deltanet_extend(
     const int32_t* d_cu_seqlens, const int32_t* h_cu_seqlens, int32_t num_seqs, int32_t key_heads,
     int32_t heads, float* states, int32_t num_slots, const int32_t* slots, void* out,
     void* workspace, size_t ws_bytes, qsa_stream_t stream) {
-  DeltaArgs a{};
+  DeltaChunkArgs a{};
   qsa_status st = extend_check_cu(h_cu_seqlens, num_seqs);
   if (st == QSA_OK)
     st = delta_args(q, k, v, log_alpha, beta, num_seqs, key_heads, heads, states, num_slots, slots,
-                    out, &a);
+                    out, &a.d);
   if (st != QSA_OK) return st;
   if (!d_cu_seqlens || !workspace) return QSA_ERR_INVALID_ARG;
   if (!aligned16(workspace) || reinterpret_cast<uintptr_t>(d_cu_seqlens) % 4 != 0)
     return QSA_ERR_ALIGNMENT;
-  if (ws_bytes < qsa_gated_deltanet_extend_workspace_size(h_cu_seqlens, num_seqs, key_heads, heads))
-    return QSA_ERR_WORKSPACE;
-  a.cu = d_cu_seqlens;
-  a.tokens = h_cu_seqlens[num_seqs];
-  if (a.tokens == 0) return QSA_OK;
-  return launch_delta_step(a, reinterpret_cast<cudaStream_t>(stream));
+  ExtendPlan p;
+  extend_plan(h_cu_seqlens, num_seqs, heads, &p);
+  if (ws_bytes < p.total) return QSA_ERR_WORKSPACE;
+  a.d.cu = d_cu_seqlens;
+  a.d.tokens = h_cu_seqlens[num_seqs];
+  if (a.d.tokens == 0) return QSA_OK;
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  a.rec = ws + p.o_rec;
+  a.records = p.records;
+  a.seg_chunks = p.seg_chunks;
+  a.seg_slots = p.seg_slots;
+  if (p.segs > 1) {
+    a.seg_state = reinterpret_cast<float*>(ws + p.o_state);
+    a.seg_trans = reinterpret_cast<float*>(ws + p.o_trans);
+  }
+  a.st = dev_status(workspace);
+  const int prep_smem = static_cast<int>(sizeof(PrepSmem));
+  if (!set_smem(k_delta_prep, prep_smem) || !set_smem(k_delta_scan, kScanSmemBytes))
+    return QSA_ERR_CUDA;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  for (int32_t h0 = 0; h0 < heads; h0 += p.pass_heads) {
+    a.head0 = h0;
+    a.nheads = std::min(p.pass_heads, heads - h0);
+    k_delta_prep<<<dim3(static_cast<unsigned>(p.records), a.nheads), kPrepThreads, prep_smem, s>>>(a);
+    QSA_CHECK_LAUNCH();
+    if (p.segs > 1) {
+      k_delta_scan<<<dim3(a.nheads, num_seqs, 2 * (p.segs - 1)), kScanThreads, kScanSmemBytes, s>>>(
+          a, kScanEnds);
+      QSA_CHECK_LAUNCH();
+      if (p.segs > 2) {
+        k_delta_join<<<dim3(a.nheads, num_seqs, kGdnDim / kJoinRows), kGdnDim, 0, s>>>(a);
+        QSA_CHECK_LAUNCH();
+      }
+    }
+    k_delta_scan<<<dim3(a.nheads, num_seqs, p.segs), kScanThreads, kScanSmemBytes, s>>>(
+        a, p.segs > 1 ? kScanOutputs : kScanWhole);
+    QSA_CHECK_LAUNCH();
+  }
+  return QSA_OK;
 }
 
 extern "C" qsa_status qsa_gated_deltanet_step(const void* q, const void* k, const void* v,

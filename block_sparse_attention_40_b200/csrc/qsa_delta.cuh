@@ -12,6 +12,8 @@
 
 #pragma once
 
+#include <cuda_fp16.h>
+
 #include "qsa_common.cuh"
 #include "qsa_gdn.cuh"
 
@@ -149,6 +151,1000 @@ __global__ void __launch_bounds__(kStepThreads) k_delta_step(DeltaArgs a) {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       __stcs(reinterpret_cast<float4*>(st + i * kGdnDim + 32 * j), S[i][j]);
+}
+
+// ---------------------------------------------------------------------------------------
+// In chunks.  With S0 the state that a chunk of C = 64 tokens is entered with, g_t the running
+// sum of its log gates, L the strictly lower part of diag(beta) (e^(g_t - g_j) k_t.k_j) and
+// Tu = (I + L)^-1,
+//     T = Tu diag(beta),   W = T diag(e^g) K,   U = T V - W S0^T      (what the tokens write)
+//     O = diag(e^g) Q S0^T + M U,   M_tj = e^(g_t - g_j) q_t.k_j  for j <= t
+//     S = e^(g_C) S0 + (diag(e^(g_C - g)) U)^T K.
+// T, W and M do not depend on the state: k_delta_prep forms them for every chunk and head at
+// once and leaves them in a record; k_delta_scan walks the chunks in order with two dependent
+// products a chunk (W S0^T, then U^T K) on the tcgen05 tensor cores.
+//
+// q, k and v are bf16 and exact as operands; the fp32 operands go in as parts.  What a token
+// writes carries T and U straight into the state: three bf16 parts each, x = hi + mid + lo to
+// 2^-24 of x.  W and S meet in a sum over 128 columns: two fp16 parts each (hi + lo to 2^-22 of
+// x), every row scaled by a power of two so that its largest entry lies in [2^7, 2^8); the
+// product lo lo (2^-24) is left out.  Operands that only the bf16 output sees carry less: the
+// fp16 hi of S in Q S^T, two bf16 parts of M and U.  Sums are fp32 throughout, running log gates
+// fp64 (a reset adds -87, after which fp32 differences would be off by 2^-11).
+
+// A record: operand tiles in the layout that the tensor core reads (rows of 128 bytes, 16-byte
+// words exchanged within 8 rows), then the gates.
+constexpr int kRecW = 0;                    // -W [64 t][128 d] fp16: hi (two 64-column panels), lo
+constexpr int kRecT = 32768;                // T [64 t][64 j] bf16: hi, mid, lo
+constexpr int kRecM = 57344;                // M [64 t][64 j] bf16: hi, lo
+constexpr int kRecQ = 73728;                // Q [64 t][128 d] fp16, rows scaled (two panels)
+constexpr int kRecGate = 90112;             // fp32: four tables of 64 (kGate..)
+constexpr int kRecBytes = 91136;
+constexpr int kGateQ = 0;                   // e^g over the scale of the Q row
+constexpr int kGateU = 64;                  // e^(g_C - g)
+constexpr int kGateC = 128;                 // e^(g_C)
+constexpr int kGateW = 192;                 // 1 over the scale of the W row
+
+// Byte of element (r, c) of a [rows][64] bf16 tile.
+__host__ __device__ constexpr uint32_t tile_byte(uint32_t r, uint32_t c) {
+  return r * 128 + (((c >> 3) ^ (r & 7)) << 4) + (c & 7) * 2;
+}
+
+// First record of sequence s whose tokens start at `begin`: sequences never overlap, since
+// floor(end / 64) - floor(begin / 64) + 1 >= ceil((end - begin) / 64).
+__host__ __device__ constexpr int64_t delta_first_record(int64_t begin, int s) {
+  return begin / kGdnChunk + s;
+}
+
+struct DeltaChunkArgs {
+  DeltaArgs d;
+  int32_t head0, nheads;     // the heads of this pass
+  unsigned char* rec;        // [records][nheads][kRecBytes]
+  int64_t records;
+  int32_t seg_chunks;        // chunks of a segment (a sequence is walked by one CTA a segment)
+  int64_t seg_slots;
+  float* seg_state;          // [segment slots][nheads][128][128]: state at the segment's end
+  float* seg_trans;          // the same shape: the segment's transition (P of S0 P + S)
+  DevStatus st;
+};
+
+__device__ __forceinline__ void split_bf16x2(float x, float y, uint32_t* hi, uint32_t* lo) {
+  *hi = pack_bf16x2(x, y);
+  *lo = pack_bf16x2(x - __uint_as_float(*hi << 16), y - __uint_as_float(*hi & 0xffff0000u));
+}
+// The same with hi cut off instead of rounded (fewer instructions, |x - hi - lo| <= 2^-17 |x|).
+__device__ __forceinline__ void cut_bf16x2(float x, float y, uint32_t* hi, uint32_t* lo) {
+  const uint32_t a = __float_as_uint(x), b = __float_as_uint(y);
+  *hi = __byte_perm(a, b, 0x7632);
+  *lo = pack_bf16x2(x - __uint_as_float(a & 0xffff0000u), y - __uint_as_float(b & 0xffff0000u));
+}
+
+__device__ __forceinline__ void cut3_bf16x2(float x, float y, uint32_t* hi, uint32_t* mid,
+                                            uint32_t* lo) {
+  const uint32_t a = __float_as_uint(x), b = __float_as_uint(y);
+  *hi = __byte_perm(a, b, 0x7632);
+  cut_bf16x2(x - __uint_as_float(a & 0xffff0000u), y - __uint_as_float(b & 0xffff0000u), mid, lo);
+}
+__device__ __forceinline__ void split_f16x2(float x, float y, uint32_t* hi, uint32_t* lo) {
+  const __half2 h = __floats2half2_rn(x, y);
+  const float2 f = __half22float2(h);
+  const __half2 l = __floats2half2_rn(x - f.x, y - f.y);
+  *hi = *reinterpret_cast<const uint32_t*>(&h);
+  *lo = *reinterpret_cast<const uint32_t*>(&l);
+}
+// The power of two that brings a largest magnitude m into [2^7, 2^8), and its inverse (rows of
+// zeros, or below 2^-119, take that of 2^-119).
+__device__ __forceinline__ float row_scale(float m, float* inverse) {
+  const uint32_t e = max(__float_as_uint(m) >> 23, 8u);
+  *inverse = __uint_as_float((e - 7u) << 23);
+  return __uint_as_float((261u - e) << 23);
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t* r, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t* r, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// c += a b, 16 x 8 x 16, bf16 operands, fp32 accumulation
+__device__ __forceinline__ void delta_mma(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// 16 bytes global -> shared, or 16 zero bytes
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(live ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() {
+  asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+}
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst),
+               "r"(smem_u32(src)), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_store_wait() {
+  asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
+}
+
+// ---- k_delta_prep: one CTA of 256 threads per (record, head) ---------------------------------
+constexpr int kPrepThreads = 256;
+constexpr int kPrepLd = kGdnDim + 8;      // bf16 row stride of K and Q: ldmatrix without conflicts
+constexpr int kPrepLdA = kGdnChunk + 4;   // fp32 row stride of L / Tu
+struct PrepSmem {
+  // K, whose bytes become the record's Q; [Q | L], which become its W; its T and M and the gates
+  __nv_bfloat16 k[kGdnChunk * kPrepLd];
+  __nv_bfloat16 q[kGdnChunk * kPrepLd];
+  float a[kGdnChunk * kPrepLdA];
+  unsigned char tail[kRecQ - kRecT];
+  float gate[256];
+  double g[kGdnChunk];
+  float beta[kGdnChunk];
+  float eg[kGdnChunk];
+  float wmax[2][kGdnChunk];
+};
+static_assert(sizeof(__nv_bfloat16) * kGdnChunk * kPrepLd + 4 * kGdnChunk * kPrepLdA >= kRecT, "W fits");
+static_assert(sizeof(__nv_bfloat16) * kGdnChunk * kPrepLd % 16 == 0, "aligned");
+
+__global__ void __launch_bounds__(kPrepThreads) k_delta_prep(DeltaChunkArgs ca) {
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  PrepSmem& S = *reinterpret_cast<PrepSmem*>(smem_raw);
+  const DeltaArgs& a = ca.d;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, tq = lane & 3;
+  const int64_t r = blockIdx.x;
+  // the last sequence whose first record is not past r
+  int lo = 0, hi = a.rows - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (delta_first_record(a.cu[mid], mid) <= r) lo = mid;
+    else hi = mid - 1;
+  }
+  int64_t len;
+  const int64_t begin = delta_row_tokens(a, lo, &len);
+  const int64_t c = r - delta_first_record(begin, lo);
+  if (c < 0 || c * kGdnChunk >= len) return;
+  const int64_t t0 = begin + c * kGdnChunk;
+  const int n = static_cast<int>(len - c * kGdnChunk < kGdnChunk ? len - c * kGdnChunk : kGdnChunk);
+  const int h = ca.head0 + blockIdx.y, kh = h / (a.heads / a.key_heads);
+  for (int e = tid; e < kGdnChunk * 16; e += kPrepThreads) {
+    const int t = e >> 4, d = (e & 15) * 8;
+    const int64_t off = ((t0 + (t < n ? t : 0)) * a.key_heads + kh) * kGdnDim + d;
+    cp_async16(smem_u32(&S.k[t * kPrepLd + d]), a.k + off, t < n);
+    cp_async16(smem_u32(&S.q[t * kPrepLd + d]), a.q + off, t < n);
+  }
+  float* gate = S.gate;
+  if (warp == 0) {
+    // two tokens a lane: an inclusive scan of the clamped log gates
+    float la[2], bt[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int t = 2 * lane + i;
+      la[i] = bt[i] = 0.f;
+      if (t < n) {
+        la[i] = fmaxf(a.log_alpha[(t0 + t) * a.heads + h], kGdnMinLogAlpha);
+        bt[i] = a.beta[(t0 + t) * a.heads + h];
+      }
+    }
+    const double pair = static_cast<double>(la[0]) + static_cast<double>(la[1]);
+    double incl = pair;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const double y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const double g0 = incl - pair + la[0], gc = __shfl_sync(0xffffffffu, incl, 31);
+    S.g[2 * lane] = g0;
+    S.g[2 * lane + 1] = incl;
+    S.beta[2 * lane] = bt[0];
+    S.beta[2 * lane + 1] = bt[1];
+    S.eg[2 * lane] = expf(static_cast<float>(g0));
+    S.eg[2 * lane + 1] = expf(static_cast<float>(incl));
+    gate[kGateU + 2 * lane] = expf(static_cast<float>(gc - g0));
+    gate[kGateU + 2 * lane + 1] = expf(static_cast<float>(gc - incl));
+    if (lane == 0) gate[kGateC] = expf(static_cast<float>(gc));
+  }
+  cp_async_wait_all();
+  __syncthreads();
+  const int rb = warp & 3;                       // 16 rows
+  const int ta = 16 * rb + gq, tb = ta + 8;
+  {
+    // K K^T (warps 0..3) and Q K^T (4..7), the columns that the causal mask keeps
+    const bool isq = warp >= 4;
+    float acc[8][4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
+    const __nv_bfloat16* ap = (isq ? S.q : S.k) + (16 * rb + (lane & 15)) * kPrepLd + 8 * (lane >> 4);
+    const __nv_bfloat16* bp = S.k + (lane & 7) * kPrepLd + 8 * (lane >> 3);
+#pragma unroll
+    for (int k0 = 0; k0 < kGdnDim; k0 += 32) {
+      uint32_t fa[2][4];
+      ldsm4(fa[0], smem_u32(ap + k0));
+      ldsm4(fa[1], smem_u32(ap + k0 + 16));
+#pragma unroll
+      for (int nt = 0; nt < 8; ++nt) {
+        if (nt < 2 * (rb + 1)) {
+          uint32_t fb[4];
+          ldsm4(fb, smem_u32(bp + 8 * nt * kPrepLd + k0));
+          delta_mma(acc[nt], fa[0], fb[0], fb[1]);
+          delta_mma(acc[nt], fa[1], fb[2], fb[3]);
+        }
+      }
+    }
+    const double ga = S.g[ta], gb = S.g[tb];
+    const float ba = S.beta[ta], bb = S.beta[tb];
+    unsigned char* mt = S.tail + (kRecM - kRecT);
+#pragma unroll
+    for (int nt = 0; nt < 8; ++nt) {
+      const int j = 8 * nt + 2 * tq;
+      float x[4] = {0.f, 0.f, 0.f, 0.f};
+      if (nt < 2 * (rb + 1)) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int t = e < 2 ? ta : tb, jj = j + (e & 1);
+          const bool in = isq ? jj <= t : jj < t;
+          if (in) x[e] = expf(static_cast<float>((e < 2 ? ga : gb) - S.g[jj])) * acc[nt][e];
+        }
+      }
+      if (isq) {
+        uint32_t vh, vl;
+        split_bf16x2(x[0], x[1], &vh, &vl);
+        *reinterpret_cast<uint32_t*>(mt + tile_byte(ta, j)) = vh;
+        *reinterpret_cast<uint32_t*>(mt + 8192 + tile_byte(ta, j)) = vl;
+        split_bf16x2(x[2], x[3], &vh, &vl);
+        *reinterpret_cast<uint32_t*>(mt + tile_byte(tb, j)) = vh;
+        *reinterpret_cast<uint32_t*>(mt + 8192 + tile_byte(tb, j)) = vl;
+      } else {
+        *reinterpret_cast<float2*>(&S.a[ta * kPrepLdA + j]) = make_float2(ba * x[0], ba * x[1]);
+        *reinterpret_cast<float2*>(&S.a[tb * kPrepLdA + j]) = make_float2(bb * x[2], bb * x[3]);
+      }
+    }
+  }
+  __syncthreads();
+  // Tu = (I + L)^-1 in place, by halves: the two 32 x 32 diagonal blocks by forward
+  // substitution (a warp each, a column a lane), then the block below them, -T22 (L21 T11)
+  if (warp < 2) {
+    const int o = 32 * warp;
+    float u[32];
+#pragma unroll
+    for (int t = 0; t < 32; ++t) {
+      float acc[4] = {t == lane ? 1.f : 0.f, 0.f, 0.f, 0.f};
+      const float* row = &S.a[(o + t) * kPrepLdA + o];
+#pragma unroll
+      for (int j = 0; j + 4 <= t; j += 4) {
+        const float4 l = *reinterpret_cast<const float4*>(row + j);
+        acc[0] = fmaf(-l.x, u[j], acc[0]);
+        acc[1] = fmaf(-l.y, u[j + 1], acc[1]);
+        acc[2] = fmaf(-l.z, u[j + 2], acc[2]);
+        acc[3] = fmaf(-l.w, u[j + 3], acc[3]);
+      }
+#pragma unroll
+      for (int j = t & ~3; j < t; ++j) acc[j & 3] = fmaf(-row[j], u[j], acc[j & 3]);
+      u[t] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int t = 0; t < 32; ++t) S.a[(o + t) * kPrepLdA + o + lane] = u[t];
+  }
+  __syncthreads();
+  {
+    // four rows a warp, a column a lane; L21 T11 goes to the unused upper block
+    const int i0 = 4 * warp;
+    float y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k0 = 0; k0 < 32; k0 += 4) {
+      float t[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) t[k] = S.a[(k0 + k) * kPrepLdA + lane];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 l = *reinterpret_cast<const float4*>(&S.a[(32 + i0 + i) * kPrepLdA + k0]);
+        y[i] = fmaf(l.x, t[0], fmaf(l.y, t[1], fmaf(l.z, t[2], fmaf(l.w, t[3], y[i]))));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) S.a[(i0 + i) * kPrepLdA + 32 + lane] = y[i];
+    __syncthreads();
+    float z[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k0 = 0; k0 < 32; k0 += 4) {
+      float t[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) t[k] = S.a[(k0 + k) * kPrepLdA + 32 + lane];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 l = *reinterpret_cast<const float4*>(&S.a[(32 + i0 + i) * kPrepLdA + 32 + k0]);
+        z[i] = fmaf(l.x, t[0], fmaf(l.y, t[1], fmaf(l.z, t[2], fmaf(l.w, t[3], z[i]))));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) S.a[(32 + i0 + i) * kPrepLdA + lane] = -z[i];
+  }
+  __syncthreads();
+  {
+    // T = Tu diag(beta): 16 columns of one row a thread
+    const int t = tid >> 2, j0 = 16 * (tid & 3);
+    unsigned char* tt = S.tail;
+    const bool zero = t < 32 && j0 >= 32;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      uint32_t vh[4], vm[4], vl[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int j = j0 + 8 * b + 2 * e;
+        const float x = zero ? 0.f : S.a[t * kPrepLdA + j] * S.beta[j];
+        const float y = zero ? 0.f : S.a[t * kPrepLdA + j + 1] * S.beta[j + 1];
+        cut3_bf16x2(x, y, &vh[e], &vm[e], &vl[e]);
+      }
+      const uint32_t at = tile_byte(t, j0 + 8 * b);
+      *reinterpret_cast<uint4*>(tt + at) = make_uint4(vh[0], vh[1], vh[2], vh[3]);
+      *reinterpret_cast<uint4*>(tt + 8192 + at) = make_uint4(vm[0], vm[1], vm[2], vm[3]);
+      *reinterpret_cast<uint4*>(tt + 16384 + at) = make_uint4(vl[0], vl[1], vl[2], vl[3]);
+    }
+  }
+  // Q as fp16 with scaled rows: a quarter of a row a thread, in registers until K is done with
+  uint32_t qv[16];
+  {
+    const int t = tid >> 2, d0 = 32 * (tid & 3);
+    uint4 raw[4];
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      raw[i] = *reinterpret_cast<const uint4*>(&S.q[t * kPrepLd + d0 + 8 * i]);
+      const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        m = fmaxf(m, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
+    }
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    float inv;
+    const float sc = row_scale(m, &inv);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const __half2 x = __floats2half2_rn(__uint_as_float(w[e] << 16) * sc,
+                                            __uint_as_float(w[e] & 0xffff0000u) * sc);
+        qv[4 * i + e] = *reinterpret_cast<const uint32_t*>(&x);
+      }
+    }
+    if ((tid & 3) == 0) gate[kGateQ + t] = S.eg[t] * inv;
+  }
+  {
+    // W = (Tu diag(beta e^g)) K: warp = 16 rows x 64 columns of K
+    const int d0 = 64 * (warp >> 2);
+    float acc[8][4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
+    const __nv_bfloat16* bp = S.k + (lane & 15) * kPrepLd + d0 + 8 * (lane >> 4);
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) {
+      if (ks <= rb) {
+        uint32_t fh[4], fm[4], fl[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int t = (e & 1) ? tb : ta, j = 16 * ks + 2 * tq + 8 * (e >> 1);
+          const float2 x = *reinterpret_cast<const float2*>(&S.a[t * kPrepLdA + j]);
+          const float2 w = make_float2(S.beta[j] * S.eg[j], S.beta[j + 1] * S.eg[j + 1]);
+          cut3_bf16x2(x.x * w.x, x.y * w.y, &fh[e], &fm[e], &fl[e]);
+        }
+#pragma unroll
+        for (int np = 0; np < 4; ++np) {
+          uint32_t fb[4];
+          ldsm4_t(fb, smem_u32(bp + 16 * ks * kPrepLd + 16 * np));
+          delta_mma(acc[2 * np], fh, fb[0], fb[1]);
+          delta_mma(acc[2 * np + 1], fh, fb[2], fb[3]);
+          delta_mma(acc[2 * np], fm, fb[0], fb[1]);
+          delta_mma(acc[2 * np + 1], fm, fb[2], fb[3]);
+          delta_mma(acc[2 * np], fl, fb[0], fb[1]);
+          delta_mma(acc[2 * np + 1], fl, fb[2], fb[3]);
+        }
+      }
+    }
+    float ma = 0.f, mb = 0.f;
+#pragma unroll
+    for (int nt = 0; nt < 8; ++nt) {
+      ma = fmaxf(ma, fmaxf(fabsf(acc[nt][0]), fabsf(acc[nt][1])));
+      mb = fmaxf(mb, fmaxf(fabsf(acc[nt][2]), fabsf(acc[nt][3])));
+    }
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, o));
+      mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, o));
+    }
+    if (tq == 0) {
+      S.wmax[warp >> 2][ta] = ma;
+      S.wmax[warp >> 2][tb] = mb;
+    }
+    __syncthreads();   // also: K, Q and Tu have been read
+    float ia, ib;
+    const float sa = -row_scale(fmaxf(S.wmax[0][ta], S.wmax[1][ta]), &ia);
+    const float sb = -row_scale(fmaxf(S.wmax[0][tb], S.wmax[1][tb]), &ib);
+    if (warp < 4 && tq == 0) {
+      gate[kGateW + ta] = ia;
+      gate[kGateW + tb] = ib;
+    }
+    unsigned char* w = reinterpret_cast<unsigned char*>(S.q) + 8192 * (warp >> 2);
+#pragma unroll
+    for (int nt = 0; nt < 8; ++nt) {
+      uint32_t vh, vl;
+      const int d = 8 * nt + 2 * tq;
+      split_f16x2(sa * acc[nt][0], sa * acc[nt][1], &vh, &vl);
+      *reinterpret_cast<uint32_t*>(w + tile_byte(ta, d)) = vh;
+      *reinterpret_cast<uint32_t*>(w + 16384 + tile_byte(ta, d)) = vl;
+      split_f16x2(sb * acc[nt][2], sb * acc[nt][3], &vh, &vl);
+      *reinterpret_cast<uint32_t*>(w + tile_byte(tb, d)) = vh;
+      *reinterpret_cast<uint32_t*>(w + 16384 + tile_byte(tb, d)) = vl;
+    }
+    const int t = tid >> 2, q4 = tid & 3;   // columns 32 q4 ..: panel q4 / 2
+    unsigned char* qd = reinterpret_cast<unsigned char*>(S.k) + 8192 * (q4 >> 1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<uint4*>(qd + tile_byte(t, 32 * (q4 & 1) + 8 * i)) =
+          make_uint4(qv[4 * i], qv[4 * i + 1], qv[4 * i + 2], qv[4 * i + 3]);
+  }
+  fence_proxy_async_smem();
+  __syncthreads();
+  if (tid == 0) {
+    unsigned char* rec = ca.rec + (r * ca.nheads + blockIdx.y) * static_cast<int64_t>(kRecBytes);
+    bulk_store(rec + kRecW, S.q, kRecT);
+    bulk_store(rec + kRecT, S.tail, kRecQ - kRecT);
+    bulk_store(rec + kRecQ, S.k, kRecGate - kRecQ);
+    bulk_store(rec + kRecGate, S.gate, kRecBytes - kRecGate);
+    bulk_store_wait();
+  }
+}
+
+// ---- k_delta_scan: one CTA per (head, sequence, segment) --------------------------------------
+// With v along the 128 lanes of tensor memory, every operand that depends on the state is an A
+// operand in tensor memory, written there by the threads that computed it, and no result goes
+// back to shared memory:
+//     D_T [v][t] = V^T T^T          A = V (shared)
+//     D_W [v][t] = -S0 W^T          A = S0 (fp16 parts)
+//     D_Q [v][t] = S0 Q^T, then U^T M^T
+//     D_S [v][d] = U'^T K,  U' = diag(e^(g_C - g)) U,  U = D_T + D_W
+// Two warpgroups hold the fp32 state in registers (a lane has one v, 64 of its d's), form U and
+// U' and then S; a third writes the outputs.  Three warps load, each its own operands, whose
+// space is free again as soon as their last product is done.
+constexpr int kScanThreads = 512;
+constexpr int kScanW = 0;                               // [2] W, K, gates
+constexpr int kScanWBytes = 32768 + 16384 + 1024;
+constexpr int kScanQ = kScanW + 2 * kScanWBytes;        // [2] Q, M
+constexpr int kScanQBytes = 32768;
+constexpr int kScanT = kScanQ + 2 * kScanQBytes;        // T, V
+constexpr int kScanTBytes = 24576 + 16384;
+constexpr int kScanOut = kScanT + kScanTBytes;          // outputs on their way: 4 KB a warp
+constexpr int kScanBars = kScanOut + 16384;
+constexpr int kScanSmemBytes = kScanBars + 4096;
+static_assert(kScanSmemBytes <= 232448, "shared memory per CTA");
+static_assert(kScanWBytes % 1024 == 0 && kScanTBytes % 1024 == 0, "tiles on 1 KB boundaries");
+
+// what a launch does: the whole walk; or, for a sequence cut into segments, their states from
+// zero and their transitions (pass 0), then the outputs from the joined states (pass 1)
+constexpr int kScanWhole = 0, kScanEnds = 1, kScanOutputs = 2;
+
+struct ScanBars {
+  uint64_t full_t, empty_t, full_w[2], empty_w[2], full_q[2], empty_q[2];
+  uint64_t s_full, d1, uw_full, u_full, ds, qs, q_free, o, o_free, mma_done;
+  uint64_t rows[4];           // the two warps of 32 rows have their maxima in place
+  uint32_t tmem;
+  int abort;
+  float scale[2][kGdnDim];    // 1 over the scale of each row of S, by the parity of the chunk
+  float rowmax[2][kGdnDim];   // largest |S| of each half row
+};
+static_assert(sizeof(ScanBars) <= 4096, "barriers");
+
+__device__ __forceinline__ void tmem_ld16_at(uint32_t taddr, float* f) {
+  uint32_t r[16];
+  tmem_ld16(taddr, r);
+  tmem_wait_ld();
+  asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+               "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+               "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
+#pragma unroll
+  for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(r[i]);
+}
+
+__global__ void __launch_bounds__(kScanThreads, 1) k_delta_scan(DeltaChunkArgs ca, int mode) {
+  extern __shared__ __align__(1024) unsigned char smem[];
+  ScanBars& B = *reinterpret_cast<ScanBars*>(smem + kScanBars);
+  const DeltaArgs& a = ca.d;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int hl = blockIdx.x, h = ca.head0 + hl, row = blockIdx.y;
+  // pass 0 has two CTAs a segment: states from zero, and transitions
+  const bool trans = mode == kScanEnds && (blockIdx.z & 1);
+  const int seg = mode == kScanEnds ? blockIdx.z >> 1 : blockIdx.z;
+  int64_t len;
+  const int64_t begin = delta_row_tokens(a, row, &len);
+  const int64_t chunks = (len + kGdnChunk - 1) / kGdnChunk;
+  const int64_t c0 = static_cast<int64_t>(seg) * ca.seg_chunks;
+  const int64_t c1 = c0 + ca.seg_chunks < chunks ? c0 + ca.seg_chunks : chunks;
+  const int nc = static_cast<int>(c1 - c0);
+  const bool last = c1 == chunks;
+  const int slot = a.slots != nullptr ? a.slots[row] : row;
+  if (nc <= 0 || slot < 0 || slot >= a.num_slots) return;
+  if (mode == kScanEnds && (last || (trans && seg == 0))) return;
+  if (delta_slot_taken(a, row, slot)) return;
+  if ((smem_u32(smem) & 1023u) != 0) {   // the tiles need it; the runtime places them so
+    if (tid == 0) report_error(ca.st, kErrDevice, 320);
+    return;
+  }
+  const bool outputs = mode != kScanEnds;
+  const int64_t rec0 = delta_first_record(begin, row);
+  const int64_t seg0 = rec0 / ca.seg_chunks + row;     // as records: segments never overlap
+  const int64_t tile = static_cast<int64_t>(kGdnDim) * kGdnDim;
+  float* state = a.states + (static_cast<int64_t>(slot) * a.heads + h) * tile;
+  const int64_t seg_stride = static_cast<int64_t>(ca.nheads) * tile;
+  float* ends = ca.seg_state + (seg0 + seg) * seg_stride + hl * tile;
+  // a cut sequence's start state waits in its last segment's place: the outputs pass reads it
+  // there, since that pass's last segment writes the pool
+  float* kept = ends + ((chunks - 1) / ca.seg_chunks - seg) * seg_stride;
+  const float* src = seg > 0 ? ends - seg_stride : mode == kScanOutputs && !last ? kept : state;
+  float* dst = mode != kScanEnds ? state : trans ? ca.seg_trans + (ends - ca.seg_state) : ends;
+  const int64_t t0 = begin + c0 * kGdnChunk;
+  const int64_t ntok = (last ? len : c1 * kGdnChunk) - c0 * kGdnChunk;
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&B.full_w[i], 2);
+      mbar_init(&B.empty_w[i], 1 + 8 + (outputs ? 4 : 0));
+      mbar_init(&B.full_q[i], 1);
+      mbar_init(&B.empty_q[i], 1);
+    }
+    mbar_init(&B.full_t, 2);
+    mbar_init(&B.empty_t, 1);
+    mbar_init(&B.s_full, 8);
+    mbar_init(&B.d1, 1);
+    mbar_init(&B.uw_full, 8);
+    mbar_init(&B.u_full, 8);
+    mbar_init(&B.ds, 1);
+    mbar_init(&B.qs, 1);
+    mbar_init(&B.q_free, 4);
+    mbar_init(&B.o, 1);
+    mbar_init(&B.o_free, 4);
+    mbar_init(&B.mma_done, 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&B.rows[i], 2);
+    B.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 12) {
+    tmem_alloc(&B.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  // all 512 columns are this CTA's, so they start at 0: addresses are known to the compiler
+  constexpr uint32_t tm = 0;
+  // columns: S hi 64, S lo 64 (U hi 32, U lo 32 once D_W is done), D_S 128, D_T 64, D_W 64 (then
+  // U' mid and lo, each half of the threads in the columns that it has read), D_Q 64, U' hi 32
+  constexpr uint32_t tS = tm, tU = tm + 64, tDS = tm + 128, tDT = tm + 256, tDW = tm + 320,
+                     tDQ = tm + 384, tUw = tm + 448;
+  volatile int* abort = &B.abort;
+  const DevStatus st = ca.st;
+
+  if (warp < 8) {
+    // ---- the state: lane = value row v, 64 columns d of it -----------------------------------
+    const int half = warp >> 2, v = 32 * (warp & 3) + lane;
+    const uint32_t lb = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    float s[64];
+    if (trans) {
+#pragma unroll
+      for (int i = 0; i < 64; ++i) s[i] = 64 * half + i == v ? 1.f : 0.f;
+    } else if (mode == kScanEnds && seg > 0) {
+#pragma unroll
+      for (int i = 0; i < 64; ++i) s[i] = 0.f;
+    } else {
+      const float4* p = reinterpret_cast<const float4*>(src + v * kGdnDim + 64 * half);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float4 x = p[i];
+        s[4 * i] = x.x;
+        s[4 * i + 1] = x.y;
+        s[4 * i + 2] = x.z;
+        s[4 * i + 3] = x.w;
+        if (mode == kScanEnds) reinterpret_cast<float4*>(kept + v * kGdnDim + 64 * half)[i] = x;
+      }
+    }
+    float inv;   // 1 over the scale of this row
+    auto put_state = [&](int c) -> bool {   // S entering chunk c, as fp16 parts
+      float m = 0.f;
+#pragma unroll
+      for (int i = 0; i < 64; ++i) m = fmaxf(m, fabsf(s[i]));
+      B.rowmax[half][v] = m;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&B.rows[warp & 3]);
+      if (!__all_sync(0xffffffffu, mbar_wait(&B.rows[warp & 3], c & 1, abort, st, 337))) return false;
+      const float sc = row_scale(fmaxf(m, B.rowmax[half ^ 1][v]), &inv);
+      if (half == 0) B.scale[c & 1][v] = inv;
+#pragma unroll
+      for (int i0 = 0; i0 < 64; i0 += 16) {
+        uint32_t vh[8], vl[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          split_f16x2(sc * s[i0 + 2 * i], sc * s[i0 + 2 * i + 1], &vh[i], &vl[i]);
+        tmem_st8(tS + lb + 32 * half + i0 / 2, vh);
+        tmem_st8(tS + lb + 64 + 32 * half + i0 / 2, vl);
+      }
+      return true;
+    };
+    auto signal = [&](uint64_t* bar) {
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
+    bool ok = put_state(0);
+    if (ok) signal(&B.s_full);
+    for (int c = 0; ok && c < nc; ++c) {
+      const int sg = c & 1;
+      const float* gate = reinterpret_cast<const float*>(smem + kScanW + sg * kScanWBytes + 49152);
+      ok = mbar_wait(&B.full_w[sg], (c >> 1) & 1, abort, st, 330) &&
+           mbar_wait(&B.d1, c & 1, abort, st, 331);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      float u[32];
+#pragma unroll
+      for (int i0 = 0; i0 < 32; i0 += 16) {
+        float x[16], y[16];
+        if (trans) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[i] = 0.f;
+        } else {
+          tmem_ld16_at(tDT + lb + 32 * half + i0, x);
+        }
+        tmem_ld16_at(tDW + lb + 32 * half + i0, y);
+        uint32_t vh[8], vm[8], vl[8];
+        const float4* wi = reinterpret_cast<const float4*>(gate + kGateW + 32 * half + i0);
+        const float4* wk = reinterpret_cast<const float4*>(gate + kGateU + 32 * half + i0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 a4 = wi[i], b4 = wk[i];
+          u[i0 + 4 * i] = fmaf(inv * a4.x, y[4 * i], x[4 * i]);
+          u[i0 + 4 * i + 1] = fmaf(inv * a4.y, y[4 * i + 1], x[4 * i + 1]);
+          u[i0 + 4 * i + 2] = fmaf(inv * a4.z, y[4 * i + 2], x[4 * i + 2]);
+          u[i0 + 4 * i + 3] = fmaf(inv * a4.w, y[4 * i + 3], x[4 * i + 3]);
+          cut3_bf16x2(b4.x * u[i0 + 4 * i], b4.y * u[i0 + 4 * i + 1], &vh[2 * i], &vm[2 * i], &vl[2 * i]);
+          cut3_bf16x2(b4.z * u[i0 + 4 * i + 2], b4.w * u[i0 + 4 * i + 3], &vh[2 * i + 1],
+                      &vm[2 * i + 1], &vl[2 * i + 1]);
+        }
+        // the first 16 tokens' mid and lo take the columns of D_W that were just read
+        tmem_st8(tUw + lb + 16 * half + i0 / 2, vh);
+        tmem_st8(tDW + lb + 32 * half + i0, vm);
+        tmem_st8(tDW + lb + 32 * half + i0 + 8, vl);
+      }
+      signal(&B.uw_full);
+      if (outputs) {
+#pragma unroll
+        for (int i0 = 0; i0 < 32; i0 += 16) {
+          uint32_t vh[8], vl[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) cut_bf16x2(u[i0 + 2 * i], u[i0 + 2 * i + 1], &vh[i], &vl[i]);
+          tmem_st8(tU + lb + 16 * half + i0 / 2, vh);
+          tmem_st8(tU + lb + 32 + 16 * half + i0 / 2, vl);
+        }
+        signal(&B.u_full);
+      }
+      const float gc = gate[kGateC];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&B.empty_w[sg]);
+      ok = mbar_wait(&B.ds, c & 1, abort, st, 332);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+#pragma unroll
+      for (int i0 = 0; i0 < 64; i0 += 16) {
+        float x[16];
+        tmem_ld16_at(tDS + lb + 64 * half + i0, x);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[i0 + i] = fmaf(gc, s[i0 + i], x[i]);
+      }
+      if (c + 1 < nc) {
+        // U, which takes the place of S lo, is done with once the outputs are
+        ok = !outputs || mbar_wait(&B.o, c & 1, abort, st, 336);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc_fence_after();
+        ok = put_state(c + 1);
+        if (ok) signal(&B.s_full);
+      }
+    }
+    // in the outputs pass the joined states hold what the inner segments would write
+    if (__all_sync(0xffffffffu, ok) && (mode == kScanEnds || last)) {
+      float4* p = reinterpret_cast<float4*>(dst + v * kGdnDim + 64 * half);
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        p[i] = make_float4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]);
+    }
+  } else if (warp < 12) {
+    // ---- outputs: lane = value v, 64 tokens --------------------------------------------------
+    if (outputs) {
+      const int v = 32 * (warp - 8) + lane;
+      const uint32_t lb = static_cast<uint32_t>(32 * (warp - 8)) << 16;
+      unsigned char* mine = smem + kScanOut + 4096 * (warp - 8);   // [64 t][32 v] bf16
+      for (int c = 0; c < nc; ++c) {
+        const int sg = c & 1;
+        const float4* eg = reinterpret_cast<const float4*>(smem + kScanW + sg * kScanWBytes + 49152) + kGateQ / 4;
+        bool ok = mbar_wait(&B.full_w[sg], (c >> 1) & 1, abort, st, 333) &&
+                  mbar_wait(&B.qs, c & 1, abort, st, 334);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc_fence_after();
+        const float inv = B.scale[c & 1][v];
+        float y[64];
+#pragma unroll
+        for (int i0 = 0; i0 < 64; i0 += 16) {
+          tmem_ld16_at(tDQ + lb + i0, y + i0);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float4 e = eg[i0 / 4 + i];
+            y[i0 + 4 * i] *= inv * e.x;
+            y[i0 + 4 * i + 1] *= inv * e.y;
+            y[i0 + 4 * i + 2] *= inv * e.z;
+            y[i0 + 4 * i + 3] *= inv * e.w;
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&B.q_free);
+          mbar_arrive(&B.empty_w[sg]);
+        }
+        ok = mbar_wait(&B.o, c & 1, abort, st, 335);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc_fence_after();
+#pragma unroll
+        for (int i0 = 0; i0 < 64; i0 += 16) {
+          float x[16];
+          tmem_ld16_at(tDQ + lb + i0, x);
+#pragma unroll
+          for (int i = 0; i < 16; i += 2) {
+            const uint32_t w = pack_bf16x2(y[i0 + i] + x[i], y[i0 + i + 1] + x[i + 1]);
+            *reinterpret_cast<uint16_t*>(mine + 64 * (i0 + i) + 2 * lane) = static_cast<uint16_t>(w);
+            *reinterpret_cast<uint16_t*>(mine + 64 * (i0 + i + 1) + 2 * lane) = static_cast<uint16_t>(w >> 16);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&B.o_free);
+        const int64_t left = ntok - static_cast<int64_t>(c) * kGdnChunk;
+        const int n = static_cast<int>(left < kGdnChunk ? left : kGdnChunk);
+        const int64_t step = static_cast<int64_t>(a.heads) * kGdnDim;
+        // four lanes to a token: its 32 values as 16-byte words
+        __nv_bfloat16* op = a.out + ((t0 + static_cast<int64_t>(c) * kGdnChunk) * a.heads + h) * kGdnDim +
+                            32 * (warp - 8) + 8 * (lane & 3);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int t = 8 * i + (lane >> 2);
+          if (t < n)
+            *reinterpret_cast<uint4*>(op + t * step) =
+                *reinterpret_cast<const uint4*>(mine + 64 * t + 16 * (lane & 3));
+        }
+        __syncwarp();   // the next chunk overwrites `mine`
+      }
+    }
+  } else if (warp == 12) {
+    // ---- products: the whole warp walks the loop, one elected lane issues ----------------------
+    constexpr uint32_t kIdTV = idesc_bf16_f32(128, 64, 1, 0);   // A = V, tokens along its rows
+    constexpr uint32_t kIdN64 = idesc_bf16_f32(128, 64, 0, 0);
+    constexpr uint32_t kIdF16 = idesc_f16_f32(128, 64, 0, 0);
+    constexpr uint32_t kIdDS = idesc_bf16_f32(128, 128, 0, 1);  // B = K, tokens along its rows
+    // descriptors; a step along a tile adds its bytes / 16
+    const uint64_t dk = smem_desc_sw128(smem_u32(smem), 0, 1024);        // rows of 128 bytes
+    const uint64_t dm = smem_desc_sw128(smem_u32(smem), 8192, 1024);     // two column panels
+    auto write_values = [&](int c) -> bool {   // D_T = V^T T^T
+      if (!mbar_wait(&B.full_t, c & 1, abort, st, 340)) return false;
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int p = 0; p < 3; ++p)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            umma_ss(tDT, dm + ((kScanT + 24576 + 2048 * k) >> 4), dk + ((kScanT + 8192 * p + 32 * k) >> 4),
+                    kIdTV, p + k > 0 ? 1u : 0u);
+        umma_commit(&B.empty_t);
+      }
+      __syncwarp();
+      return true;
+    };
+    bool ok = trans || write_values(0);
+    for (int c = 0; ok && c < nc; ++c) {
+      const int sg = c & 1;
+      const uint32_t ph = (c >> 1) & 1;
+      const uint64_t sw = (kScanW + sg * kScanWBytes) >> 4, sq = (kScanQ + sg * kScanQBytes) >> 4;
+      if (!mbar_wait(&B.full_w[sg], ph, abort, st, 342)) break;
+      if (!mbar_wait(&B.s_full, c & 1, abort, st, 341)) break;
+      tc_fence_after();
+      if (elect_one()) {
+        // D_W = -S0 W^T: (hi, hi), (lo, hi), (hi, lo)
+#pragma unroll
+        for (int p = 0; p < 3; ++p)
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            umma_ts(tDW, tS + (p == 1 ? 64 : 0) + 8 * k,
+                    dk + sw + (((p == 2 ? 16384 : 0) + 8192 * (k >> 2) + 32 * (k & 3)) >> 4), kIdF16,
+                    p + k > 0 ? 1u : 0u);
+        umma_commit(&B.d1);   // covers D_T too
+      }
+      __syncwarp();
+      if (outputs) {
+        if (!mbar_wait(&B.full_q[sg], ph, abort, st, 343)) break;
+        if (c > 0 && !mbar_wait(&B.o_free, (c - 1) & 1, abort, st, 344)) break;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            umma_ts(tDQ, tS + 8 * k, dk + sq + ((8192 * (k >> 2) + 32 * (k & 3)) >> 4), kIdF16,
+                    k > 0 ? 1u : 0u);
+          umma_commit(&B.qs);
+        }
+        __syncwarp();
+      }
+      if (!mbar_wait(&B.uw_full, c & 1, abort, st, 345)) break;
+      tc_fence_after();
+      if (elect_one()) {
+        // D_S = U'^T K: hi, mid, lo; a step is 16 tokens, mid and lo at 16-column strides
+#pragma unroll
+        for (int p = 0; p < 3; ++p)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            umma_ts(tDS, p == 0 ? tUw + 8 * k : tDW + 16 * k + 8 * (p - 1),
+                    dm + sw + ((32768 + 2048 * k) >> 4), kIdDS, p + k > 0 ? 1u : 0u);
+        umma_commit(&B.ds);
+        umma_commit(&B.empty_w[sg]);
+      }
+      __syncwarp();
+      if (outputs) {
+        if (!mbar_wait(&B.q_free, c & 1, abort, st, 346)) break;
+        if (!mbar_wait(&B.u_full, c & 1, abort, st, 348)) break;
+        tc_fence_after();
+        if (elect_one()) {
+          // D_Q = U^T M^T: (hi, hi), (lo, hi), (hi, lo)
+#pragma unroll
+          for (int p = 0; p < 3; ++p)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              umma_ts(tDQ, tU + (p == 1 ? 32 : 0) + 8 * k,
+                      dk + sq + ((16384 + (p == 2 ? 8192 : 0) + 32 * k) >> 4), kIdN64,
+                      p + k > 0 ? 1u : 0u);
+          umma_commit(&B.o);
+          umma_commit(&B.empty_q[sg]);
+        }
+        __syncwarp();
+      }
+      if (!trans && c + 1 < nc && !write_values(c + 1)) break;
+    }
+    __syncwarp();
+    if (elect_one()) umma_commit(&B.mma_done);
+    mbar_drain(&B.mma_done, 0);
+    __syncwarp();
+  } else {
+    // ---- loads: warp 13: W, K and the gates; 14: T and V; 15: Q and M ---------------------------
+    const int who = warp - 13, stages = who == 1 ? 1 : 2;
+    uint64_t* full = who == 0 ? B.full_w : who == 1 ? &B.full_t : B.full_q;
+    uint64_t* empty = who == 0 ? B.empty_w : who == 1 ? &B.empty_t : B.empty_q;
+    const bool on = who == 0 || (who == 1 ? !trans : outputs);
+    const __nv_bfloat16* base = who == 0 ? a.k + h / (a.heads / a.key_heads) * kGdnDim : a.v + h * kGdnDim;
+    const int64_t step = static_cast<int64_t>(who == 0 ? a.key_heads : a.heads) * kGdnDim;
+    int issued = 0;
+    for (int c = 0; on && c < nc; ++c) {
+      const int sg = c % stages, turn = c / stages;
+      const bool ok = turn == 0 || mbar_wait(&empty[sg], (turn & 1) ^ 1, abort, st, 347);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      unsigned char* stage = smem + (who == 0 ? kScanW + sg * kScanWBytes : who == 1 ? kScanT : kScanQ + sg * kScanQBytes);
+      if (lane == 0) {
+        const unsigned char* rec = ca.rec + ((rec0 + c0 + c) * ca.nheads + hl) * static_cast<int64_t>(kRecBytes);
+        if (who == 0) {
+          mbar_arrive_expect_tx(&full[sg], 32768 + 1024);
+          bulk_load(stage, rec + kRecW, 32768, &full[sg]);
+          bulk_load(stage + 49152, rec + kRecGate, 1024, &full[sg]);
+        } else if (who == 1) {
+          mbar_arrive_expect_tx(&full[sg], 24576);
+          bulk_load(stage, rec + kRecT, 24576, &full[sg]);
+        } else {
+          mbar_arrive_expect_tx(&full[sg], 32768);
+          bulk_load(stage, rec + kRecQ, 16384, &full[sg]);
+          bulk_load(stage + 16384, rec + kRecM, 16384, &full[sg]);
+        }
+      }
+      __syncwarp();
+      ++issued;
+      if (who < 2) {
+        const int64_t left = ntok - static_cast<int64_t>(c) * kGdnChunk;
+        const int n = static_cast<int>(left < kGdnChunk ? left : kGdnChunk);
+        const uint32_t to = smem_u32(stage) + (who == 0 ? 32768 : 24576);
+        const __nv_bfloat16* from = base + (t0 + static_cast<int64_t>(c) * kGdnChunk) * step;
+#pragma unroll 8
+        for (int e = lane; e < kGdnChunk * 16; e += 32) {
+          const int t = e >> 4, w = e & 15;
+          cp_async16(to + 8192 * (w >> 3) + tile_byte(t, 8 * (w & 7)),
+                     from + (t < n ? t : 0) * step + 8 * w, t < n);
+        }
+        cp_async_wait_all();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[sg]);
+      }
+    }
+    if (lane == 0 && *abort)   // no copy may land after the CTA is gone
+      for (int c = issued > stages ? issued - stages : 0; c < issued; ++c)
+        mbar_drain(&full[c % stages], (c / stages) & 1);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tm, 512);
+  }
+}
+
+// Joins the segments of a sequence: entered with E (the state at its start), a segment ends with
+// E P + S.  Rows of the state are independent: a CTA takes 8 of them through the segments in
+// order, a thread one column.
+constexpr int kJoinRows = 8;
+
+// grid (heads of the pass, sequences, 128 / kJoinRows), 128 threads
+__global__ void __launch_bounds__(kGdnDim) k_delta_join(DeltaChunkArgs ca) {
+  __shared__ __align__(16) float e[kJoinRows][kGdnDim];
+  const DeltaArgs& a = ca.d;
+  const int row = blockIdx.y, hl = blockIdx.x, d = threadIdx.x, v0 = blockIdx.z * kJoinRows;
+  int64_t len;
+  const int64_t begin = delta_row_tokens(a, row, &len);
+  const int64_t chunks = (len + kGdnChunk - 1) / kGdnChunk;
+  const int64_t segs = (chunks + ca.seg_chunks - 1) / ca.seg_chunks;
+  if (segs < 3) return;
+  const int64_t tile = static_cast<int64_t>(kGdnDim) * kGdnDim, stride = ca.nheads * tile;
+  const int64_t at = ((delta_first_record(begin, row) / ca.seg_chunks + row) * ca.nheads + hl) * tile;
+  float* s = ca.seg_state + at + v0 * kGdnDim + d;
+  const float* p = ca.seg_trans + at + d;
+#pragma unroll
+  for (int i = 0; i < kJoinRows; ++i) e[i][d] = s[i * kGdnDim];
+  for (int64_t g = 1; g + 1 < segs; ++g) {
+    s += stride;
+    p += stride;
+    float acc[kJoinRows];
+#pragma unroll
+    for (int i = 0; i < kJoinRows; ++i) acc[i] = s[i * kGdnDim];
+    __syncthreads();
+#pragma unroll 4
+    for (int k = 0; k < kGdnDim; k += 4) {
+      float x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = p[(k + j) * kGdnDim];
+#pragma unroll
+      for (int i = 0; i < kJoinRows; ++i) {
+        const float4 y = *reinterpret_cast<const float4*>(&e[i][k]);
+        acc[i] = fmaf(y.x, x[0], fmaf(y.y, x[1], fmaf(y.z, x[2], fmaf(y.w, x[3], acc[i]))));
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kJoinRows; ++i) {
+      e[i][d] = acc[i];
+      s[i * kGdnDim] = acc[i];
+    }
+  }
 }
 
 }  // namespace qsa
