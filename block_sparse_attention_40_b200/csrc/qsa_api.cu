@@ -192,6 +192,25 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
+// Launches a kernel in clusters of c CTAs along x.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, int c,
+                           cudaStream_t s, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = c;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
 #define QSA_CHECK_PDL(expr)                                  \
   do {                                                       \
     g_launches.fetch_add(1, std::memory_order_relaxed);      \
@@ -1255,7 +1274,7 @@ struct ExtendPlan {
   size_t o_rec = 0, o_state = 0, o_trans = 0, total = 0;
 };
 
-constexpr int64_t kRecordBudget = int64_t(5) << 29;   // 2.7 GB: every listed size in one pass
+constexpr int64_t kRecordBudget = int64_t(1) << 32;
 
 void extend_plan(const int32_t* h_cu, int32_t num_seqs, int32_t heads, ExtendPlan* p) {
   const int64_t tokens = h_cu[num_seqs];
@@ -1362,7 +1381,9 @@ extern "C" qsa_status qsa_gated_deltanet_extend(
           a, kScanEnds);
       QSA_CHECK_LAUNCH();
       if (p.segs > 2) {
-        k_delta_join<<<dim3(a.nheads, num_seqs, kGdnDim / kJoinRows), kGdnDim, 0, s>>>(a);
+        if (!set_smem(k_delta_join, kJoinSmemBytes)) return QSA_ERR_CUDA;
+        k_delta_join<<<dim3(a.nheads, num_seqs, kGdnDim / kJoinRows), kGdnDim, kJoinSmemBytes,
+                       s>>>(a);
         QSA_CHECK_LAUNCH();
       }
     }
@@ -1427,24 +1448,14 @@ qsa_status weights_impl(const void* q, const CacheView& view, const int32_t* sel
   while (cluster > 1 && int64_t(cluster) * c->batch > 2 * num_sms()) cluster /= 2;
   const int smem = wt_smem_bytes(topk, cluster);
   if (!set_smem(k_block_weights, smem)) return QSA_ERR_CUDA;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(cluster, c->batch);
-  cfg.blockDim = dim3(kWtThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = cluster;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  QSA_CHECK_PDL(cudaLaunchKernelEx(&cfg, k_block_weights, a));
+  QSA_CHECK_PDL(launch_cluster(k_block_weights, dim3(cluster, c->batch), dim3(kWtThreads), smem,
+                               cluster, reinterpret_cast<cudaStream_t>(stream), a));
   return QSA_OK;
 }
 
 struct EvictGeom {
-  size_t o_meta = 0, o_src = 0, total = 0;
+  size_t o_meta = 0, o_src = 0, o_loaded = 0, o_before = 0, o_ticket = 0, total = 0;
+  int32_t tiles = 0;
 };
 
 qsa_status evict_geom(const qsa_cache* c, int32_t keep, int32_t sinks, int32_t recent,
@@ -1457,6 +1468,11 @@ qsa_status evict_geom(const qsa_cache* c, int32_t keep, int32_t sinks, int32_t r
   Carver cv;
   g->o_meta = cv.take(static_cast<size_t>(c->batch) * sizeof(EvictMeta));
   g->o_src = cv.take(static_cast<size_t>(c->batch) * (static_cast<size_t>(keep) + 1) * 4);
+  // a cache that cannot hold more than keep complete blocks has nothing to move
+  g->tiles = c->capacity / kBlock > keep ? keep / kMvPlaces + 1 : 0;
+  g->o_loaded = cv.take(static_cast<size_t>(c->batch) * g->tiles * 4);
+  g->o_before = cv.take(static_cast<size_t>(c->batch) * (g->tiles + 1) * 4);
+  g->o_ticket = cv.take(4);
   g->total = cv.off;
   return QSA_OK;
 }
@@ -1490,13 +1506,22 @@ qsa_status evict_impl(const CacheView& view, float* mass, int32_t keep, int32_t 
   a.kbar = static_cast<uint4*>(c->kbar);
   a.pg = view.pg;
   a.st = dev_status(workspace);
-  k_evict_select<<<c->batch, kEvThreads, 0, s>>>(a);
-  QSA_CHECK_LAUNCH();
-  // enough column parts for two CTAs an SM
-  a.parts = 1;
-  while (a.parts < 16 && int64_t(4) * a.parts * c->batch < 2 * num_sms()) a.parts *= 2;
-  k_evict_move<<<dim3(4 * a.parts + 2, c->batch), kMvThreads, 0, s>>>(a);
-  QSA_CHECK_LAUNCH();
+  a.tiles = g.tiles;
+  a.loaded = reinterpret_cast<int32_t*>(ws + g.o_loaded);
+  a.before = reinterpret_cast<int32_t*>(ws + g.o_before);
+  a.ticket = reinterpret_cast<int32_t*>(ws + g.o_ticket);
+  // as many CTAs to a sequence as the SMs hold, with at least 4,096 weights each (a batch of four
+  // per thread): below that the cluster's barriers cost more than its reads
+  int cluster = kEvMaxCluster;
+  while (cluster > 1 && (int64_t(cluster) * c->batch > num_sms() ||
+                         a.cap_blocks / cluster < kEvThreads * kEvBatch))
+    cluster /= 2;
+  if (cudaFuncSetAttribute(k_evict_select, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+    return QSA_ERR_CUDA;
+  QSA_CHECK_PDL(launch_cluster(k_evict_select, dim3(cluster, c->batch), dim3(kEvThreads), 0, cluster, s, a));
+  if (g.tiles > 0)
+    QSA_CHECK_PDL(launch_pdl(k_evict_move, dim3(static_cast<unsigned>(g.tiles) * c->batch),
+                             dim3(kMvThreads), 0, s, a));
   return QSA_OK;
 }
 }  // namespace

@@ -167,23 +167,25 @@ __global__ void __launch_bounds__(kStepThreads) k_delta_step(DeltaArgs a) {
 // q, k and v are bf16 and exact as operands; the fp32 operands go in as parts.  What a token
 // writes carries T and U straight into the state: three bf16 parts each, x = hi + mid + lo to
 // 2^-24 of x.  W and S meet in a sum over 128 columns: two fp16 parts each (hi + lo to 2^-22 of
-// x), every row scaled by a power of two so that its largest entry lies in [2^7, 2^8); the
-// product lo lo (2^-24) is left out.  Operands that only the bf16 output sees carry less: the
-// fp16 hi of S in Q S^T, two bf16 parts of M and U.  Sums are fp32 throughout, running log gates
-// fp64 (a reset adds -87, after which fp32 differences would be off by 2^-11).
+// x), scaled by powers of two (a row of S, all of W) so that fp16 holds them; the product lo lo
+// (2^-24) is left out.  What only the bf16 output sees, S in Q S^T and M and U, is rounded to
+// fp16 once, scaled by rows as well.  Sums are fp32 throughout, running log gates fp64 (a reset
+// adds -87, after which fp32 differences would be off by 2^-11).
 
 // A record: operand tiles in the layout that the tensor core reads (rows of 128 bytes, 16-byte
 // words exchanged within 8 rows), then the gates.
 constexpr int kRecW = 0;                    // -W [64 t][128 d] fp16: hi (two 64-column panels), lo
 constexpr int kRecT = 32768;                // T [64 t][64 j] bf16: hi, mid, lo
-constexpr int kRecM = 57344;                // M [64 t][64 j] bf16: hi, lo
-constexpr int kRecQ = 73728;                // Q [64 t][128 d] fp16, rows scaled (two panels)
-constexpr int kRecGate = 90112;             // fp32: four tables of 64 (kGate..)
-constexpr int kRecBytes = 91136;
-constexpr int kGateQ = 0;                   // e^g over the scale of the Q row
-constexpr int kGateU = 64;                  // e^(g_C - g)
+constexpr int kRecM = 57344;                // M [64 t][64 j] fp16, rows scaled
+constexpr int kRecQ = 65536;                // Q [64 t][128 d] fp16, rows scaled (two panels)
+constexpr int kRecGate = 81920;             // fp32 [256], as follows
+constexpr int kRecBytes = 82944;
+constexpr int kGateQ = 0;                   // [64] e^g over the scale of the Q row
+constexpr int kGateU = 64;                  // [64] e^(g_C - g)
 constexpr int kGateC = 128;                 // e^(g_C)
-constexpr int kGateW = 192;                 // 1 over the scale of the W row
+constexpr int kGateK = 129;                 // the largest |K|
+constexpr int kGateW = 130;                 // 1 over the scale of W
+constexpr int kGateM = 192;                 // [64] 1 over the scale of the M row
 
 // Byte of element (r, c) of a [rows][64] bf16 tile.
 __host__ __device__ constexpr uint32_t tile_byte(uint32_t r, uint32_t c) {
@@ -208,29 +210,35 @@ struct DeltaChunkArgs {
   DevStatus st;
 };
 
-__device__ __forceinline__ void split_bf16x2(float x, float y, uint32_t* hi, uint32_t* lo) {
+// x -= lo(h), y -= hi(h): one mixed-precision instruction each
+__device__ __forceinline__ void take_bf16x2(uint32_t h, float* x, float* y) {
+  asm("{\n\t.reg .b16 l, h, m;\n\tmov.b32 {l, h}, %2;\n\tmov.b16 m, 0xBF80;\n\t"
+      "fma.rn.f32.bf16 %0, l, m, %0;\n\tfma.rn.f32.bf16 %1, h, m, %1;\n\t}"
+      : "+f"(*x), "+f"(*y)
+      : "r"(h));
+}
+__device__ __forceinline__ void take_f16x2(uint32_t h, float* x, float* y) {
+  asm("{\n\t.reg .b16 l, h, m;\n\tmov.b32 {l, h}, %2;\n\tmov.b16 m, 0xBC00;\n\t"
+      "fma.rn.f32.f16 %0, l, m, %0;\n\tfma.rn.f32.f16 %1, h, m, %1;\n\t}"
+      : "+f"(*x), "+f"(*y)
+      : "r"(h));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float x, float y) {
+  const __half2 h = __floats2half2_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ void split3_bf16x2(float x, float y, uint32_t* hi, uint32_t* mid,
+                                              uint32_t* lo) {
   *hi = pack_bf16x2(x, y);
-  *lo = pack_bf16x2(x - __uint_as_float(*hi << 16), y - __uint_as_float(*hi & 0xffff0000u));
-}
-// The same with hi cut off instead of rounded (fewer instructions, |x - hi - lo| <= 2^-17 |x|).
-__device__ __forceinline__ void cut_bf16x2(float x, float y, uint32_t* hi, uint32_t* lo) {
-  const uint32_t a = __float_as_uint(x), b = __float_as_uint(y);
-  *hi = __byte_perm(a, b, 0x7632);
-  *lo = pack_bf16x2(x - __uint_as_float(a & 0xffff0000u), y - __uint_as_float(b & 0xffff0000u));
-}
-
-__device__ __forceinline__ void cut3_bf16x2(float x, float y, uint32_t* hi, uint32_t* mid,
-                                            uint32_t* lo) {
-  const uint32_t a = __float_as_uint(x), b = __float_as_uint(y);
-  *hi = __byte_perm(a, b, 0x7632);
-  cut_bf16x2(x - __uint_as_float(a & 0xffff0000u), y - __uint_as_float(b & 0xffff0000u), mid, lo);
+  take_bf16x2(*hi, &x, &y);
+  *mid = pack_bf16x2(x, y);
+  take_bf16x2(*mid, &x, &y);
+  *lo = pack_bf16x2(x, y);
 }
 __device__ __forceinline__ void split_f16x2(float x, float y, uint32_t* hi, uint32_t* lo) {
-  const __half2 h = __floats2half2_rn(x, y);
-  const float2 f = __half22float2(h);
-  const __half2 l = __floats2half2_rn(x - f.x, y - f.y);
-  *hi = *reinterpret_cast<const uint32_t*>(&h);
-  *lo = *reinterpret_cast<const uint32_t*>(&l);
+  *hi = pack_f16x2(x, y);
+  take_f16x2(*hi, &x, &y);
+  *lo = pack_f16x2(x, y);
 }
 // The power of two that brings a largest magnitude m into [2^7, 2^8), and its inverse (rows of
 // zeros, or below 2^-119, take that of 2^-119).
@@ -281,169 +289,263 @@ __device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t 
                "r"(smem_u32(src)), "r"(bytes)
                : "memory");
 }
+// until the shared memory of this thread's stores has been read
 __device__ __forceinline__ void bulk_store_wait() {
-  asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
+  asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 
 // ---- k_delta_prep: one CTA of 256 threads per (record, head) ---------------------------------
+// Bound by the latency of its steps, so four CTAs share an SM; the record leaves in pieces, each
+// by a bulk copy out of the space of an operand that is done with: Q becomes the scaled fp16 Q in
+// place, then holds M, then T hi and mid, then T lo; K and Tu become W.
 constexpr int kPrepThreads = 256;
-constexpr int kPrepLd = kGdnDim + 8;      // bf16 row stride of K and Q: ldmatrix without conflicts
-constexpr int kPrepLdA = kGdnChunk + 4;   // fp32 row stride of L / Tu
+constexpr int kPrepLdA = kGdnChunk + 8;   // fp32 row stride of L / Tu: 8 rows x 4 pairs without conflicts
 struct PrepSmem {
-  // K, whose bytes become the record's Q; [Q | L], which become its W; its T and M and the gates
-  __nv_bfloat16 k[kGdnChunk * kPrepLd];
-  __nv_bfloat16 q[kGdnChunk * kPrepLd];
-  float a[kGdnChunk * kPrepLdA];
-  unsigned char tail[kRecQ - kRecT];
+  unsigned char k[16384];                 // [64 t][128 d] bf16 as two tiles of 64 columns
+  float a[kGdnChunk * kPrepLdA];          // L, then Tu
+  unsigned char q[16384];
   float gate[256];
-  double g[kGdnChunk];
-  float beta[kGdnChunk];
-  float eg[kGdnChunk];
-  float wmax[2][kGdnChunk];
+  float g_hi[kGdnChunk], g_lo[kGdnChunk]; // running log gate in base 2, as a sum
+  float beta[kGdnChunk], eg[kGdnChunk], beg[kGdnChunk];   // beta, e^g, their product
+  float wmax[8], kmax[2];
 };
-static_assert(sizeof(__nv_bfloat16) * kGdnChunk * kPrepLd + 4 * kGdnChunk * kPrepLdA >= kRecT, "W fits");
-static_assert(sizeof(__nv_bfloat16) * kGdnChunk * kPrepLd % 16 == 0, "aligned");
+static_assert(16384 + 4 * kGdnChunk * kPrepLdA >= 32768, "W fits");
+static_assert(sizeof(PrepSmem) <= 55 * 1024, "four CTAs an SM");
 
-__global__ void __launch_bounds__(kPrepThreads) k_delta_prep(DeltaChunkArgs ca) {
-  extern __shared__ __align__(16) unsigned char smem_raw[];
+__device__ __forceinline__ float exp2_approx(float x) {   // 2 ulp; -inf gives 0
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__global__ void __launch_bounds__(kPrepThreads, 4) k_delta_prep(DeltaChunkArgs ca) {
+  extern __shared__ __align__(128) unsigned char smem_raw[];
   PrepSmem& S = *reinterpret_cast<PrepSmem*>(smem_raw);
   const DeltaArgs& a = ca.d;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, tq = lane & 3;
   const int64_t r = blockIdx.x;
-  // the last sequence whose first record is not past r
-  int lo = 0, hi = a.rows - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (delta_first_record(a.cu[mid], mid) <= r) lo = mid;
-    else hi = mid - 1;
+  // the last sequence whose first record is not past r, 256 candidates at a time
+  int seq = 0;
+  for (int step = a.rows > kPrepThreads ? kPrepThreads : 1; step > 0; step = step > 1 ? 1 : 0) {
+    const int64_t s = seq + static_cast<int64_t>(tid) * step;
+    const bool in = s < a.rows && delta_first_record(a.cu[s], static_cast<int>(s)) <= r;
+    const int m = __syncthreads_count(in);
+    seq += (m > 0 ? m - 1 : 0) * step;
   }
   int64_t len;
-  const int64_t begin = delta_row_tokens(a, lo, &len);
-  const int64_t c = r - delta_first_record(begin, lo);
+  const int64_t begin = delta_row_tokens(a, seq, &len);
+  const int64_t c = r - delta_first_record(begin, seq);
   if (c < 0 || c * kGdnChunk >= len) return;
   const int64_t t0 = begin + c * kGdnChunk;
   const int n = static_cast<int>(len - c * kGdnChunk < kGdnChunk ? len - c * kGdnChunk : kGdnChunk);
   const int h = ca.head0 + blockIdx.y, kh = h / (a.heads / a.key_heads);
-  for (int e = tid; e < kGdnChunk * 16; e += kPrepThreads) {
-    const int t = e >> 4, d = (e & 15) * 8;
-    const int64_t off = ((t0 + (t < n ? t : 0)) * a.key_heads + kh) * kGdnDim + d;
-    cp_async16(smem_u32(&S.k[t * kPrepLd + d]), a.k + off, t < n);
-    cp_async16(smem_u32(&S.q[t * kPrepLd + d]), a.q + off, t < n);
-  }
-  float* gate = S.gate;
-  if (warp == 0) {
-    // two tokens a lane: an inclusive scan of the clamped log gates
-    float la[2], bt[2];
+  unsigned char* rec = ca.rec + (r * ca.nheads + blockIdx.y) * static_cast<int64_t>(kRecBytes);
+  float la[2] = {0.f, 0.f}, bt[2] = {0.f, 0.f};
+  if (warp == 0) {   // two tokens a lane
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int t = 2 * lane + i;
-      la[i] = bt[i] = 0.f;
       if (t < n) {
         la[i] = fmaxf(a.log_alpha[(t0 + t) * a.heads + h], kGdnMinLogAlpha);
         bt[i] = a.beta[(t0 + t) * a.heads + h];
       }
     }
-    const double pair = static_cast<double>(la[0]) + static_cast<double>(la[1]);
+  }
+  const uint32_t sk = smem_u32(S.k), sq = smem_u32(S.q);
+  for (int e = tid; e < kGdnChunk * 16; e += kPrepThreads) {
+    const int t = e >> 4, w = e & 15;
+    const int64_t off = ((t0 + (t < n ? t : 0)) * a.key_heads + kh) * kGdnDim + 8 * w;
+    const uint32_t at = 8192 * (w >> 3) + tile_byte(t, 8 * (w & 7));
+    cp_async16(sk + at, a.k + off, t < n);
+    cp_async16(sq + at, a.q + off, t < n);
+  }
+  float* gate = S.gate;
+  if (warp == 0) {
+    // an inclusive scan of the clamped log gates, in base 2
+    const double l2e = 1.4426950408889634;
+    const double l0 = l2e * la[0], pair = l0 + l2e * la[1];
     double incl = pair;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const double y = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += y;
     }
-    const double g0 = incl - pair + la[0], gc = __shfl_sync(0xffffffffu, incl, 31);
-    S.g[2 * lane] = g0;
-    S.g[2 * lane + 1] = incl;
-    S.beta[2 * lane] = bt[0];
-    S.beta[2 * lane + 1] = bt[1];
-    S.eg[2 * lane] = expf(static_cast<float>(g0));
-    S.eg[2 * lane + 1] = expf(static_cast<float>(incl));
-    gate[kGateU + 2 * lane] = expf(static_cast<float>(gc - g0));
-    gate[kGateU + 2 * lane + 1] = expf(static_cast<float>(gc - incl));
-    if (lane == 0) gate[kGateC] = expf(static_cast<float>(gc));
+    const double g2[2] = {incl - pair + l0, incl}, gc = __shfl_sync(0xffffffffu, incl, 31);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int t = 2 * lane + i;
+      S.g_hi[t] = static_cast<float>(g2[i]);
+      S.g_lo[t] = static_cast<float>(g2[i] - static_cast<double>(S.g_hi[t]));
+      S.beta[t] = bt[i];
+      S.eg[t] = exp2f(static_cast<float>(g2[i]));
+      S.beg[t] = bt[i] * S.eg[t];
+      gate[kGateU + t] = exp2f(static_cast<float>(gc - g2[i]));
+    }
+    if (lane == 0) gate[kGateC] = exp2f(static_cast<float>(gc));
   }
   cp_async_wait_all();
   __syncthreads();
   const int rb = warp & 3;                       // 16 rows
   const int ta = 16 * rb + gq, tb = ta + 8;
+  const bool isq = warp >= 4;
+  float acc[8][4];
   {
     // K K^T (warps 0..3) and Q K^T (4..7), the columns that the causal mask keeps
-    const bool isq = warp >= 4;
-    float acc[8][4];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
-    const __nv_bfloat16* ap = (isq ? S.q : S.k) + (16 * rb + (lane & 15)) * kPrepLd + 8 * (lane >> 4);
-    const __nv_bfloat16* bp = S.k + (lane & 7) * kPrepLd + 8 * (lane >> 3);
+    const uint32_t ap = isq ? sq : sk;
+    const int ar = 16 * rb + (lane & 15), ac = 8 * (lane >> 4), br = lane & 7, bc = 8 * (lane >> 3);
 #pragma unroll
     for (int k0 = 0; k0 < kGdnDim; k0 += 32) {
+      const uint32_t panel = 8192 * (k0 >> 6);
       uint32_t fa[2][4];
-      ldsm4(fa[0], smem_u32(ap + k0));
-      ldsm4(fa[1], smem_u32(ap + k0 + 16));
+      ldsm4(fa[0], ap + panel + tile_byte(ar, (k0 & 63) + ac));
+      ldsm4(fa[1], ap + panel + tile_byte(ar, (k0 & 63) + 16 + ac));
 #pragma unroll
       for (int nt = 0; nt < 8; ++nt) {
         if (nt < 2 * (rb + 1)) {
           uint32_t fb[4];
-          ldsm4(fb, smem_u32(bp + 8 * nt * kPrepLd + k0));
+          ldsm4(fb, sk + panel + tile_byte(8 * nt + br, (k0 & 63) + bc));
           delta_mma(acc[nt], fa[0], fb[0], fb[1]);
           delta_mma(acc[nt], fa[1], fb[2], fb[3]);
         }
       }
     }
-    const double ga = S.g[ta], gb = S.g[tb];
-    const float ba = S.beta[ta], bb = S.beta[tb];
-    unsigned char* mt = S.tail + (kRecM - kRecT);
+    const float ha = S.g_hi[ta], hb = S.g_hi[tb], la2 = S.g_lo[ta], lb2 = S.g_lo[tb];
+    const float ba = isq ? 1.f : S.beta[ta], bb = isq ? 1.f : S.beta[tb];
 #pragma unroll
     for (int nt = 0; nt < 8; ++nt) {
-      const int j = 8 * nt + 2 * tq;
-      float x[4] = {0.f, 0.f, 0.f, 0.f};
       if (nt < 2 * (rb + 1)) {
+        const float2 jh = *reinterpret_cast<const float2*>(&S.g_hi[8 * nt + 2 * tq]);
+        const float2 jl = *reinterpret_cast<const float2*>(&S.g_lo[8 * nt + 2 * tq]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int t = e < 2 ? ta : tb, jj = j + (e & 1);
-          const bool in = isq ? jj <= t : jj < t;
-          if (in) x[e] = expf(static_cast<float>((e < 2 ? ga : gb) - S.g[jj])) * acc[nt][e];
+          const int t = e < 2 ? ta : tb, j = 8 * nt + 2 * tq + (e & 1);
+          const float d = ((e < 2 ? ha : hb) - ((e & 1) ? jh.y : jh.x)) +
+                          ((e < 2 ? la2 : lb2) - ((e & 1) ? jl.y : jl.x));
+          const bool in = isq ? j <= t : j < t;
+          acc[nt][e] = in ? exp2_approx(d) * ((e < 2 ? ba : bb) * acc[nt][e]) : 0.f;
         }
       }
-      if (isq) {
-        uint32_t vh, vl;
-        split_bf16x2(x[0], x[1], &vh, &vl);
-        *reinterpret_cast<uint32_t*>(mt + tile_byte(ta, j)) = vh;
-        *reinterpret_cast<uint32_t*>(mt + 8192 + tile_byte(ta, j)) = vl;
-        split_bf16x2(x[2], x[3], &vh, &vl);
-        *reinterpret_cast<uint32_t*>(mt + tile_byte(tb, j)) = vh;
-        *reinterpret_cast<uint32_t*>(mt + 8192 + tile_byte(tb, j)) = vl;
-      } else {
-        *reinterpret_cast<float2*>(&S.a[ta * kPrepLdA + j]) = make_float2(ba * x[0], ba * x[1]);
-        *reinterpret_cast<float2*>(&S.a[tb * kPrepLdA + j]) = make_float2(bb * x[2], bb * x[3]);
+    }
+    if (!isq) {
+#pragma unroll
+      for (int nt = 0; nt < 8; ++nt) {
+        const int j = 8 * nt + 2 * tq;
+        *reinterpret_cast<float2*>(&S.a[ta * kPrepLdA + j]) = make_float2(acc[nt][0], acc[nt][1]);
+        *reinterpret_cast<float2*>(&S.a[tb * kPrepLdA + j]) = make_float2(acc[nt][2], acc[nt][3]);
       }
     }
   }
   __syncthreads();
-  // Tu = (I + L)^-1 in place, by halves: the two 32 x 32 diagonal blocks by forward
-  // substitution (a warp each, a column a lane), then the block below them, -T22 (L21 T11)
-  if (warp < 2) {
+  if (isq) {
+    // Q as fp16 with scaled rows, in place (half a row a thread); then M in its space
+    const int t = (tid - 128) >> 1, half = tid & 1;
+    unsigned char* p = S.q + 8192 * half;
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      // the two panels' words of a row lie in the same banks: the halves take them in turn
+      const uint4 x = *reinterpret_cast<const uint4*>(p + tile_byte(t, 8 * (i ^ (4 * half))));
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        m = fmaxf(m, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
+    }
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    float inv;
+    const float sc = row_scale(m, &inv);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint4* at = reinterpret_cast<uint4*>(p + tile_byte(t, 8 * (i ^ (4 * half))));
+      const uint4 x = *at;
+      uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const __half2 y = __floats2half2_rn(__uint_as_float(w[e] << 16) * sc,
+                                            __uint_as_float(w[e] & 0xffff0000u) * sc);
+        w[e] = *reinterpret_cast<const uint32_t*>(&y);
+      }
+      *at = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    if (half == 0) gate[kGateQ + t] = S.eg[t] * inv;
+    fence_proxy_async_smem();
+    named_barrier_sync(1, 128);
+    if (tid == 128) {
+      bulk_store(rec + kRecQ, S.q, 16384);
+      bulk_store_wait();
+    }
+    named_barrier_sync(1, 128);
+    float ma = 0.f, mb = 0.f;
+#pragma unroll
+    for (int nt = 0; nt < 8; ++nt) {
+      ma = fmaxf(ma, fmaxf(fabsf(acc[nt][0]), fabsf(acc[nt][1])));
+      mb = fmaxf(mb, fmaxf(fabsf(acc[nt][2]), fabsf(acc[nt][3])));
+    }
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, o));
+      mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, o));
+    }
+    float ia, ib;
+    const float sa = row_scale(ma, &ia), sb = row_scale(mb, &ib);
+    if (tq == 0) {
+      gate[kGateM + ta] = ia;
+      gate[kGateM + tb] = ib;
+    }
+#pragma unroll
+    for (int nt = 0; nt < 8; ++nt) {
+      const int j = 8 * nt + 2 * tq;
+      *reinterpret_cast<uint32_t*>(S.q + tile_byte(ta, j)) = pack_f16x2(sa * acc[nt][0], sa * acc[nt][1]);
+      *reinterpret_cast<uint32_t*>(S.q + tile_byte(tb, j)) = pack_f16x2(sb * acc[nt][2], sb * acc[nt][3]);
+    }
+    fence_proxy_async_smem();
+    named_barrier_sync(1, 128);
+    if (tid == 128) {
+      bulk_store(rec + kRecM, S.q, 8192);
+      bulk_store_wait();
+    }
+  } else if (warp < 2) {
+    // Tu = (I + L)^-1 in place, by halves: the two 32 x 32 diagonal blocks by forward
+    // substitution (a warp each, a column a lane), then the block below them, -T22 (L21 T11)
     const int o = 32 * warp;
     float u[32];
 #pragma unroll
     for (int t = 0; t < 32; ++t) {
-      float acc[4] = {t == lane ? 1.f : 0.f, 0.f, 0.f, 0.f};
+      float x[4] = {t == lane ? 1.f : 0.f, 0.f, 0.f, 0.f};
       const float* row = &S.a[(o + t) * kPrepLdA + o];
 #pragma unroll
       for (int j = 0; j + 4 <= t; j += 4) {
         const float4 l = *reinterpret_cast<const float4*>(row + j);
-        acc[0] = fmaf(-l.x, u[j], acc[0]);
-        acc[1] = fmaf(-l.y, u[j + 1], acc[1]);
-        acc[2] = fmaf(-l.z, u[j + 2], acc[2]);
-        acc[3] = fmaf(-l.w, u[j + 3], acc[3]);
+        x[0] = fmaf(-l.x, u[j], x[0]);
+        x[1] = fmaf(-l.y, u[j + 1], x[1]);
+        x[2] = fmaf(-l.z, u[j + 2], x[2]);
+        x[3] = fmaf(-l.w, u[j + 3], x[3]);
       }
 #pragma unroll
-      for (int j = t & ~3; j < t; ++j) acc[j & 3] = fmaf(-row[j], u[j], acc[j & 3]);
-      u[t] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+      for (int j = t & ~3; j < t; ++j) x[j & 3] = fmaf(-row[j], u[j], x[j & 3]);
+      u[t] = (x[0] + x[1]) + (x[2] + x[3]);
     }
     __syncwarp();
 #pragma unroll
     for (int t = 0; t < 32; ++t) S.a[(o + t) * kPrepLdA + o + lane] = u[t];
+  } else {
+    // the largest |K|: one row a lane
+    const int t = tid - 64;
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const uint4 x = *reinterpret_cast<const uint4*>(S.k + 8192 * (i >> 3) + tile_byte(t, 8 * (i & 7)));
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        m = fmaxf(m, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (lane == 0) S.kmax[warp - 2] = m;
   }
   __syncthreads();
   {
@@ -480,139 +582,103 @@ __global__ void __launch_bounds__(kPrepThreads) k_delta_prep(DeltaChunkArgs ca) 
     for (int i = 0; i < 4; ++i) S.a[(32 + i0 + i) * kPrepLdA + lane] = -z[i];
   }
   __syncthreads();
+  uint32_t t_lo[8];   // T lo of 16 columns of one row, until its space is free
+  const int tt = tid >> 2, tj = 16 * (tid & 3);
   {
-    // T = Tu diag(beta): 16 columns of one row a thread
-    const int t = tid >> 2, j0 = 16 * (tid & 3);
-    unsigned char* tt = S.tail;
-    const bool zero = t < 32 && j0 >= 32;
+    // T = Tu diag(beta)
+    const bool zero = tt < 32 && tj >= 32;
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-      uint32_t vh[4], vm[4], vl[4];
+      uint32_t vh[4], vm[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int j = j0 + 8 * b + 2 * e;
-        const float x = zero ? 0.f : S.a[t * kPrepLdA + j] * S.beta[j];
-        const float y = zero ? 0.f : S.a[t * kPrepLdA + j + 1] * S.beta[j + 1];
-        cut3_bf16x2(x, y, &vh[e], &vm[e], &vl[e]);
+      for (int e = 0; e < 4; e += 2) {
+        const int j = tj + 8 * b + 2 * e;
+        float4 x = *reinterpret_cast<const float4*>(&S.a[tt * kPrepLdA + j]);
+        const float4 y = *reinterpret_cast<const float4*>(&S.beta[j]);
+        if (zero) x = make_float4(0.f, 0.f, 0.f, 0.f);
+        split3_bf16x2(x.x * y.x, x.y * y.y, &vh[e], &vm[e], &t_lo[4 * b + e]);
+        split3_bf16x2(x.z * y.z, x.w * y.w, &vh[e + 1], &vm[e + 1], &t_lo[4 * b + e + 1]);
       }
-      const uint32_t at = tile_byte(t, j0 + 8 * b);
-      *reinterpret_cast<uint4*>(tt + at) = make_uint4(vh[0], vh[1], vh[2], vh[3]);
-      *reinterpret_cast<uint4*>(tt + 8192 + at) = make_uint4(vm[0], vm[1], vm[2], vm[3]);
-      *reinterpret_cast<uint4*>(tt + 16384 + at) = make_uint4(vl[0], vl[1], vl[2], vl[3]);
+      const uint32_t at = tile_byte(tt, tj + 8 * b);
+      *reinterpret_cast<uint4*>(S.q + at) = make_uint4(vh[0], vh[1], vh[2], vh[3]);
+      *reinterpret_cast<uint4*>(S.q + 8192 + at) = make_uint4(vm[0], vm[1], vm[2], vm[3]);
     }
   }
-  // Q as fp16 with scaled rows: a quarter of a row a thread, in registers until K is done with
-  uint32_t qv[16];
-  {
-    const int t = tid >> 2, d0 = 32 * (tid & 3);
-    uint4 raw[4];
-    float m = 0.f;
+  fence_proxy_async_smem();
+  __syncthreads();
+  if (tid == 128) {
+    bulk_store(rec + kRecT, S.q, 16384);
+    bulk_store_wait();
+  }
+  __syncwarp();
+  // W = (Tu diag(beta e^g)) K: warp = 16 rows x 64 columns of K
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      raw[i] = *reinterpret_cast<const uint4*>(&S.q[t * kPrepLd + d0 + 8 * i]);
-      const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+  for (int i = 0; i < 8; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        m = fmaxf(m, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
-    }
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    float inv;
-    const float sc = row_scale(m, &inv);
+    for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
+  const uint32_t wk = sk + 8192 * (warp >> 2);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+  for (int ks = 0; ks < 4; ++ks) {
+    if (ks <= rb) {
+      uint32_t fh[4], fm[4], fl[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const __half2 x = __floats2half2_rn(__uint_as_float(w[e] << 16) * sc,
-                                            __uint_as_float(w[e] & 0xffff0000u) * sc);
-        qv[4 * i + e] = *reinterpret_cast<const uint32_t*>(&x);
+        const int t = (e & 1) ? tb : ta, j = 16 * ks + 2 * tq + 8 * (e >> 1);
+        const float2 x = *reinterpret_cast<const float2*>(&S.a[t * kPrepLdA + j]);
+        const float2 y = *reinterpret_cast<const float2*>(&S.beg[j]);
+        split3_bf16x2(x.x * y.x, x.y * y.y, &fh[e], &fm[e], &fl[e]);
+      }
+#pragma unroll
+      for (int np = 0; np < 4; ++np) {
+        uint32_t fb[4];
+        ldsm4_t(fb, wk + tile_byte(16 * ks + (lane & 15), 16 * np + 8 * (lane >> 4)));
+        delta_mma(acc[2 * np], fh, fb[0], fb[1]);
+        delta_mma(acc[2 * np + 1], fh, fb[2], fb[3]);
+        delta_mma(acc[2 * np], fm, fb[0], fb[1]);
+        delta_mma(acc[2 * np + 1], fm, fb[2], fb[3]);
+        delta_mma(acc[2 * np], fl, fb[0], fb[1]);
+        delta_mma(acc[2 * np + 1], fl, fb[2], fb[3]);
       }
     }
-    if ((tid & 3) == 0) gate[kGateQ + t] = S.eg[t] * inv;
   }
-  {
-    // W = (Tu diag(beta e^g)) K: warp = 16 rows x 64 columns of K
-    const int d0 = 64 * (warp >> 2);
-    float acc[8][4];
+  float m = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+  for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
-    const __nv_bfloat16* bp = S.k + (lane & 15) * kPrepLd + d0 + 8 * (lane >> 4);
+    for (int e = 0; e < 4; ++e) m = fmaxf(m, fabsf(acc[nt][e]));
 #pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      if (ks <= rb) {
-        uint32_t fh[4], fm[4], fl[4];
+  for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (lane == 0) S.wmax[warp] = m;
+  __syncthreads();   // also: K and Tu have been read, and T hi and mid are on their way
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int t = (e & 1) ? tb : ta, j = 16 * ks + 2 * tq + 8 * (e >> 1);
-          const float2 x = *reinterpret_cast<const float2*>(&S.a[t * kPrepLdA + j]);
-          const float2 w = make_float2(S.beta[j] * S.eg[j], S.beta[j + 1] * S.eg[j + 1]);
-          cut3_bf16x2(x.x * w.x, x.y * w.y, &fh[e], &fm[e], &fl[e]);
-        }
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, S.wmax[i]);
+  float inv_w;
+  const float sw = -row_scale(m, &inv_w);
+  if (tid == 0) {
+    gate[kGateK] = fmaxf(S.kmax[0], S.kmax[1]);
+    gate[kGateW] = inv_w;
+  }
 #pragma unroll
-        for (int np = 0; np < 4; ++np) {
-          uint32_t fb[4];
-          ldsm4_t(fb, smem_u32(bp + 16 * ks * kPrepLd + 16 * np));
-          delta_mma(acc[2 * np], fh, fb[0], fb[1]);
-          delta_mma(acc[2 * np + 1], fh, fb[2], fb[3]);
-          delta_mma(acc[2 * np], fm, fb[0], fb[1]);
-          delta_mma(acc[2 * np + 1], fm, fb[2], fb[3]);
-          delta_mma(acc[2 * np], fl, fb[0], fb[1]);
-          delta_mma(acc[2 * np + 1], fl, fb[2], fb[3]);
-        }
-      }
-    }
-    float ma = 0.f, mb = 0.f;
+  for (int b = 0; b < 2; ++b)
+    *reinterpret_cast<uint4*>(S.q + tile_byte(tt, tj + 8 * b)) =
+        make_uint4(t_lo[4 * b], t_lo[4 * b + 1], t_lo[4 * b + 2], t_lo[4 * b + 3]);
+  unsigned char* w = S.k + 8192 * (warp >> 2);   // on into Tu's space
 #pragma unroll
-    for (int nt = 0; nt < 8; ++nt) {
-      ma = fmaxf(ma, fmaxf(fabsf(acc[nt][0]), fabsf(acc[nt][1])));
-      mb = fmaxf(mb, fmaxf(fabsf(acc[nt][2]), fabsf(acc[nt][3])));
-    }
-#pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-      ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, o));
-      mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, o));
-    }
-    if (tq == 0) {
-      S.wmax[warp >> 2][ta] = ma;
-      S.wmax[warp >> 2][tb] = mb;
-    }
-    __syncthreads();   // also: K, Q and Tu have been read
-    float ia, ib;
-    const float sa = -row_scale(fmaxf(S.wmax[0][ta], S.wmax[1][ta]), &ia);
-    const float sb = -row_scale(fmaxf(S.wmax[0][tb], S.wmax[1][tb]), &ib);
-    if (warp < 4 && tq == 0) {
-      gate[kGateW + ta] = ia;
-      gate[kGateW + tb] = ib;
-    }
-    unsigned char* w = reinterpret_cast<unsigned char*>(S.q) + 8192 * (warp >> 2);
-#pragma unroll
-    for (int nt = 0; nt < 8; ++nt) {
-      uint32_t vh, vl;
-      const int d = 8 * nt + 2 * tq;
-      split_f16x2(sa * acc[nt][0], sa * acc[nt][1], &vh, &vl);
-      *reinterpret_cast<uint32_t*>(w + tile_byte(ta, d)) = vh;
-      *reinterpret_cast<uint32_t*>(w + 16384 + tile_byte(ta, d)) = vl;
-      split_f16x2(sb * acc[nt][2], sb * acc[nt][3], &vh, &vl);
-      *reinterpret_cast<uint32_t*>(w + tile_byte(tb, d)) = vh;
-      *reinterpret_cast<uint32_t*>(w + 16384 + tile_byte(tb, d)) = vl;
-    }
-    const int t = tid >> 2, q4 = tid & 3;   // columns 32 q4 ..: panel q4 / 2
-    unsigned char* qd = reinterpret_cast<unsigned char*>(S.k) + 8192 * (q4 >> 1);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      *reinterpret_cast<uint4*>(qd + tile_byte(t, 32 * (q4 & 1) + 8 * i)) =
-          make_uint4(qv[4 * i], qv[4 * i + 1], qv[4 * i + 2], qv[4 * i + 3]);
+  for (int nt = 0; nt < 8; ++nt) {
+    uint32_t vh, vl;
+    const int d = 8 * nt + 2 * tq;
+    split_f16x2(sw * acc[nt][0], sw * acc[nt][1], &vh, &vl);
+    *reinterpret_cast<uint32_t*>(w + tile_byte(ta, d)) = vh;
+    *reinterpret_cast<uint32_t*>(w + 16384 + tile_byte(ta, d)) = vl;
+    split_f16x2(sw * acc[nt][2], sw * acc[nt][3], &vh, &vl);
+    *reinterpret_cast<uint32_t*>(w + tile_byte(tb, d)) = vh;
+    *reinterpret_cast<uint32_t*>(w + 16384 + tile_byte(tb, d)) = vl;
   }
   fence_proxy_async_smem();
   __syncthreads();
   if (tid == 0) {
-    unsigned char* rec = ca.rec + (r * ca.nheads + blockIdx.y) * static_cast<int64_t>(kRecBytes);
-    bulk_store(rec + kRecW, S.q, kRecT);
-    bulk_store(rec + kRecT, S.tail, kRecQ - kRecT);
-    bulk_store(rec + kRecQ, S.k, kRecGate - kRecQ);
+    bulk_store(rec + kRecW, S.k, 32768);
+    bulk_store(rec + kRecT + 16384, S.q, 8192);
     bulk_store(rec + kRecGate, S.gate, kRecBytes - kRecGate);
     bulk_store_wait();
   }
@@ -628,17 +694,20 @@ __global__ void __launch_bounds__(kPrepThreads) k_delta_prep(DeltaChunkArgs ca) 
 //     D_S [v][d] = U'^T K,  U' = diag(e^(g_C - g)) U,  U = D_T + D_W
 // Two warpgroups hold the fp32 state in registers (a lane has one v, 64 of its d's), form U and
 // U' and then S; a third writes the outputs.  Three warps load, each its own operands, whose
-// space is free again as soon as their last product is done.
+// space is free again as soon as their last product is done.  The chain of a chunk is S -> D_W ->
+// U' -> D_S -> S: S goes over in four parts and U' in two, so that the products of a part run
+// while the next one is converted.  S is scaled before it is known, by a bound on its rows:
+// |S| <= e^(g_C) max|S0| + 64 max|U| max|K|.
 constexpr int kScanThreads = 512;
 constexpr int kScanW = 0;                               // [2] W, K, gates
 constexpr int kScanWBytes = 32768 + 16384 + 1024;
 constexpr int kScanQ = kScanW + 2 * kScanWBytes;        // [2] Q, M
-constexpr int kScanQBytes = 32768;
+constexpr int kScanQBytes = 16384 + 8192;
 constexpr int kScanT = kScanQ + 2 * kScanQBytes;        // T, V
 constexpr int kScanTBytes = 24576 + 16384;
 constexpr int kScanOut = kScanT + kScanTBytes;          // outputs on their way: 4 KB a warp
 constexpr int kScanBars = kScanOut + 16384;
-constexpr int kScanSmemBytes = kScanBars + 4096;
+constexpr int kScanSmemBytes = kScanBars + 5120;
 static_assert(kScanSmemBytes <= 232448, "shared memory per CTA");
 static_assert(kScanWBytes % 1024 == 0 && kScanTBytes % 1024 == 0, "tiles on 1 KB boundaries");
 
@@ -648,22 +717,28 @@ constexpr int kScanWhole = 0, kScanEnds = 1, kScanOutputs = 2;
 
 struct ScanBars {
   uint64_t full_t, empty_t, full_w[2], empty_w[2], full_q[2], empty_q[2];
-  uint64_t s_full, d1, uw_full, u_full, ds, qs, q_free, o, o_free, mma_done;
-  uint64_t rows[4];           // the two warps of 32 rows have their maxima in place
+  uint64_t s_part[4], uw_part[2];   // 16 columns of S, 16 tokens of U', of either half
+  uint64_t d1, u_full, ds, qs, q_free, o, o_free, mma_done;
+  uint64_t rows[4];             // the two warps of 32 rows have their maxima in place
   uint32_t tmem;
   int abort;
-  float scale[2][kGdnDim];    // 1 over the scale of each row of S, by the parity of the chunk
-  float rowmax[2][kGdnDim];   // largest |S| of each half row
+  // by row: 1 over the scales of S and U (by the parity of the chunk); the halves' largest |S|, |U|
+  float scale[2][kGdnDim], uscale[2][kGdnDim];
+  float smax[2][kGdnDim], umax[2][kGdnDim];
 };
-static_assert(sizeof(ScanBars) <= 4096, "barriers");
+static_assert(sizeof(ScanBars) <= 5120, "barriers");
 
+// Keeps the reads of a tcgen05.ld's 16 registers behind tcgen05.wait::ld.
+__device__ __forceinline__ void reg_fence16(uint32_t* r) {
+  asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+               "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+               "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
+}
 __device__ __forceinline__ void tmem_ld16_at(uint32_t taddr, float* f) {
   uint32_t r[16];
   tmem_ld16(taddr, r);
   tmem_wait_ld();
-  asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
-               "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
-               "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
+  reg_fence16(r);
 #pragma unroll
   for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(r[i]);
 }
@@ -716,9 +791,9 @@ __global__ void __launch_bounds__(kScanThreads, 1) k_delta_scan(DeltaChunkArgs c
     }
     mbar_init(&B.full_t, 2);
     mbar_init(&B.empty_t, 1);
-    mbar_init(&B.s_full, 8);
+    for (int i = 0; i < 4; ++i) mbar_init(&B.s_part[i], 8);
+    for (int i = 0; i < 2; ++i) mbar_init(&B.uw_part[i], 8);
     mbar_init(&B.d1, 1);
-    mbar_init(&B.uw_full, 8);
     mbar_init(&B.u_full, 8);
     mbar_init(&B.ds, 1);
     mbar_init(&B.qs, 1);
@@ -739,14 +814,15 @@ __global__ void __launch_bounds__(kScanThreads, 1) k_delta_scan(DeltaChunkArgs c
   tc_fence_after();
   // all 512 columns are this CTA's, so they start at 0: addresses are known to the compiler
   constexpr uint32_t tm = 0;
-  // columns: S hi 64, S lo 64 (U hi 32, U lo 32 once D_W is done), D_S 128, D_T 64, D_W 64 (then
-  // U' mid and lo, each half of the threads in the columns that it has read), D_Q 64, U' hi 32
-  constexpr uint32_t tS = tm, tU = tm + 64, tDS = tm + 128, tDT = tm + 256, tDW = tm + 320,
-                     tDQ = tm + 384, tUw = tm + 448;
+  // columns: S hi 64, S lo 64, D_S 128, D_T 64, D_W 64 (then U' mid and lo, each half of the
+  // threads in the columns that it has read), D_Q 64, U' hi 32, U 32
+  constexpr uint32_t tS = tm, tDS = tm + 128, tDT = tm + 256, tDW = tm + 320, tDQ = tm + 384,
+                     tUw = tm + 448, tU = tm + 480;
   volatile int* abort = &B.abort;
   const DevStatus st = ca.st;
 
   if (warp < 8) {
+    regs_raise<168>();
     // ---- the state: lane = value row v, 64 columns d of it -----------------------------------
     const int half = warp >> 2, v = 32 * (warp & 3) + lane;
     const uint32_t lb = static_cast<uint32_t>(32 * (warp & 3)) << 16;
@@ -769,36 +845,42 @@ __global__ void __launch_bounds__(kScanThreads, 1) k_delta_scan(DeltaChunkArgs c
         if (mode == kScanEnds) reinterpret_cast<float4*>(kept + v * kGdnDim + 64 * half)[i] = x;
       }
     }
-    float inv;   // 1 over the scale of this row
-    auto put_state = [&](int c) -> bool {   // S entering chunk c, as fp16 parts
-      float m = 0.f;
-#pragma unroll
-      for (int i = 0; i < 64; ++i) m = fmaxf(m, fabsf(s[i]));
-      B.rowmax[half][v] = m;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&B.rows[warp & 3]);
-      if (!__all_sync(0xffffffffu, mbar_wait(&B.rows[warp & 3], c & 1, abort, st, 337))) return false;
-      const float sc = row_scale(fmaxf(m, B.rowmax[half ^ 1][v]), &inv);
-      if (half == 0) B.scale[c & 1][v] = inv;
-#pragma unroll
-      for (int i0 = 0; i0 < 64; i0 += 16) {
-        uint32_t vh[8], vl[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          split_f16x2(sc * s[i0 + 2 * i], sc * s[i0 + 2 * i + 1], &vh[i], &vl[i]);
-        tmem_st8(tS + lb + 32 * half + i0 / 2, vh);
-        tmem_st8(tS + lb + 64 + 32 * half + i0 / 2, vl);
-      }
-      return true;
-    };
     auto signal = [&](uint64_t* bar) {
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
     };
-    bool ok = put_state(0);
-    if (ok) signal(&B.s_full);
+    auto joined = [&](int phase) -> bool {   // the maxima of both halves of the rows are in place
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&B.rows[warp & 3]);
+      return __all_sync(0xffffffffu, mbar_wait(&B.rows[warp & 3], phase & 1, abort, st, 337));
+    };
+    auto put_part = [&](int g, float sc) {   // columns 16 g .. of this half, as fp16 parts
+      uint32_t vh[8], vl[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        split_f16x2(sc * s[16 * g + 2 * i], sc * s[16 * g + 2 * i + 1], &vh[i], &vl[i]);
+      tmem_st8(tS + lb + 32 * half + 8 * g, vh);
+      tmem_st8(tS + lb + 64 + 32 * half + 8 * g, vl);
+      signal(&B.s_part[g]);
+    };
+    auto largest = [&]() -> float {
+      float m[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < 64; ++i) m[i & 3] = fmaxf(m[i & 3], fabsf(s[i]));
+      return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+    };
+    float smax = largest();
+    B.smax[half][v] = smax;
+    bool ok = joined(0);
+    float inv;   // 1 over the scale of this row
+    if (ok) {
+      const float sc = row_scale(fmaxf(smax, B.smax[half ^ 1][v]), &inv);
+      if (half == 0) B.scale[0][v] = inv;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) put_part(g, sc);
+    }
     for (int c = 0; ok && c < nc; ++c) {
       const int sg = c & 1;
       const float* gate = reinterpret_cast<const float*>(smem + kScanW + sg * kScanWBytes + 49152);
@@ -806,69 +888,72 @@ __global__ void __launch_bounds__(kScanThreads, 1) k_delta_scan(DeltaChunkArgs c
            mbar_wait(&B.d1, c & 1, abort, st, 331);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
+      const float winv = inv * gate[kGateW];
       float u[32];
 #pragma unroll
-      for (int i0 = 0; i0 < 32; i0 += 16) {
-        float x[16], y[16];
-        if (trans) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) x[i] = 0.f;
-        } else {
-          tmem_ld16_at(tDT + lb + 32 * half + i0, x);
-        }
-        tmem_ld16_at(tDW + lb + 32 * half + i0, y);
+      for (int g = 0; g < 2; ++g) {
+        uint32_t x[16], y[16];
+        if (!trans) tmem_ld16(tDT + lb + 32 * half + 16 * g, x);
+        tmem_ld16(tDW + lb + 32 * half + 16 * g, y);
+        tmem_wait_ld();
+        reg_fence16(x);
+        reg_fence16(y);
         uint32_t vh[8], vm[8], vl[8];
-        const float4* wi = reinterpret_cast<const float4*>(gate + kGateW + 32 * half + i0);
-        const float4* wk = reinterpret_cast<const float4*>(gate + kGateU + 32 * half + i0);
+        const float4* wk = reinterpret_cast<const float4*>(gate + kGateU + 32 * half + 16 * g);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float4 a4 = wi[i], b4 = wk[i];
-          u[i0 + 4 * i] = fmaf(inv * a4.x, y[4 * i], x[4 * i]);
-          u[i0 + 4 * i + 1] = fmaf(inv * a4.y, y[4 * i + 1], x[4 * i + 1]);
-          u[i0 + 4 * i + 2] = fmaf(inv * a4.z, y[4 * i + 2], x[4 * i + 2]);
-          u[i0 + 4 * i + 3] = fmaf(inv * a4.w, y[4 * i + 3], x[4 * i + 3]);
-          cut3_bf16x2(b4.x * u[i0 + 4 * i], b4.y * u[i0 + 4 * i + 1], &vh[2 * i], &vm[2 * i], &vl[2 * i]);
-          cut3_bf16x2(b4.z * u[i0 + 4 * i + 2], b4.w * u[i0 + 4 * i + 3], &vh[2 * i + 1],
-                      &vm[2 * i + 1], &vl[2 * i + 1]);
+          const float4 w = wk[i];
+          float* p = u + 16 * g + 4 * i;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            p[e] = fmaf(winv, __uint_as_float(y[4 * i + e]), trans ? 0.f : __uint_as_float(x[4 * i + e]));
+          split3_bf16x2(w.x * p[0], w.y * p[1], &vh[2 * i], &vm[2 * i], &vl[2 * i]);
+          split3_bf16x2(w.z * p[2], w.w * p[3], &vh[2 * i + 1], &vm[2 * i + 1], &vl[2 * i + 1]);
         }
-        // the first 16 tokens' mid and lo take the columns of D_W that were just read
-        tmem_st8(tUw + lb + 16 * half + i0 / 2, vh);
-        tmem_st8(tDW + lb + 32 * half + i0, vm);
-        tmem_st8(tDW + lb + 32 * half + i0 + 8, vl);
+        // mid and lo take the columns of D_W that were just read
+        tmem_st8(tUw + lb + 16 * half + 8 * g, vh);
+        tmem_st8(tDW + lb + 32 * half + 16 * g, vm);
+        tmem_st8(tDW + lb + 32 * half + 16 * g + 8, vl);
+        signal(&B.uw_part[g]);
       }
-      signal(&B.uw_full);
+      float umax = 0.f;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) umax = fmaxf(umax, fabsf(u[i]));
+      B.smax[half][v] = smax;
+      B.umax[half][v] = umax;
+      const float gc = gate[kGateC], kmax = gate[kGateK];
+      ok = joined(c + 1);
+      if (!ok) break;
+      if (lane == 0) mbar_arrive(&B.empty_w[sg]);
+      umax = fmaxf(umax, B.umax[half ^ 1][v]);
+      const float sc = row_scale(fmaf(gc, fmaxf(smax, B.smax[half ^ 1][v]), 64.f * kmax * umax), &inv);
       if (outputs) {
+        float iu;
+        const float su = row_scale(umax, &iu);
+        uint32_t w[16];
 #pragma unroll
-        for (int i0 = 0; i0 < 32; i0 += 16) {
-          uint32_t vh[8], vl[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) cut_bf16x2(u[i0 + 2 * i], u[i0 + 2 * i + 1], &vh[i], &vl[i]);
-          tmem_st8(tU + lb + 16 * half + i0 / 2, vh);
-          tmem_st8(tU + lb + 32 + 16 * half + i0 / 2, vl);
-        }
+        for (int i = 0; i < 16; ++i) w[i] = pack_f16x2(su * u[2 * i], su * u[2 * i + 1]);
+        if (half == 0) B.uscale[c & 1][v] = iu;
+        tmem_st16(tU + lb + 16 * half, w);
         signal(&B.u_full);
       }
-      const float gc = gate[kGateC];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&B.empty_w[sg]);
       ok = mbar_wait(&B.ds, c & 1, abort, st, 332);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
+      const bool more = c + 1 < nc;
+      if (more && half == 0) B.scale[(c + 1) & 1][v] = inv;
+      uint32_t x[2][16];
+      tmem_ld16(tDS + lb + 64 * half, x[0]);
 #pragma unroll
-      for (int i0 = 0; i0 < 64; i0 += 16) {
-        float x[16];
-        tmem_ld16_at(tDS + lb + 64 * half + i0, x);
+      for (int g = 0; g < 4; ++g) {
+        tmem_wait_ld();
+        reg_fence16(x[g & 1]);
+        if (g < 3) tmem_ld16(tDS + lb + 64 * half + 16 * (g + 1), x[(g + 1) & 1]);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) s[i0 + i] = fmaf(gc, s[i0 + i], x[i]);
+        for (int i = 0; i < 16; ++i) s[16 * g + i] = fmaf(gc, s[16 * g + i], __uint_as_float(x[g & 1][i]));
+        if (more) put_part(g, sc);
       }
-      if (c + 1 < nc) {
-        // U, which takes the place of S lo, is done with once the outputs are
-        ok = !outputs || mbar_wait(&B.o, c & 1, abort, st, 336);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        tc_fence_after();
-        ok = put_state(c + 1);
-        if (ok) signal(&B.s_full);
-      }
+      smax = largest();
     }
     // in the outputs pass the joined states hold what the inner segments would write
     if (__all_sync(0xffffffffu, ok) && (mode == kScanEnds || last)) {
@@ -878,6 +963,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) k_delta_scan(DeltaChunkArgs c
         p[i] = make_float4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]);
     }
   } else if (warp < 12) {
+    regs_lower<112>();
     // ---- outputs: lane = value v, 64 tokens --------------------------------------------------
     if (outputs) {
       const int v = 32 * (warp - 8) + lane;
@@ -891,6 +977,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) k_delta_scan(DeltaChunkArgs c
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
         const float inv = B.scale[c & 1][v];
+        const float4* gm = eg + (kGateM - kGateQ) / 4;
         float y[64];
 #pragma unroll
         for (int i0 = 0; i0 < 64; i0 += 16) {
@@ -906,27 +993,30 @@ __global__ void __launch_bounds__(kScanThreads, 1) k_delta_scan(DeltaChunkArgs c
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&B.q_free);
-          mbar_arrive(&B.empty_w[sg]);
-        }
+        if (lane == 0) mbar_arrive(&B.q_free);
         ok = mbar_wait(&B.o, c & 1, abort, st, 335);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
+        const float iu = B.uscale[c & 1][v];
 #pragma unroll
         for (int i0 = 0; i0 < 64; i0 += 16) {
           float x[16];
           tmem_ld16_at(tDQ + lb + i0, x);
 #pragma unroll
           for (int i = 0; i < 16; i += 2) {
-            const uint32_t w = pack_bf16x2(y[i0 + i] + x[i], y[i0 + i + 1] + x[i + 1]);
+            const float2 e = *reinterpret_cast<const float2*>(reinterpret_cast<const float*>(gm) + i0 + i);
+            const uint32_t w = pack_bf16x2(fmaf(iu * e.x, x[i], y[i0 + i]),
+                                           fmaf(iu * e.y, x[i + 1], y[i0 + i + 1]));
             *reinterpret_cast<uint16_t*>(mine + 64 * (i0 + i) + 2 * lane) = static_cast<uint16_t>(w);
             *reinterpret_cast<uint16_t*>(mine + 64 * (i0 + i + 1) + 2 * lane) = static_cast<uint16_t>(w >> 16);
           }
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&B.o_free);
+        if (lane == 0) {
+          mbar_arrive(&B.o_free);
+          mbar_arrive(&B.empty_w[sg]);
+        }
         const int64_t left = ntok - static_cast<int64_t>(c) * kGdnChunk;
         const int n = static_cast<int>(left < kGdnChunk ? left : kGdnChunk);
         const int64_t step = static_cast<int64_t>(a.heads) * kGdnDim;
@@ -943,10 +1033,11 @@ __global__ void __launch_bounds__(kScanThreads, 1) k_delta_scan(DeltaChunkArgs c
         __syncwarp();   // the next chunk overwrites `mine`
       }
     }
-  } else if (warp == 12) {
+  } else {
+    regs_lower<64>();
+    if (warp == 12) {
     // ---- products: the whole warp walks the loop, one elected lane issues ----------------------
     constexpr uint32_t kIdTV = idesc_bf16_f32(128, 64, 1, 0);   // A = V, tokens along its rows
-    constexpr uint32_t kIdN64 = idesc_bf16_f32(128, 64, 0, 0);
     constexpr uint32_t kIdF16 = idesc_f16_f32(128, 64, 0, 0);
     constexpr uint32_t kIdDS = idesc_bf16_f32(128, 128, 0, 1);  // B = K, tokens along its rows
     // descriptors; a step along a tile adds its bytes / 16
@@ -973,20 +1064,24 @@ __global__ void __launch_bounds__(kScanThreads, 1) k_delta_scan(DeltaChunkArgs c
       const uint32_t ph = (c >> 1) & 1;
       const uint64_t sw = (kScanW + sg * kScanWBytes) >> 4, sq = (kScanQ + sg * kScanQBytes) >> 4;
       if (!mbar_wait(&B.full_w[sg], ph, abort, st, 342)) break;
-      if (!mbar_wait(&B.s_full, c & 1, abort, st, 341)) break;
-      tc_fence_after();
-      if (elect_one()) {
-        // D_W = -S0 W^T: (hi, hi), (lo, hi), (hi, lo)
+      // D_W = -S0 W^T: (hi, hi), (lo, hi), (hi, lo) of 16 columns of each half at a time
+      for (int g = 0; g < 4 && ok; ++g) {
+        ok = mbar_wait(&B.s_part[g], c & 1, abort, st, 341);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
-        for (int p = 0; p < 3; ++p)
+          for (int p = 0; p < 3; ++p)
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            umma_ts(tDW, tS + (p == 1 ? 64 : 0) + 8 * k,
-                    dk + sw + (((p == 2 ? 16384 : 0) + 8192 * (k >> 2) + 32 * (k & 3)) >> 4), kIdF16,
-                    p + k > 0 ? 1u : 0u);
-        umma_commit(&B.d1);   // covers D_T too
+            for (int kh = 0; kh < 2; ++kh)
+              umma_ts(tDW, tS + (p == 1 ? 64 : 0) + 32 * kh + 8 * g,
+                      dk + sw + (((p == 2 ? 16384 : 0) + 8192 * kh + 32 * g) >> 4), kIdF16,
+                      (g > 0 || p + kh > 0) ? 1u : 0u);
+          if (g == 3) umma_commit(&B.d1);   // covers D_T too
+        }
+        __syncwarp();
       }
-      __syncwarp();
+      if (!ok) break;
       if (outputs) {
         if (!mbar_wait(&B.full_q[sg], ph, abort, st, 343)) break;
         if (c > 0 && !mbar_wait(&B.o_free, (c - 1) & 1, abort, st, 344)) break;
@@ -1000,33 +1095,38 @@ __global__ void __launch_bounds__(kScanThreads, 1) k_delta_scan(DeltaChunkArgs c
         }
         __syncwarp();
       }
-      if (!mbar_wait(&B.uw_full, c & 1, abort, st, 345)) break;
-      tc_fence_after();
-      if (elect_one()) {
-        // D_S = U'^T K: hi, mid, lo; a step is 16 tokens, mid and lo at 16-column strides
+      // D_S = U'^T K: hi, mid, lo of 16 tokens of each half at a time (mid and lo at 16-column
+      // strides)
+      for (int g = 0; g < 2 && ok; ++g) {
+        ok = mbar_wait(&B.uw_part[g], c & 1, abort, st, 345);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
-        for (int p = 0; p < 3; ++p)
+          for (int p = 0; p < 3; ++p)
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            umma_ts(tDS, p == 0 ? tUw + 8 * k : tDW + 16 * k + 8 * (p - 1),
-                    dm + sw + ((32768 + 2048 * k) >> 4), kIdDS, p + k > 0 ? 1u : 0u);
-        umma_commit(&B.ds);
-        umma_commit(&B.empty_w[sg]);
+            for (int kh = 0; kh < 2; ++kh) {
+              const int k = g + 2 * kh;
+              umma_ts(tDS, p == 0 ? tUw + 8 * k : tDW + 16 * k + 8 * (p - 1),
+                      dm + sw + ((32768 + 2048 * k) >> 4), kIdDS, (g > 0 || p + kh > 0) ? 1u : 0u);
+            }
+          if (g == 1) {
+            umma_commit(&B.ds);
+            umma_commit(&B.empty_w[sg]);
+          }
+        }
+        __syncwarp();
       }
-      __syncwarp();
+      if (!ok) break;
       if (outputs) {
         if (!mbar_wait(&B.q_free, c & 1, abort, st, 346)) break;
         if (!mbar_wait(&B.u_full, c & 1, abort, st, 348)) break;
         tc_fence_after();
         if (elect_one()) {
-          // D_Q = U^T M^T: (hi, hi), (lo, hi), (hi, lo)
+          // D_Q = U^T M^T
 #pragma unroll
-          for (int p = 0; p < 3; ++p)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              umma_ts(tDQ, tU + (p == 1 ? 32 : 0) + 8 * k,
-                      dk + sq + ((16384 + (p == 2 ? 8192 : 0) + 32 * k) >> 4), kIdN64,
-                      p + k > 0 ? 1u : 0u);
+          for (int k = 0; k < 4; ++k)
+            umma_ts(tDQ, tU + 8 * k, dk + sq + ((16384 + 32 * k) >> 4), kIdF16, k > 0 ? 1u : 0u);
           umma_commit(&B.o);
           umma_commit(&B.empty_q[sg]);
         }
@@ -1062,9 +1162,9 @@ __global__ void __launch_bounds__(kScanThreads, 1) k_delta_scan(DeltaChunkArgs c
           mbar_arrive_expect_tx(&full[sg], 24576);
           bulk_load(stage, rec + kRecT, 24576, &full[sg]);
         } else {
-          mbar_arrive_expect_tx(&full[sg], 32768);
+          mbar_arrive_expect_tx(&full[sg], 24576);
           bulk_load(stage, rec + kRecQ, 16384, &full[sg]);
-          bulk_load(stage + 16384, rec + kRecM, 16384, &full[sg]);
+          bulk_load(stage + 16384, rec + kRecM, 8192, &full[sg]);
         }
       }
       __syncwarp();
@@ -1089,6 +1189,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) k_delta_scan(DeltaChunkArgs c
     if (lane == 0 && *abort)   // no copy may land after the CTA is gone
       for (int c = issued > stages ? issued - stages : 0; c < issued; ++c)
         mbar_drain(&full[c % stages], (c / stages) & 1);
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -1100,12 +1201,16 @@ __global__ void __launch_bounds__(kScanThreads, 1) k_delta_scan(DeltaChunkArgs c
 }
 
 // Joins the segments of a sequence: entered with E (the state at its start), a segment ends with
-// E P + S.  Rows of the state are independent: a CTA takes 8 of them through the segments in
-// order, a thread one column.
-constexpr int kJoinRows = 8;
+// E P + S.  Rows of the state are independent: a CTA takes four of them through the segments in
+// order, a thread one column.  Bound by the latency of a step (512 multiply-adds a thread, P from
+// shared memory); the P of the next two segments are on their way meanwhile.
+constexpr int kJoinRows = 4;
+constexpr int kJoinStages = 3;
+constexpr int kJoinSmemBytes = kJoinStages * kGdnDim * kGdnDim * 4;
 
 // grid (heads of the pass, sequences, 128 / kJoinRows), 128 threads
 __global__ void __launch_bounds__(kGdnDim) k_delta_join(DeltaChunkArgs ca) {
+  extern __shared__ __align__(128) float join_p[];   // [stages][128][128]
   __shared__ __align__(16) float e[kJoinRows][kGdnDim];
   const DeltaArgs& a = ca.d;
   const int row = blockIdx.y, hl = blockIdx.x, d = threadIdx.x, v0 = blockIdx.z * kJoinRows;
@@ -1117,21 +1222,33 @@ __global__ void __launch_bounds__(kGdnDim) k_delta_join(DeltaChunkArgs ca) {
   const int64_t tile = static_cast<int64_t>(kGdnDim) * kGdnDim, stride = ca.nheads * tile;
   const int64_t at = ((delta_first_record(begin, row) / ca.seg_chunks + row) * ca.nheads + hl) * tile;
   float* s = ca.seg_state + at + v0 * kGdnDim + d;
-  const float* p = ca.seg_trans + at + d;
+  const float* p = ca.seg_trans + at;
+  auto fetch = [&](int64_t g) {   // segment g's transition (one group a call, empty past the end)
+    if (g + 1 < segs) {
+      const uint32_t to = smem_u32(join_p + (g % kJoinStages) * tile);
+      for (int i = d; i < kGdnDim * kGdnDim / 4; i += kGdnDim)
+        cp_async16(to + 16 * i, p + g * stride + 4 * i, true);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  fetch(1);
+  fetch(2);
 #pragma unroll
   for (int i = 0; i < kJoinRows; ++i) e[i][d] = s[i * kGdnDim];
   for (int64_t g = 1; g + 1 < segs; ++g) {
     s += stride;
-    p += stride;
     float acc[kJoinRows];
 #pragma unroll
     for (int i = 0; i < kJoinRows; ++i) acc[i] = s[i * kGdnDim];
-    __syncthreads();
-#pragma unroll 4
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    __syncthreads();   // this segment's P and E are in place, the last one's are done with
+    fetch(g + 2);
+    const float* pg = join_p + (g % kJoinStages) * tile + d;
+#pragma unroll 8
     for (int k = 0; k < kGdnDim; k += 4) {
       float x[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] = p[(k + j) * kGdnDim];
+      for (int j = 0; j < 4; ++j) x[j] = pg[(k + j) * kGdnDim];
 #pragma unroll
       for (int i = 0; i < kJoinRows; ++i) {
         const float4 y = *reinterpret_cast<const float4*>(&e[i][k]);

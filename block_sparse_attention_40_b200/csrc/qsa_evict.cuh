@@ -200,14 +200,19 @@ __global__ void __launch_bounds__(kWtThreads) k_block_weights(WeightArgs a) {
 }
 
 // ---------------------------------------------------------------------------------------
-// Which blocks stay.  One CTA per sequence: a radix select (digits of 11, 11 and 10 bits, high
-// to low, histograms in shared memory) finds the key of the last block that stays and how many
-// blocks of exactly that key stay, then one ordered pass writes the kept blocks in ascending
-// order.  A weight's key orders as the weight does; NaN counts below every number and -0 as 0.
+// Which blocks stay.  A cluster of CTAs per sequence, each with a contiguous part of its blocks:
+// a radix select (digits of 11, 11 and 10 bits, high to low; histograms in shared memory, summed
+// over the cluster through distributed shared memory) finds the key of the last block that stays
+// and how many blocks of exactly that key stay, then one ordered pass writes the kept blocks in
+// ascending order.  A weight's key orders as the weight does; NaN counts below every number and
+// -0 as 0.  Bound by latency: a row of 262,143 weights is 1 MB, read four times from L2.
 constexpr int kEvThreads = 1024;
 constexpr int kEvBins = 2048;
+constexpr int kEvMaxCluster = 16;
+constexpr int kMvPlaces = 16;   // places of a tile of the move
+constexpr int kEvBatch = 4;     // consecutive weights of a thread
 
-// What the select leaves for the move, per sequence (a CTA's worth of 32-bit words).
+// What the select leaves for the move, per sequence.
 struct EvictMeta {
   int32_t count;   // blocks to place, the incomplete last one included; 0: nothing moves
   int32_t first;   // first place whose block comes from elsewhere
@@ -224,11 +229,14 @@ struct EvictArgs {
   int32_t* kept;         // [B][keep] or null
   int32_t* src;          // [B][keep + 1] workspace: place j takes block src[j]
   EvictMeta* meta;       // [B] workspace
+  int32_t tiles;         // tiles of kMvPlaces places per sequence
+  int32_t* loaded;       // [B][tiles] workspace: the tile's blocks have been read
+  int32_t* before;       // [B][tiles + 1] workspace: kept blocks below the tile's first place
+  int32_t* ticket;       // [1] workspace
   uint4* k_blocks;       // pools, 64 units of 16 bytes a block (K, V), 8 (kbar)
   uint4* v_blocks;
   uint4* kbar;
   Paging pg;
-  int32_t parts;         // column parts of a block that move independently
   DevStatus st;
 };
 
@@ -237,32 +245,82 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return float_key(w + 0.f);
 }
 
-__global__ void __launch_bounds__(kEvThreads) k_evict_select(EvictArgs a) {
-  __shared__ uint32_t hist[kEvBins];
+// Runs f(first index, keys, how many are in range) over i0 .. i1-1, kEvBatch consecutive weights
+// a thread, all threads of the CTA together; the next batch is on its way meanwhile.
+template <typename F>
+__device__ __forceinline__ void ev_scan(const float* mass, int i0, int i1, F&& f) {
+  float w[2][kEvBatch];
+  auto fetch = [&](int base, float* x) {
+    const int i = base + kEvBatch * static_cast<int>(threadIdx.x);
+#pragma unroll
+    for (int b = 0; b < kEvBatch; ++b) x[b] = i + b < i1 ? mass[i + b] : 0.f;
+  };
+  fetch(i0, w[0]);
+  for (int base = i0; base < i1; base += kEvThreads * kEvBatch) {
+    fetch(base + kEvThreads * kEvBatch, w[1]);
+    const int i = base + kEvBatch * static_cast<int>(threadIdx.x);
+    uint32_t key[kEvBatch];
+#pragma unroll
+    for (int b = 0; b < kEvBatch; ++b) key[b] = weight_key(w[0][b]);
+    f(i, key, i1 - i);
+#pragma unroll
+    for (int b = 0; b < kEvBatch; ++b) w[0][b] = w[1][b];
+  }
+}
+
+// Sum over the warps before this one of a value per warp, and over all 32 (in *total).
+__device__ __forceinline__ uint32_t ev_warps_before(const uint32_t* warp_sum, int warp, int lane,
+                                                    uint32_t* total) {
+  uint32_t x = warp_sum[lane];
+  const uint32_t own = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  *total = __shfl_sync(0xffffffffu, x, 31);
+  return __shfl_sync(0xffffffffu, x - own, warp);
+}
+
+// grid (C, B), clusters of (C, 1, 1), C a power of two
+__global__ void __launch_bounds__(kEvThreads, 1) k_evict_select(EvictArgs a) {
+  namespace cg = cooperative_groups;
+  cg::cluster_group cl = cg::this_cluster();
+  __shared__ uint32_t hist[kEvBins];   // this CTA's counts
+  __shared__ uint32_t all[kEvBins];    // the cluster's (every CTA sums a slice for all)
   __shared__ uint32_t warp_sum[32];
-  __shared__ uint32_t sh_prefix, sh_need;
+  __shared__ uint32_t sh_prefix, sh_need, sh_gt, sh_eq;
   __shared__ int sh_first;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, b = blockIdx.x;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, b = blockIdx.y;
+  const int C = gridDim.x, rank = blockIdx.x;
   const int len = a.len[b];
   const int nb = len / kBlock, tail = len % kBlock;
   const float* mass = a.mass + static_cast<int64_t>(b) * a.cap_blocks;
   int32_t* src = a.src + static_cast<int64_t>(b) * (a.keep + 1);
+  int32_t* before = a.before + static_cast<int64_t>(b) * (a.tiles + 1);
   int32_t* kept = a.kept != nullptr ? a.kept + static_cast<int64_t>(b) * a.keep : nullptr;
+  const int gtid = rank * kEvThreads + tid, gthreads = C * kEvThreads;
+  for (int i = gtid; i < a.tiles; i += gthreads) a.loaded[static_cast<int64_t>(b) * a.tiles + i] = 0;
+  if (gtid == 0) before[a.tiles] = a.keep + 1;   // where the sequence ends below
+  if (b == 0 && gtid == 0) *a.ticket = 0;
   if (len < 0 || nb > a.cap_blocks || nb <= a.keep) {   // nothing to cut (or a length out of range)
-    if (tid == 0) {
+    if (gtid == 0) {
       if (len < 0 || nb > a.cap_blocks) report_error(a.st, kErrDevice, 310);
       a.meta[b] = EvictMeta{0, 0, 0, 0};
     }
     if (kept != nullptr)
-      for (int j = tid; j < a.keep; j += kEvThreads) kept[j] = j < nb ? j : -1;
-    return;
+      for (int j = gtid; j < a.keep; j += gthreads) kept[j] = j < nb ? j : -1;
+    return;   // the whole cluster
   }
   const int lo = a.sinks, hi = nb - a.recent;            // candidates lo .. hi-1
   const uint32_t want = static_cast<uint32_t>(a.keep - a.sinks - a.recent);
+  const int per = (hi - lo + C - 1) / C;
+  const int i0 = min(hi, lo + rank * per), i1 = min(hi, i0 + per);   // this CTA's
   // key of the last candidate that stays (prefix) and how many of that key stay (need)
   if (tid == 0) {
     sh_prefix = 0u;
     sh_need = want;
+    sh_first = 0x7fffffff;   // becomes the first block that goes
   }
   const int shift[3] = {21, 10, 0}, bits[3] = {11, 11, 10};
   for (int d = 0; d < 3 && want > 0; ++d) {
@@ -270,21 +328,45 @@ __global__ void __launch_bounds__(kEvThreads) k_evict_select(EvictArgs a) {
     __syncthreads();
     const uint32_t prefix = sh_prefix, need = sh_need;
     const uint32_t bins = 1u << bits[d];
-    for (int i0 = lo; i0 < hi; i0 += kEvThreads) {
-      const int i = i0 + tid;
-      uint32_t bin = 0xffffffffu;
-      if (i < hi) {
-        const uint32_t key = weight_key(mass[i]);
-        if (d == 0 || (key >> (shift[d] + bits[d])) == prefix) bin = (key >> shift[d]) & (bins - 1);
+    uint32_t zeros = 0;   // blocks that were never attended to: counted apart, not one by one
+    const uint32_t zero_key = weight_key(0.f);
+    ev_scan(mass, i0, i1, [&](int, const uint32_t* key, int n) {
+#pragma unroll
+      for (int j = 0; j < kEvBatch; ++j) {
+        const bool on = j < n && (d == 0 || (key[j] >> (shift[d] + bits[d])) == prefix);
+        const uint32_t bin = (key[j] >> shift[d]) & (bins - 1);
+        // a warp of one bin would queue up: one lane adds for all
+        const uint32_t first_bin = __shfl_sync(0xffffffffu, bin, 0);
+        const bool alone = __all_sync(0xffffffffu, on && bin == first_bin);
+        if (alone) {
+          if (lane == 0) atomicAdd(&hist[bin], 32u);
+        } else if (on) {
+          if (key[j] == zero_key) ++zeros;
+          else atomicAdd(&hist[bin], 1u);
+        }
       }
-      // equal bins of a warp (runs of zero weight) count as one addition
-      const uint32_t same = __match_any_sync(0xffffffffu, bin);
-      if (bin != 0xffffffffu && lane == __ffs(same) - 1) atomicAdd(&hist[bin], __popc(same));
+    });
+    zeros = __reduce_add_sync(0xffffffffu, zeros);
+    if (lane == 0 && zeros > 0) atomicAdd(&hist[(zero_key >> shift[d]) & (bins - 1)], zeros);
+    const uint32_t* counts = hist;
+    if (C > 1) {
+      counts = all;
+      cl.sync();
+      // a slice of the bins: the cluster's sum, to every CTA
+      const int slice = kEvBins / C;
+      if (tid < slice) {
+        const int bin = rank * slice + tid;
+        uint32_t x = 0;
+        for (int c = 0; c < C; ++c) x += *cl.map_shared_rank(&hist[bin], c);
+        for (int c = 0; c < C; ++c) *cl.map_shared_rank(&all[bin], c) = x;
+      }
+      cl.sync();
+    } else {
+      __syncthreads();
     }
-    __syncthreads();
     // suffix counts, two bins a thread from the top: thread t has bins bins-1-2t, bins-2-2t
     const int b1 = static_cast<int>(bins) - 1 - 2 * tid, b0 = b1 - 1;
-    const uint32_t h1 = b1 >= 0 ? hist[b1] : 0u, h0 = b0 >= 0 ? hist[b0] : 0u;
+    const uint32_t h1 = b1 >= 0 ? counts[b1] : 0u, h0 = b0 >= 0 ? counts[b0] : 0u;
     uint32_t incl = h1 + h0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -293,8 +375,8 @@ __global__ void __launch_bounds__(kEvThreads) k_evict_select(EvictArgs a) {
     }
     if (lane == 31) warp_sum[warp] = incl;
     __syncthreads();
-    uint32_t base = 0;
-    for (int w = 0; w < warp; ++w) base += warp_sum[w];
+    uint32_t total;
+    const uint32_t base = ev_warps_before(warp_sum, warp, lane, &total);
     const uint32_t above = base + incl - h1 - h0;   // candidates in higher bins
     if (b1 >= 0 && above < need && above + h1 >= need) {
       sh_prefix = (prefix << bits[d]) | static_cast<uint32_t>(b1);
@@ -307,153 +389,218 @@ __global__ void __launch_bounds__(kEvThreads) k_evict_select(EvictArgs a) {
   }
   __syncthreads();
   const uint32_t last = sh_prefix, ties = sh_need;
-  // ordered pass: a block before which m larger and e equal candidates stand takes place
-  // sinks + m + min(e, ties)
+  // larger and equal candidates in the parts before this one
   uint32_t done_gt = 0, done_eq = 0;
-  if (tid == 0) sh_first = want > 0 ? hi : lo;   // becomes the first block that goes
-  __syncthreads();
-  for (int j = tid; j < a.sinks; j += kEvThreads) {
+  if (want > 0) {
+    if (C > 1) {
+      uint32_t gt = 0, eq = 0;
+      ev_scan(mass, i0, i1, [&](int, const uint32_t* key, int n) {
+#pragma unroll
+        for (int j = 0; j < kEvBatch; ++j) {
+          gt += j < n && key[j] > last;
+          eq += j < n && key[j] == last;
+        }
+      });
+      if (tid == 0) sh_gt = sh_eq = 0u;
+      __syncthreads();
+      gt = __reduce_add_sync(0xffffffffu, gt);
+      eq = __reduce_add_sync(0xffffffffu, eq);
+      if (lane == 0) {
+        atomicAdd(&sh_gt, gt);
+        atomicAdd(&sh_eq, eq);
+      }
+      cl.sync();
+      for (int c = 0; c < rank; ++c) {
+        done_gt += *cl.map_shared_rank(&sh_gt, c);
+        done_eq += *cl.map_shared_rank(&sh_eq, c);
+      }
+    }
+    // ordered pass: a block before which m larger and e equal candidates stand takes place
+    // sinks + m + min(e, ties)
+    ev_scan(mass, i0, i1, [&](int i, const uint32_t* key, int n) {
+      // counts of both in one 32-bit scan (at most 4,096 of each)
+      uint32_t own = 0;
+#pragma unroll
+      for (int j = 0; j < kEvBatch; ++j)
+        if (j < n) own += key[j] > last ? 0x10000u : key[j] == last ? 1u : 0u;
+      uint32_t incl = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      if (lane == 31) warp_sum[warp] = incl;
+      __syncthreads();
+      uint32_t total;
+      const uint32_t ex = ev_warps_before(warp_sum, warp, lane, &total) + incl - own;
+      uint32_t m = done_gt + (ex >> 16), e = done_eq + (ex & 0xffffu);
+#pragma unroll
+      for (int j = 0; j < kEvBatch; ++j) {
+        if (j >= n) break;
+        const int at = i + j;
+        const uint32_t below = m + min(e, ties);   // kept candidates before this one
+        if (at % kMvPlaces == 0 && at / kMvPlaces <= a.tiles)
+          before[at / kMvPlaces] = lo + static_cast<int>(below);
+        const bool gt = key[j] > last, eq = key[j] == last;
+        if (gt || (eq && e < ties)) {
+          const int place = lo + static_cast<int>(below);
+          src[place] = at;
+          if (kept != nullptr) kept[place] = at;
+        } else if (below == static_cast<uint32_t>(at - lo)) {
+          sh_first = at;   // all before it stay: at most one block finds that
+        }
+        m += gt;
+        e += eq;
+      }
+      done_gt += total >> 16;
+      done_eq += total & 0xffffu;
+      __syncthreads();
+    });
+  } else {
+    if (gtid == 0) sh_first = lo;
+    for (int i = i0 + tid; i < i1; i += kEvThreads)
+      if (i % kMvPlaces == 0 && i / kMvPlaces <= a.tiles) before[i / kMvPlaces] = lo;
+  }
+  for (int j = gtid; j < a.sinks; j += gthreads) {
     src[j] = j;
+    if (j % kMvPlaces == 0) before[j / kMvPlaces] = j;
     if (kept != nullptr) kept[j] = j;
   }
-  for (int i0 = lo; i0 < hi && want > 0; i0 += kEvThreads) {
-    const int i = i0 + tid;
-    uint32_t gt = 0, eq = 0;
-    if (i < hi) {
-      const uint32_t key = weight_key(mass[i]);
-      gt = key > last;
-      eq = key == last;
-    }
-    // counts of both in one 32-bit scan (at most 1,024 of each)
-    uint32_t incl = gt << 16 | eq;
-    const uint32_t own = incl;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    if (lane == 31) warp_sum[warp] = incl;
-    __syncthreads();
-    uint32_t base = 0, total = 0;
-    for (int w = 0; w < 32; ++w) {
-      if (w == warp) base = total;
-      total += warp_sum[w];
-    }
-    const uint32_t ex = base + incl - own;
-    const uint32_t m = done_gt + (ex >> 16), e = done_eq + (ex & 0xffffu);
-    if (gt || (eq && e < ties)) {
-      const int place = lo + static_cast<int>(m + min(e, ties));
-      src[place] = i;
-      if (kept != nullptr) kept[place] = i;
-    } else if (i < hi && done_gt + min(done_eq, ties) == static_cast<uint32_t>(i0 - lo)) {
-      atomicMin(&sh_first, i);   // no block before this pass has gone
-    }
-    done_gt += total >> 16;
-    done_eq += total & 0xffffu;
-    __syncthreads();
-  }
-  for (int j = tid; j < a.recent; j += kEvThreads) {
+  // (the last blocks, and the incomplete one behind them)
+  for (int j = gtid; j <= a.recent; j += gthreads)
+    if ((hi + j) % kMvPlaces == 0 && (hi + j) / kMvPlaces <= a.tiles)
+      before[(hi + j) / kMvPlaces] = a.keep - a.recent + j;
+  for (int j = gtid; j < a.recent; j += gthreads) {
     const int place = a.keep - a.recent + j;
     src[place] = hi + j;
     if (kept != nullptr) kept[place] = hi + j;
   }
-  __syncthreads();
-  if (tid == 0) {
+  cl.sync();
+  if (gtid == 0) {
+    int first = sh_first;
+    for (int c = 1; c < C; ++c) first = min(first, *cl.map_shared_rank(&sh_first, c));
     src[a.keep] = nb;
-    a.meta[b] = EvictMeta{a.keep + (tail > 0), sh_first, a.keep, nb + (tail > 0)};
+    a.meta[b] = EvictMeta{a.keep + (tail > 0), min(first, hi), a.keep, nb + (tail > 0)};
     a.len[b] = kBlock * a.keep + tail;
   }
+  cl.sync();   // no CTA exits while another reads its shared memory
 }
 
-// Moves the kept blocks together.  Place j takes block src[j] >= j and src is ascending, so a
-// CTA that walks its places in order, a tile at a time, reads nothing that it has overwritten:
-// the tile's loads (into registers) come before the barrier, its stores after it, and the next
-// tile's sources lie beyond this tile's places.  Streams that are independent go to their own
-// CTAs: K and V of each KV head, each cut into `parts` column ranges, the compressed keys and
-// the weights.  Nothing before the first place that changes is touched.
+// Moves the kept blocks together, in place: place j takes block src[j] >= j, and src ascends.  A
+// CTA takes a tile of places in ticket order, reads its blocks into registers and says so; it
+// writes once the tiles whose blocks lie in its places have been read.  Those are lower ones (or
+// itself), whose CTAs are running already, so the waits end; they are bounded all the same, and a
+// CTA that gave up writes nothing.  Bound by the moved bytes (4 KB of K and V, 132 of compressed
+// key and weight, each read and written once): any tile may be on its way.
 constexpr int kMvThreads = 512;
-constexpr int kMvUnits = 8;   // 16-byte units a thread holds
+constexpr int kMvUnits = kMvPlaces * 4 * 64 / kMvThreads;       // 16-byte units a thread holds
 
-__global__ void __launch_bounds__(kMvThreads) k_evict_move(EvictArgs a) {
-  const int tid = threadIdx.x, b = blockIdx.y;
+// grid (tiles * batch)
+__global__ void __launch_bounds__(kMvThreads, 2) k_evict_move(EvictArgs a) {
+  __shared__ int sh_ticket, sh_ok;
+  __shared__ int64_t sh_from[kMvPlaces], sh_to[kMvPlaces];   // pool blocks of KV head 0, or -1
+  __shared__ int64_t sh_kfrom[kMvPlaces], sh_kto[kMvPlaces];
+  const int tid = threadIdx.x;
+  pdl_wait();
+  if (tid == 0) sh_ticket = atomicAdd(a.ticket, 1);
+  __syncthreads();
+  // a sequence's tiles in order, the sequences side by side
+  const int b = sh_ticket % a.batch, tile = sh_ticket / a.batch;
   const EvictMeta m = a.meta[b];
   if (m.count == 0) return;
   const int32_t* src = a.src + static_cast<int64_t>(b) * (a.keep + 1);
-  const int stream = blockIdx.x;
-  if (stream < 4 * a.parts) {
-    const int which = stream / a.parts, part = stream % a.parts, g = which & 1;
-    uint4* pool = which < 2 ? a.k_blocks : a.v_blocks;
-    const int upb = 64 / a.parts;   // units of a block in this stream (a power of two)
-    const int64_t u_end = static_cast<int64_t>(m.count) * upb;
-    auto unit = [&](int64_t blk, int u) -> uint4* {
-      const int64_t row = pool_kv_row(a.pg, b, g, blk);
-      return row < 0 ? nullptr : pool + row * 16 + part * upb + u;
-    };
-    for (int64_t u0 = static_cast<int64_t>(m.first) * upb; u0 < u_end;
-         u0 += kMvThreads * kMvUnits) {
-      uint4 x[kMvUnits];
-#pragma unroll
-      for (int i = 0; i < kMvUnits; ++i) {
-        const int64_t u = u0 + i * kMvThreads + tid;
-        x[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (u < u_end) {
-          const uint4* p = unit(src[u / upb], static_cast<int>(u % upb));
-          if (p != nullptr) x[i] = __ldcg(p);
-          else if (stream == 0 && u % upb == 0) report_error(a.st, kErrDevice, 311);
-        }
+  int32_t* loaded = a.loaded + static_cast<int64_t>(b) * a.tiles;
+  float* mass = a.mass + static_cast<int64_t>(b) * a.cap_blocks;
+  const int j0 = tile * kMvPlaces, j1 = min(j0 + kMvPlaces, m.count);
+  const bool moves = j1 > m.first;
+  // the kept blocks that lie in this tile's places, as the tiles that read them: [dep0, dep1)
+  const int32_t* before = a.before + static_cast<int64_t>(b) * (a.tiles + 1);
+  const int dep0 = moves ? before[tile] / kMvPlaces : 0;
+  const int dep1 = moves ? min((before[tile + 1] + kMvPlaces - 1) / kMvPlaces, tile) : 0;
+  const int64_t kv = static_cast<int64_t>(a.pg.page_blocks);    // blocks from a head to the next
+  if (moves) {
+    if (tid < kMvPlaces) {
+      const int j = j0 + tid;
+      int64_t from = -1, to = -1, kfrom = -1, kto = -1;
+      if (j >= m.first && j < j1) {
+        from = pool_kv_row(a.pg, b, 0, src[j]);
+        to = pool_kv_row(a.pg, b, 0, j);
+        kfrom = pool_block(a.pg, b, src[j]);
+        kto = pool_block(a.pg, b, j);
+        if (from < 0) report_error(a.st, kErrDevice, 311);
+        if (to < 0) report_error(a.st, kErrDevice, 312);
+      } else {
+        to = -2;   // stays where it is
       }
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < kMvUnits; ++i) {
-        const int64_t u = u0 + i * kMvThreads + tid;
-        if (u < u_end) {
-          uint4* p = unit(u / upb, static_cast<int>(u % upb));
-          if (p != nullptr) __stcg(p, x[i]);
-          else if (stream == 0 && u % upb == 0) report_error(a.st, kErrDevice, 312);
-        }
-      }
-    }
-  } else if (stream == 4 * a.parts) {
-    const int64_t u_end = static_cast<int64_t>(m.whole) * 8;
-    for (int64_t u0 = static_cast<int64_t>(m.first) * 8; u0 < u_end; u0 += kMvThreads * kMvUnits) {
-      uint4 x[kMvUnits];
-#pragma unroll
-      for (int i = 0; i < kMvUnits; ++i) {
-        const int64_t u = u0 + i * kMvThreads + tid;
-        x[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (u < u_end) {
-          const int64_t blk = pool_block(a.pg, b, src[u / 8]);
-          if (blk >= 0) x[i] = __ldcg(a.kbar + blk * 8 + u % 8);
-        }
-      }
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < kMvUnits; ++i) {
-        const int64_t u = u0 + i * kMvThreads + tid;
-        if (u < u_end) {
-          const int64_t blk = pool_block(a.pg, b, u / 8);
-          if (blk >= 0) __stcg(a.kbar + blk * 8 + u % 8, x[i]);
-        }
-      }
-    }
-  } else {
-    float* mass = a.mass + static_cast<int64_t>(b) * a.cap_blocks;
-    for (int j0 = m.first; j0 < m.count; j0 += kMvThreads * kMvUnits) {
-      float x[kMvUnits];
-#pragma unroll
-      for (int i = 0; i < kMvUnits; ++i) {
-        const int j = j0 + i * kMvThreads + tid;
-        x[i] = j < m.count ? __ldcg(mass + src[j]) : 0.f;
-      }
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < kMvUnits; ++i) {
-        const int j = j0 + i * kMvThreads + tid;
-        if (j < m.count) __stcg(mass + j, x[i]);
-      }
+      sh_from[tid] = from;
+      sh_to[tid] = to;
+      sh_kfrom[tid] = kfrom;
+      sh_kto[tid] = j < m.whole ? kto : -1;
     }
     __syncthreads();
-    for (int j = m.count + tid; j < m.old; j += kMvThreads) mass[j] = 0.f;
+  }
+  uint4 x[kMvUnits], xk = make_uint4(0u, 0u, 0u, 0u);
+  float xm = 0.f;
+  // unit i of a thread: place i / 2 (of 16), K (i even) or V, both KV heads: 2 x 64 units of 16
+  // bytes by 512 threads is four places at a time
+  const int sub = tid >> 7, head = (tid >> 6) & 1, unit = tid & 63;
+  if (moves) {
+#pragma unroll
+    for (int i = 0; i < kMvUnits; ++i) {
+      const int p = 4 * (i >> 1) + sub;
+      const int64_t from = sh_from[p];
+      x[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (from >= 0)
+        x[i] = __ldcs(((i & 1) ? a.v_blocks : a.k_blocks) + (from + head * kv * kBlock) * 16 + unit);
+    }
+    if (tid < kMvPlaces * 8 && sh_kfrom[tid >> 3] >= 0)
+      xk = __ldcs(a.kbar + sh_kfrom[tid >> 3] * 8 + (tid & 7));
+    if (tid < kMvPlaces && j0 + tid >= m.first && j0 + tid < j1) xm = __ldcg(mass + src[j0 + tid]);
+  }
+  // Every thread's loads are done behind this barrier, since it takes their values (one release
+  // by one thread then does for all: a fence in each warp cost 4 times the move's time).
+  uint32_t fold = __float_as_uint(xm) ^ xk.x;
+#pragma unroll
+  for (int i = 0; i < kMvUnits; ++i) fold ^= moves ? x[i].x : 0u;
+  __syncthreads_or(fold == 0x5a5a5a5au);
+  if (tid == 0) {
+    sh_ok = 1;
+    asm volatile("st.release.gpu.global.s32 [%0], 1;" ::"l"(loaded + tile) : "memory");
+    if (moves) {
+      const uint64_t t0 = globaltimer();
+      for (int t = dep0; t < dep1 && sh_ok; ++t) {
+        int seen = 0;
+        while (true) {
+          asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(seen) : "l"(loaded + t) : "memory");
+          if (seen) break;
+          if (globaltimer() - t0 > kWaitLimitNs) {
+            sh_ok = 0;
+            report_error(a.st, kErrTimeout, 313);
+            break;
+          }
+        }
+      }
+    }
+  }
+  if (j0 < j1) {
+    // Weights behind the places become zero, each by the tile that holds the next kept block:
+    // no other tile reads or writes them.
+    const int from = j0 > 0 ? src[j0 - 1] + 1 : 0;
+    const int to = j1 == m.count ? m.old : src[j1 - 1] + 1;
+    for (int i = max(from, m.count) + tid; i < to; i += kMvThreads) mass[i] = 0.f;
+  }
+  __syncthreads();
+  if (moves && sh_ok) {
+#pragma unroll
+    for (int i = 0; i < kMvUnits; ++i) {
+      const int p = 4 * (i >> 1) + sub;
+      const int64_t to = sh_to[p];
+      if (to >= 0)
+        __stcs(((i & 1) ? a.v_blocks : a.k_blocks) + (to + head * kv * kBlock) * 16 + unit, x[i]);
+    }
+    if (tid < kMvPlaces * 8 && sh_kto[tid >> 3] >= 0)
+      __stcs(a.kbar + sh_kto[tid >> 3] * 8 + (tid & 7), xk);
+    if (tid < kMvPlaces && j0 + tid >= m.first && j0 + tid < j1) __stcg(mass + j0 + tid, xm);
   }
 }
 
