@@ -654,38 +654,70 @@ def gated_deltanet(q, k, v, log_alpha, beta, cu_seqlens, out=None, with_state=Fa
 
 
 # --------------------------------------------------------------------------------------
-def _same_device(dev, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+# A decode step calls these once per layer, so their checks are kept to a few attribute reads per
+# tensor; only a tensor that fails them is looked at more closely, for the message.
+def _is(t, name, dtype, shape, index):
+    """t must be a contiguous tensor of this dtype and shape on CUDA device `index`."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if (t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous()):
+        return
+    _need(t, name, dtype, tuple(shape), len(shape))
+    raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
 
 
-def _delta_shapes(q, k, v, log_alpha, beta, states, slots, out, lead, rows):
+def _raw_stream(index: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+class _on:
+    """`with torch.cuda.device(index)` that does nothing where index is current already."""
+
+    def __init__(self, index: int):
+        self.index = index
+
+    def __enter__(self):
+        self.before = torch._C._cuda_getDevice()
+        if self.before != self.index:
+            torch._C._cuda_setDevice(self.index)
+
+    def __exit__(self, *exc):
+        if self.before != self.index:
+            torch._C._cuda_setDevice(self.before)
+
+
+def _delta_shapes(q, k, v, log_alpha, beta, states, slots, out, lead, rows, index):
     """Checks of the tensors that extend and step share; `lead`: the leading dimensions of the
     token tensors.  Returns (key_heads, heads)."""
     nd = len(lead)
-    _need(v, "v", torch.bfloat16, (HEAD_DIM,), nd + 2)
-    _need(q, "q", torch.bfloat16, (HEAD_DIM,), nd + 2)
-    Hk, H = q.shape[nd], v.shape[nd]
-    _need(k, "k", torch.bfloat16, (Hk, HEAD_DIM), nd + 2)
-    _need(log_alpha, "log_alpha", torch.float32, (H,), nd + 1)
-    _need(beta, "beta", torch.float32, (H,), nd + 1)
-    for name, t in (("q", q), ("k", k), ("v", v), ("log_alpha", log_alpha), ("beta", beta)):
-        if tuple(t.shape[:nd]) != tuple(lead):
-            raise ValueError(f"{name} has leading dimensions {tuple(t.shape[:nd])}, expected "
-                             f"{tuple(lead)}")
+    for name, t in (("v", v), ("q", q)):
+        if not isinstance(t, torch.Tensor) or t.dim() != nd + 2:
+            _need(t, name, torch.bfloat16, None, nd + 2)
+    H, Hk = v.shape[nd], q.shape[nd]
+    shape = (*lead, H, HEAD_DIM)
+    keys = shape if Hk == H else (*lead, Hk, HEAD_DIM)
+    gates = shape[:-1]
+    _is(v, "v", torch.bfloat16, shape, index)
+    _is(q, "q", torch.bfloat16, keys, index)
+    _is(k, "k", torch.bfloat16, keys, index)
+    _is(log_alpha, "log_alpha", torch.float32, gates, index)
+    _is(beta, "beta", torch.float32, gates, index)
     if Hk < 1 or H % Hk:
         raise ValueError(f"{H} heads do not divide over {Hk} key heads")
-    _need(states, "states", torch.float32, (H, HEAD_DIM, HEAD_DIM), 4)
+    if not isinstance(states, torch.Tensor) or states.dim() != 4:
+        _need(states, "states", torch.float32, None, 4)
+    _is(states, "states", torch.float32, (states.shape[0], H, HEAD_DIM, HEAD_DIM), index)
     if slots is not None:
-        _need(slots, "slots", torch.int32, (rows,), 1)
+        _is(slots, "slots", torch.int32, (rows,), index)
     elif states.shape[0] < rows:
         raise ValueError(f"{rows} rows need as many states, got {states.shape[0]}")
     if out is not None:
-        _need(out, "out", torch.bfloat16, tuple(v.shape), nd + 2)
-    _same_device(v.device, q=q, k=k, log_alpha=log_alpha, beta=beta, states=states, slots=slots,
-                 out=out)
+        _is(out, "out", torch.bfloat16, shape, index)
     return Hk, H
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 class DeltaExtend:
@@ -717,20 +749,22 @@ class DeltaExtend:
         [T, heads]; states fp32 [slots, heads, 128 (v), 128 (k)] is updated in place: sequence s
         continues states[slots[s]] (int32 on the device; None: states[s]).  Returns out bf16
         [T, heads, 128]."""
+        index = self.device.index
         Hk, H = _delta_shapes(q, k, v, log_alpha, beta, states, slots, out, (self.T,),
-                              self.num_seqs)
+                              self.num_seqs, index)
         if (Hk, H) != (self.key_heads, self.heads):
             raise ValueError(f"{Hk} key heads and {H} heads, the context has {self.key_heads} and "
                              f"{self.heads}")
-        _same_device(self.device, v=v)
         if out is None:
             out = torch.empty_like(v)
-        with torch.cuda.device(self.device):
-            _check("qsa_gated_deltanet_extend", self.lib.qsa_gated_deltanet_extend(
-                _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta), _ptr(self.d_cu),
-                ctypes.c_void_p(self.h_cu.data_ptr()), self.num_seqs, Hk, H, _ptr(states),
-                states.shape[0], _ptr(slots), _ptr(out), _ptr(self.ws), self.ws.numel(),
-                _stream(self.device)))
+        with _on(index):
+            r = self.lib.qsa_gated_deltanet_extend(
+                q.data_ptr(), k.data_ptr(), v.data_ptr(), log_alpha.data_ptr(), beta.data_ptr(),
+                self.d_cu.data_ptr(), self.h_cu.data_ptr(), self.num_seqs, Hk, H,
+                states.data_ptr(), states.shape[0], _addr(slots), out.data_ptr(),
+                self.ws.data_ptr(), self.ws.numel(), _raw_stream(index))
+        if r:
+            raise QSAError("qsa_gated_deltanet_extend", r)
         return out
 
     def device_error(self):
@@ -753,16 +787,19 @@ def gated_deltanet_step(q, k, v, log_alpha, beta, states, slots=None, counts=Non
     if not isinstance(v, torch.Tensor) or v.dim() != 4:
         raise ValueError("v must be a [B, n, heads, 128] tensor")
     B, n = v.shape[:2]
-    Hk, H = _delta_shapes(q, k, v, log_alpha, beta, states, slots, out, (B, n), B)
+    index = v.get_device()
+    Hk, H = _delta_shapes(q, k, v, log_alpha, beta, states, slots, out, (B, n), B, index)
     if counts is not None:
-        _need(counts, "counts", torch.int32, (B,), 1)
-        _same_device(v.device, counts=counts)
+        _is(counts, "counts", torch.int32, (B,), index)
     if out is None:
         out = torch.empty_like(v) if slots is None and counts is None else torch.zeros_like(v)
-    with torch.cuda.device(v.device):
-        _check("qsa_gated_deltanet_step", load().qsa_gated_deltanet_step(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta), B, n, _ptr(counts), Hk, H,
-            _ptr(states), states.shape[0], _ptr(slots), _ptr(out), _stream(v.device)))
+    with _on(index):
+        r = load().qsa_gated_deltanet_step(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), log_alpha.data_ptr(), beta.data_ptr(), B, n,
+            _addr(counts), Hk, H, states.data_ptr(), states.shape[0], _addr(slots),
+            out.data_ptr(), _raw_stream(index))
+    if r:
+        raise QSAError("qsa_gated_deltanet_step", r)
     return out
 
 
@@ -783,12 +820,14 @@ class Evictor:
                                               self.recent)
         if n == 0:
             raise QSAError("qsa_evict_workspace_size", 1)
+        paged = "_paged" if self._paged else ""
+        self._accumulate = getattr(self.lib, "qsa_accumulate_weights" + paged)
+        self._evict = getattr(self.lib, "qsa_evict" + paged)
         shape = (cache.batch, cache.capacity // BLOCK)
         dev = cache.len.device
         if mass is None:
             mass = torch.zeros(shape, dtype=torch.float32, device=dev)
-        _need(mass, "mass", torch.float32, shape, 2)
-        _same_device(dev, mass=mass)
+        _is(mass, "mass", torch.float32, shape, cache.len.get_device())
         self.mass = mass
         with torch.cuda.device(dev):
             self.ws = new_workspace(n, dev)
@@ -797,34 +836,36 @@ class Evictor:
         """Add the attention weights of one decode step: its q [B, 24, 128] and the selection it
         returned (Decoder.run(with_selection=True)).  Returns mass."""
         B = self.cache.batch
-        _need(q, "q", torch.bfloat16, (B, NUM_HEADS, HEAD_DIM), 3)
-        _need(sel_idx, "sel_idx", torch.int32, ndim=2)
-        _need(sel_cnt, "sel_cnt", torch.int32, (B,), 1)
-        if sel_idx.shape[0] != B:
-            raise ValueError(f"sel_idx has {sel_idx.shape[0]} rows, the cache {B} sequences")
-        dev = self.mass.device
-        _same_device(dev, q=q, sel_idx=sel_idx, sel_cnt=sel_cnt)
+        index = self.mass.get_device()
+        _is(q, "q", torch.bfloat16, (B, NUM_HEADS, HEAD_DIM), index)
+        if not isinstance(sel_idx, torch.Tensor) or sel_idx.dim() != 2:
+            _need(sel_idx, "sel_idx", torch.int32, None, 2)
+        _is(sel_idx, "sel_idx", torch.int32, (B, sel_idx.shape[1]), index)
+        _is(sel_cnt, "sel_cnt", torch.int32, (B,), index)
         desc = self.cache.desc()
-        name = "qsa_accumulate_weights" + ("_paged" if self._paged else "")
-        with torch.cuda.device(dev):
-            _check(name, getattr(self.lib, name)(
-                _ptr(q), ctypes.byref(desc), _ptr(sel_idx), _ptr(sel_cnt), sel_idx.shape[1],
-                _ptr(self.mass), _ptr(self.ws), self.ws.numel(), _stream(dev)))
+        with _on(index):
+            r = self._accumulate(
+                q.data_ptr(), ctypes.byref(desc), sel_idx.data_ptr(), sel_cnt.data_ptr(),
+                sel_idx.shape[1], self.mass.data_ptr(), self.ws.data_ptr(), self.ws.numel(),
+                _raw_stream(index))
+        if r:
+            raise QSAError(self._accumulate.__name__, r)
         return self.mass
 
     def evict(self, with_kept: bool = False):
         """Cut every sequence of more than keep_blocks complete blocks to keep_blocks (in place;
         the cache's lengths follow).  With with_kept, returns the old indices of the blocks that
         stay, int32 [B, keep_blocks] (-1 padded)."""
-        dev = self.mass.device
-        kept = (torch.empty((self.cache.batch, self.keep), dtype=torch.int32, device=dev)
-                if with_kept else None)
+        index = self.mass.get_device()
+        kept = (torch.empty((self.cache.batch, self.keep), dtype=torch.int32,
+                            device=self.mass.device) if with_kept else None)
         desc = self.cache.desc()
-        name = "qsa_evict" + ("_paged" if self._paged else "")
-        with torch.cuda.device(dev):
-            _check(name, getattr(self.lib, name)(
-                ctypes.byref(desc), _ptr(self.mass), self.keep, self.sinks, self.recent,
-                _ptr(kept), _ptr(self.ws), self.ws.numel(), _stream(dev)))
+        with _on(index):
+            r = self._evict(
+                ctypes.byref(desc), self.mass.data_ptr(), self.keep, self.sinks, self.recent,
+                _addr(kept), self.ws.data_ptr(), self.ws.numel(), _raw_stream(index))
+        if r:
+            raise QSAError(self._evict.__name__, r)
         self.cache.h_len = [BLOCK * self.keep + n % BLOCK if n // BLOCK > self.keep else n
                             for n in self.cache.h_len]
         return kept

@@ -1444,8 +1444,14 @@ qsa_status weights_impl(const void* q, const CacheView& view, const int32_t* sel
   a.pg = view.pg;
   a.st = dev_status(workspace);
   // as many CTAs to a sequence as keep the grid within two CTAs an SM
-  int cluster = 8;
-  while (cluster > 1 && int64_t(cluster) * c->batch > 2 * num_sms()) cluster /= 2;
+  // (and at least a tile to a warp)
+  int cluster = kWtMaxCluster;
+  while (cluster > 1 && (int64_t(cluster) * c->batch > 2 * num_sms() ||
+                         wt_tiles_per_cta(topk, cluster) < kWtWarps / 2))
+    cluster /= 2;
+  if (cudaFuncSetAttribute(k_block_weights, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+      cudaSuccess)
+    return QSA_ERR_CUDA;
   const int smem = wt_smem_bytes(topk, cluster);
   if (!set_smem(k_block_weights, smem)) return QSA_ERR_CUDA;
   QSA_CHECK_PDL(launch_cluster(k_block_weights, dim3(cluster, c->batch), dim3(kWtThreads), smem,

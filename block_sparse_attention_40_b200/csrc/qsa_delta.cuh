@@ -54,7 +54,7 @@ __device__ __forceinline__ int64_t delta_row_tokens(const DeltaArgs& a, int r, i
   return begin;
 }
 
-// Whether an earlier row with tokens to take names row r's slot.  All threads of the block call
+// Whether an earlier row names row r's slot.  All threads of the block call
 // it, and all get the answer.
 __device__ __forceinline__ bool delta_slot_taken(const DeltaArgs& a, int r, int slot) {
   if (a.slots == nullptr) return false;
@@ -96,24 +96,40 @@ __global__ void __launch_bounds__(kStepThreads) k_delta_step(DeltaArgs a) {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       S[i][j] = __ldcs(reinterpret_cast<const float4*>(st + i * kGdnDim + 32 * j));
-  if (delta_slot_taken(a, r, slot)) return;
-  for (int64_t t = t0; t < t0 + n; ++t) {
+  // a token's inputs, on their way while the one before it is taken
+  uint2 wq[4], wk[4];
+  float la, beta;
+  __nv_bfloat16 wv[RV];
+  auto fetch = [&](int64_t t) {
     const uint2* qp = reinterpret_cast<const uint2*>(a.q + (t * a.key_heads + kh) * kGdnDim) + l8;
     const uint2* kp = reinterpret_cast<const uint2*>(a.k + (t * a.key_heads + kh) * kGdnDim) + l8;
-    const float al = expf(fmaxf(a.log_alpha[t * a.heads + h], kGdnMinLogAlpha));
-    const float bt = a.beta[t * a.heads + h];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      wq[j] = qp[8 * j];
+      wk[j] = kp[8 * j];
+    }
+    la = a.log_alpha[t * a.heads + h];
+    beta = a.beta[t * a.heads + h];
     const __nv_bfloat16* vp = a.v + (t * a.heads + h) * kGdnDim + v0;
+#pragma unroll
+    for (int i = 0; i < RV; ++i) wv[i] = vp[i];
+  };
+  fetch(t0);
+  if (delta_slot_taken(a, r, slot)) return;
+  for (int64_t t = t0; t < t0 + n; ++t) {
+    const float al = expf(fmaxf(la, kGdnMinLogAlpha));
+    const float bt = beta;
     float q[16], k[16], x[RV];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const uint2 wq = qp[8 * j], wk = kp[8 * j];
-      unpack_bf16x2(wq.x, q + 4 * j);
-      unpack_bf16x2(wq.y, q + 4 * j + 2);
-      unpack_bf16x2(wk.x, k + 4 * j);
-      unpack_bf16x2(wk.y, k + 4 * j + 2);
+      unpack_bf16x2(wq[j].x, q + 4 * j);
+      unpack_bf16x2(wq[j].y, q + 4 * j + 2);
+      unpack_bf16x2(wk[j].x, k + 4 * j);
+      unpack_bf16x2(wk[j].y, k + 4 * j + 2);
     }
 #pragma unroll
-    for (int i = 0; i < RV; ++i) x[i] = __bfloat162float(vp[i]);
+    for (int i = 0; i < RV; ++i) x[i] = __bfloat162float(wv[i]);
+    if (t + 1 < t0 + n) fetch(t + 1);
     float kq = 0.f, sk[RV], sq[RV];
 #pragma unroll
     for (int e = 0; e < 16; ++e) kq = fmaf(k[e], q[e], kq);

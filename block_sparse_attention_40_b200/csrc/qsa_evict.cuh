@@ -18,16 +18,17 @@ namespace qsa {
 // Attention weights per block.  For each head, with the scaled logits x of the live tokens of
 // the selected blocks and the own block,  w[blk] = sum_heads sum_{t in blk} e^(x_t - lse_h).
 //
-// One cluster of C CTAs per sequence; a warp takes tiles of 4 blocks (16 token rows) of one KV
-// head.  A tile's logits are one 16 x 16 x 128 product (tokens x the group's 12 heads, padded
-// to 16): warp MMAs, since 12 query rows would leave most of a tcgen05 tile empty and the
-// kernel is bound by the keys' bytes (2 KB a block).  Keys go straight from global memory to the
-// operand registers: the order of the 128 dims inside the product is free, so each lane's
-// fragments are whole 16-byte words.  Every (block, head) pair leaves one number, the log2 of
-// the sum of its 4 exponentials, in shared memory; the heads' totals are then joined over the
-// CTA and the cluster (distributed shared memory) in a fixed order, and each block's weight
-// is the sum over heads of 2^(block's log-sum - head's total): one pass over the keys and no
-// second launch.
+// One cluster of C CTAs per sequence, each with a part of the selected blocks, whose places in the
+// pool it looks up first.  A warp takes tiles of 4 blocks (16 token rows) of one KV head, the next
+// tile's keys on their way.  A tile's logits are one 16 x 16 x 128 product (tokens x the group's
+// 12 heads, padded to 16): warp MMAs, since 12 query rows would leave most of a tcgen05 tile empty
+// and the kernel is bound by the keys' bytes (2 KB a block), or by latency where there are few.
+// Keys go straight from global memory to the operand registers: the order of the 128 dims inside
+// the product is free, so each lane's fragments are whole 16-byte words.  Every (block, head) pair
+// leaves one number, the log2 of the sum of its 4 exponentials, in shared memory; the heads'
+// totals are then joined over the CTA and the cluster (distributed shared memory) in a fixed
+// order, and each block's weight is the sum over heads of 2^(block's log-sum - head's total): one
+// pass over the keys and no second launch.
 constexpr int kWtThreads = 256;
 constexpr int kWtWarps = kWtThreads / 32;
 constexpr int kWtMaxCluster = 16;
@@ -45,6 +46,18 @@ struct WeightArgs {
   DevStatus st;
 };
 
+// 2^x to 2 ulp (0 for -inf) and log2 x to 2^-22 (-inf for 0): a weight is off by as much
+__device__ __forceinline__ float wt_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float wt_log2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 __device__ __forceinline__ void mma_bf16_16816(float* c, const uint32_t* a, uint32_t b0,
                                                uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
@@ -57,8 +70,9 @@ __device__ __forceinline__ void mma_bf16_16816(float* c, const uint32_t* a, uint
 __host__ __device__ constexpr int wt_tiles_per_cta(int topk, int c) {
   return ((topk + 1 + 3) / 4 + c - 1) / c;
 }
+// log-sums (rows of 25: without bank conflicts), logical blocks, places in the pool
 __host__ __device__ constexpr int wt_smem_bytes(int topk, int c) {
-  return wt_tiles_per_cta(topk, c) * 4 * (kHeads + 1) * 4;
+  return wt_tiles_per_cta(topk, c) * 4 * (kHeads + 1 + 2) * 4;
 }
 
 // grid (C, B), clusters of (C, 1, 1)
@@ -70,6 +84,9 @@ __global__ void __launch_bounds__(kWtThreads) k_block_weights(WeightArgs a) {
   __shared__ float head_lse[kHeads];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tq = lane & 3;
   const int C = gridDim.x, rank = blockIdx.x, b = blockIdx.y;
+  const int per = wt_tiles_per_cta(a.topk, C) * 4;    // items per CTA: selected blocks, own block
+  int32_t* blk_sh = reinterpret_cast<int32_t*>(lse_sh + per * (kHeads + 1));   // -1: not used
+  int32_t* at_sh = blk_sh + per;                      // its K rows / 4 (KV head 0); -1: reads as zeros
   const int len = a.len[b];
   const int own = (len - 1) / kBlock;
   int n = a.cnt[b];
@@ -77,16 +94,8 @@ __global__ void __launch_bounds__(kWtThreads) k_block_weights(WeightArgs a) {
   if (bad && tid == 0 && rank == 0) report_error(a.st, kErrDevice, 300);
   if (bad) n = 0;
   const int items = bad ? 0 : n + 1;
-  const int per = wt_tiles_per_cta(a.topk, C) * 4;    // items per CTA
   const int i0 = rank * per, mine = max(0, min(per, items - i0));
   const int32_t* idx = a.idx + static_cast<int64_t>(b) * a.topk;
-  // block of item i, -1 where it cannot be used (out of order or range)
-  auto item_block = [&](int i) -> int {
-    if (i == n) return own;
-    const int x = idx[i];
-    const int before = i > 0 ? idx[i - 1] : -1;
-    return (x <= before || x < 0 || x >= own) ? -1 : x;
-  };
   const int kv = warp & 1;
   // this KV head's queries as B fragments: n-tile 0 is heads 0..7, n-tile 1 heads 8..11
   uint4 qf[2][4];
@@ -100,32 +109,47 @@ __global__ void __launch_bounds__(kWtThreads) k_block_weights(WeightArgs a) {
         qf[nt][j] = *reinterpret_cast<const uint4*>(
             a.q + ((static_cast<int64_t>(b) * kHeads + kv * kGroup + hd) * kHeadDim + 32 * j + 8 * tq));
     }
-  const float scale = 0.08838834764831845f * 1.4426950408889634f;   // 1/sqrt(128) in log2 units
-  for (int tile = warp >> 1; tile * 4 < mine; tile += kWtWarps / 2) {
-    uint4 kf[2][4];
-    bool live[2];
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int li = tile * 4 + (g >> 2) + 2 * half, tok = g & 3;
-      int blk = -1;
-      if (li < mine) {
-        blk = item_block(i0 + li);
-        if (blk < 0 && kv == 0 && (lane & 15) == 0) report_error(a.st, kErrDevice, 301);
+  for (int li = tid; li < per; li += kWtThreads) {
+    int blk = -1, at = -1;
+    if (li < mine) {
+      const int i = i0 + li;
+      if (i == n) {
+        blk = own;
+      } else {
+        // out of order or range: left out
+        const int x = idx[i], before = i > 0 ? idx[i - 1] : -1;
+        blk = (x <= before || x < 0 || x >= own) ? -1 : x;
+        if (blk < 0) report_error(a.st, kErrDevice, 301);
       }
-      live[half] = blk >= 0 && blk * kBlock + tok < len;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) kf[half][j] = make_uint4(0u, 0u, 0u, 0u);
-      if (live[half]) {
-        const int64_t row = pool_kv_row(a.pg, b, kv, blk);
-        if (row < 0) {   // reads as zeros, as in the decode attention
-          if (tq == 0) report_error(a.st, kErrDevice, 302);
-        } else {
-          const uint4* kp = reinterpret_cast<const uint4*>(a.k_blocks + (row + tok) * kHeadDim) + tq;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) kf[half][j] = kp[4 * j];
-        }
+      if (blk >= 0) {
+        const int64_t row = pool_kv_row(a.pg, b, 0, blk);
+        at = row < 0 ? -1 : static_cast<int32_t>(row / kBlock);
+        if (row < 0) report_error(a.st, kErrDevice, 302);
       }
     }
+    blk_sh[li] = blk;
+    at_sh[li] = at;
+  }
+  __syncthreads();
+  const float scale = 0.08838834764831845f * 1.4426950408889634f;   // 1/sqrt(128) in log2 units
+  const int tiles = (mine + 3) / 4, step = kWtWarps / 2;
+  auto fetch = [&](int tile, uint4 (*kf)[4]) {
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int li = tile * 4 + (g >> 2) + 2 * half;
+      const int at = tile < tiles ? at_sh[li] : -1;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) kf[half][j] = make_uint4(0u, 0u, 0u, 0u);
+      // tokens behind the last one are read too (the block's space is there) and masked below
+      if (at >= 0) {
+        const int64_t row = (static_cast<int64_t>(at) + kv * a.pg.page_blocks) * kBlock + (g & 3);
+        const uint4* kp = reinterpret_cast<const uint4*>(a.k_blocks + row * kHeadDim) + tq;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) kf[half][j] = kp[4 * j];
+      }
+    }
+  };
+  auto logits = [&](int tile, const uint4 (*kf)[4]) {
     float acc[2][4];
 #pragma unroll
     for (int nt = 0; nt < 2; ++nt)
@@ -143,22 +167,37 @@ __global__ void __launch_bounds__(kWtThreads) k_block_weights(WeightArgs a) {
     }
     // rows of one block sit in lanes that differ in bits 2 and 3: join its four tokens
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt)
+    for (int half = 0; half < 2; ++half) {
+      const int li = tile * 4 + (g >> 2) + 2 * half;
+      const int blk = blk_sh[li];
+      const bool live = blk >= 0 && blk * kBlock + (g & 3) < len;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int half = e >> 1;
-        const float x = live[half] ? acc[nt][e] * scale : -INFINITY;
-        float m = x;
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-        float s = x == -INFINITY ? 0.f : exp2f(x - m);
-        s += __shfl_xor_sync(0xffffffffu, s, 4);
-        s += __shfl_xor_sync(0xffffffffu, s, 8);
-        const int hd = nt * 8 + 2 * tq + (e & 1);
-        const int li = tile * 4 + (g >> 2) + 2 * half;
-        if ((g & 3) == 0 && hd < kGroup && li < mine)
-          lse_sh[li * (kHeads + 1) + kv * kGroup + hd] = m + log2f(s);
-      }
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int e = 2 * half; e < 2 * half + 2; ++e) {
+          const float x = live ? acc[nt][e] * scale : -INFINITY;
+          float m = x;
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+          float s = x == -INFINITY ? 0.f : wt_exp2(x - m);
+          s += __shfl_xor_sync(0xffffffffu, s, 4);
+          s += __shfl_xor_sync(0xffffffffu, s, 8);
+          const int hd = nt * 8 + 2 * tq + (e & 1);
+          if ((g & 3) == 0 && hd < kGroup) lse_sh[li * (kHeads + 1) + kv * kGroup + hd] = m + wt_log2(s);
+        }
+    }
+  };
+  {
+    uint4 ka[2][4], kb[2][4];
+    int tile = warp >> 1;
+    fetch(tile, ka);
+    for (; tile < tiles; tile += 2 * step) {
+      fetch(tile + step, kb);
+      logits(tile, ka);
+      if (tile + step >= tiles) break;
+      fetch(tile + 2 * step, ka);
+      logits(tile + step, kb);
+    }
   }
   __syncthreads();
   // per head: this CTA's max and sum (one warp takes heads warp, warp + 8, ..)
@@ -169,7 +208,7 @@ __global__ void __launch_bounds__(kWtThreads) k_block_weights(WeightArgs a) {
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     float s = 0.f;
     if (m > -INFINITY)
-      for (int i = lane; i < mine; i += 32) s += exp2f(lse_sh[i * (kHeads + 1) + hd] - m);
+      for (int i = lane; i < mine; i += 32) s += wt_exp2(lse_sh[i * (kHeads + 1) + hd] - m);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (lane == 0) {
@@ -178,25 +217,37 @@ __global__ void __launch_bounds__(kWtThreads) k_block_weights(WeightArgs a) {
     }
   }
   cl.sync();
-  if (tid < kHeads) {
-    float m = -INFINITY;
-    for (int c = 0; c < C; ++c) m = fmaxf(m, *cl.map_shared_rank(&head_m[tid], c));
-    float s = 0.f;
-    for (int c = 0; c < C; ++c) {
-      const float mc = *cl.map_shared_rank(&head_m[tid], c);
-      if (mc > -INFINITY) s += *cl.map_shared_rank(&head_s[tid], c) * exp2f(mc - m);
+  // the heads' totals over the cluster, a CTA a lane
+  for (int hd = warp; hd < kHeads; hd += kWtWarps) {
+    float mc = -INFINITY, s = 0.f;
+    if (lane < C) {
+      mc = *cl.map_shared_rank(&head_m[hd], lane);
+      s = *cl.map_shared_rank(&head_s[hd], lane);
     }
-    head_lse[tid] = m + log2f(s);
-  }
-  cl.sync();   // also: no CTA exits while another reads its shared memory
-  for (int li = tid; li < mine; li += kWtThreads) {
-    const int blk = item_block(i0 + li);
-    if (blk < 0) continue;
-    float w = 0.f;
+    float m = mc;
 #pragma unroll
-    for (int hd = 0; hd < kHeads; ++hd) w += exp2f(lse_sh[li * (kHeads + 1) + hd] - head_lse[hd]);
-    a.mass[static_cast<int64_t>(b) * a.cap_blocks + blk] += w;
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    s = mc > -INFINITY ? s * wt_exp2(mc - m) : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) head_lse[hd] = m + wt_log2(s);
   }
+  __syncthreads();
+  cl.barrier_arrive();   // this CTA has read the others' sums
+  // four lanes to a block, six heads each
+  for (int l0 = 0; l0 < mine; l0 += kWtThreads / 4) {
+    const int li = l0 + (tid >> 2), h0 = (tid & 3) * (kHeads / 4);
+    const int blk = li < mine ? blk_sh[li] : -1;
+    float w = 0.f;
+    if (blk >= 0)
+#pragma unroll
+      for (int hd = 0; hd < kHeads / 4; ++hd)
+        w += wt_exp2(lse_sh[li * (kHeads + 1) + h0 + hd] - head_lse[h0 + hd]);
+    w += __shfl_xor_sync(0xffffffffu, w, 1);
+    w += __shfl_xor_sync(0xffffffffu, w, 2);
+    if (blk >= 0 && (tid & 3) == 0) a.mass[static_cast<int64_t>(b) * a.cap_blocks + blk] += w;
+  }
+  cl.barrier_wait();   // no CTA exits while another reads its shared memory
 }
 
 // ---------------------------------------------------------------------------------------
@@ -246,19 +297,35 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 }
 
 // Runs f(first index, keys, how many are in range) over i0 .. i1-1, kEvBatch consecutive weights
-// a thread, all threads of the CTA together; the next batch is on its way meanwhile.
-template <typename F>
-__device__ __forceinline__ void ev_scan(const float* mass, int i0, int i1, F&& f) {
-  float w[2][kEvBatch];
-  auto fetch = [&](int base, float* x) {
-    const int i = base + kEvBatch * static_cast<int>(threadIdx.x);
+// a thread, all threads of the CTA together.  A part of one batch a thread stays in registers
+// (`held`, from ev_hold); of a longer one the next batch is on its way meanwhile.
+constexpr int kEvOnce = kEvThreads * kEvBatch;
+
+__device__ __forceinline__ void ev_fetch(const float* mass, int base, int i1, float* x) {
+  const int i = base + kEvBatch * static_cast<int>(threadIdx.x);
 #pragma unroll
-    for (int b = 0; b < kEvBatch; ++b) x[b] = i + b < i1 ? mass[i + b] : 0.f;
-  };
-  fetch(i0, w[0]);
-  for (int base = i0; base < i1; base += kEvThreads * kEvBatch) {
-    fetch(base + kEvThreads * kEvBatch, w[1]);
-    const int i = base + kEvBatch * static_cast<int>(threadIdx.x);
+  for (int b = 0; b < kEvBatch; ++b) x[b] = i + b < i1 ? mass[i + b] : 0.f;
+}
+
+__device__ __forceinline__ void ev_hold(const float* mass, int i0, int i1, uint32_t* held) {
+  float w[kEvBatch];
+  ev_fetch(mass, i0, i1, w);
+#pragma unroll
+  for (int b = 0; b < kEvBatch; ++b) held[b] = weight_key(w[b]);
+}
+
+template <typename F>
+__device__ __forceinline__ void ev_scan(const float* mass, int i0, int i1, const uint32_t* held,
+                                        F&& f) {
+  const int first = i0 + kEvBatch * static_cast<int>(threadIdx.x);
+  if (i1 - i0 <= kEvOnce) {
+    if (i0 < i1) f(first, held, i1 - first);
+    return;
+  }
+  float w[2][kEvBatch];
+  ev_fetch(mass, i0, i1, w[0]);
+  for (int base = i0, i = first; base < i1; base += kEvOnce, i += kEvOnce) {
+    ev_fetch(mass, base + kEvOnce, i1, w[1]);
     uint32_t key[kEvBatch];
 #pragma unroll
     for (int b = 0; b < kEvBatch; ++b) key[b] = weight_key(w[0][b]);
@@ -316,6 +383,8 @@ __global__ void __launch_bounds__(kEvThreads, 1) k_evict_select(EvictArgs a) {
   const uint32_t want = static_cast<uint32_t>(a.keep - a.sinks - a.recent);
   const int per = (hi - lo + C - 1) / C;
   const int i0 = min(hi, lo + rank * per), i1 = min(hi, i0 + per);   // this CTA's
+  uint32_t held[kEvBatch];
+  ev_hold(mass, i0, i1, held);
   // key of the last candidate that stays (prefix) and how many of that key stay (need)
   if (tid == 0) {
     sh_prefix = 0u;
@@ -330,7 +399,7 @@ __global__ void __launch_bounds__(kEvThreads, 1) k_evict_select(EvictArgs a) {
     const uint32_t bins = 1u << bits[d];
     uint32_t zeros = 0;   // blocks that were never attended to: counted apart, not one by one
     const uint32_t zero_key = weight_key(0.f);
-    ev_scan(mass, i0, i1, [&](int, const uint32_t* key, int n) {
+    ev_scan(mass, i0, i1, held, [&](int, const uint32_t* key, int n) {
 #pragma unroll
       for (int j = 0; j < kEvBatch; ++j) {
         const bool on = j < n && (d == 0 || (key[j] >> (shift[d] + bits[d])) == prefix);
@@ -394,7 +463,7 @@ __global__ void __launch_bounds__(kEvThreads, 1) k_evict_select(EvictArgs a) {
   if (want > 0) {
     if (C > 1) {
       uint32_t gt = 0, eq = 0;
-      ev_scan(mass, i0, i1, [&](int, const uint32_t* key, int n) {
+      ev_scan(mass, i0, i1, held, [&](int, const uint32_t* key, int n) {
 #pragma unroll
         for (int j = 0; j < kEvBatch; ++j) {
           gt += j < n && key[j] > last;
@@ -417,7 +486,7 @@ __global__ void __launch_bounds__(kEvThreads, 1) k_evict_select(EvictArgs a) {
     }
     // ordered pass: a block before which m larger and e equal candidates stand takes place
     // sinks + m + min(e, ties)
-    ev_scan(mass, i0, i1, [&](int i, const uint32_t* key, int n) {
+    ev_scan(mass, i0, i1, held, [&](int i, const uint32_t* key, int n) {
       // counts of both in one 32-bit scan (at most 4,096 of each)
       uint32_t own = 0;
 #pragma unroll
