@@ -1367,6 +1367,17 @@ extern "C" qsa_status qsa_gated_deltanet_extend(
     a.seg_trans = reinterpret_cast<float*>(ws + p.o_trans);
   }
   a.st = dev_status(workspace);
+  ScanMaps maps;
+  {
+    const uint32_t box[3] = {64, 1, kGdnChunk};
+    const uint64_t tok = static_cast<uint64_t>(a.d.tokens);
+    const uint64_t kd[3] = {kGdnDim, static_cast<uint64_t>(key_heads), tok};
+    const uint64_t ks[2] = {kGdnDim * 2, static_cast<uint64_t>(key_heads) * kGdnDim * 2};
+    const uint64_t vd[3] = {kGdnDim, static_cast<uint64_t>(heads), tok};
+    const uint64_t vs[2] = {kGdnDim * 2, static_cast<uint64_t>(heads) * kGdnDim * 2};
+    if (!make_tmap(&maps.k, k, 3, kd, ks, box) || !make_tmap(&maps.v, v, 3, vd, vs, box))
+      return QSA_ERR_CUDA;
+  }
   const int prep_smem = static_cast<int>(sizeof(PrepSmem));
   if (!set_smem(k_delta_prep, prep_smem) || !set_smem(k_delta_scan, kScanSmemBytes))
     return QSA_ERR_CUDA;
@@ -1378,7 +1389,7 @@ extern "C" qsa_status qsa_gated_deltanet_extend(
     QSA_CHECK_LAUNCH();
     if (p.segs > 1) {
       k_delta_scan<<<dim3(a.nheads, num_seqs, 2 * (p.segs - 1)), kScanThreads, kScanSmemBytes, s>>>(
-          a, kScanEnds);
+          maps, a, kScanEnds);
       QSA_CHECK_LAUNCH();
       if (p.segs > 2) {
         if (!set_smem(k_delta_join, kJoinSmemBytes)) return QSA_ERR_CUDA;
@@ -1388,7 +1399,7 @@ extern "C" qsa_status qsa_gated_deltanet_extend(
       }
     }
     k_delta_scan<<<dim3(a.nheads, num_seqs, p.segs), kScanThreads, kScanSmemBytes, s>>>(
-        a, p.segs > 1 ? kScanOutputs : kScanWhole);
+        maps, a, p.segs > 1 ? kScanOutputs : kScanWhole);
     QSA_CHECK_LAUNCH();
   }
   return QSA_OK;

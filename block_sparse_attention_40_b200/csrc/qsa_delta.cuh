@@ -717,15 +717,14 @@ __global__ void __launch_bounds__(kPrepThreads, 4) k_delta_prep(DeltaChunkArgs c
 constexpr int kScanThreads = 512;
 constexpr int kScanW = 0;                               // [2] W, K, gates
 constexpr int kScanWBytes = 32768 + 16384 + 1024;
-constexpr int kScanQ = kScanW + 2 * kScanWBytes;        // [2] Q, M
-constexpr int kScanQBytes = 16384 + 8192;
+constexpr int kScanQ = kScanW + 2 * kScanWBytes;        // [2] Q, M, the gates again (the outputs' warps read them late)
+constexpr int kScanQBytes = 16384 + 8192 + 1024;
 constexpr int kScanT = kScanQ + 2 * kScanQBytes;        // T, V
 constexpr int kScanTBytes = 24576 + 16384;
-constexpr int kScanOut = kScanT + kScanTBytes;          // outputs on their way: 4 KB a warp
-constexpr int kScanBars = kScanOut + 16384;
+constexpr int kScanBars = kScanT + kScanTBytes;
 constexpr int kScanSmemBytes = kScanBars + 5120;
 static_assert(kScanSmemBytes <= 232448, "shared memory per CTA");
-static_assert(kScanWBytes % 1024 == 0 && kScanTBytes % 1024 == 0, "tiles on 1 KB boundaries");
+static_assert(kScanWBytes % 1024 == 0 && kScanQBytes % 1024 == 0 && kScanTBytes % 1024 == 0, "tiles on 1 KB boundaries");
 
 // what a launch does: the whole walk; or, for a sequence cut into segments, their states from
 // zero and their transitions (pass 0), then the outputs from the joined states (pass 1)
@@ -759,7 +758,13 @@ __device__ __forceinline__ void tmem_ld16_at(uint32_t taddr, float* f) {
   for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(r[i]);
 }
 
-__global__ void __launch_bounds__(kScanThreads, 1) k_delta_scan(DeltaChunkArgs ca, int mode) {
+// K and V as [tokens][heads][128], boxes of 64 tokens x 64 columns of one head
+struct ScanMaps {
+  CUtensorMap k, v;
+};
+
+__global__ void __launch_bounds__(kScanThreads, 1)
+    k_delta_scan(const __grid_constant__ ScanMaps maps, DeltaChunkArgs ca, int mode) {
   extern __shared__ __align__(1024) unsigned char smem[];
   ScanBars& B = *reinterpret_cast<ScanBars*>(smem + kScanBars);
   const DeltaArgs& a = ca.d;
@@ -801,9 +806,9 @@ __global__ void __launch_bounds__(kScanThreads, 1) k_delta_scan(DeltaChunkArgs c
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&B.full_w[i], 2);
-      mbar_init(&B.empty_w[i], 1 + 8 + (outputs ? 4 : 0));
+      mbar_init(&B.empty_w[i], 1 + 8);
       mbar_init(&B.full_q[i], 1);
-      mbar_init(&B.empty_q[i], 1);
+      mbar_init(&B.empty_q[i], 1 + 4);
     }
     mbar_init(&B.full_t, 2);
     mbar_init(&B.empty_t, 1);
@@ -830,15 +835,15 @@ __global__ void __launch_bounds__(kScanThreads, 1) k_delta_scan(DeltaChunkArgs c
   tc_fence_after();
   // all 512 columns are this CTA's, so they start at 0: addresses are known to the compiler
   constexpr uint32_t tm = 0;
-  // columns: S hi 64, S lo 64, D_S 128, D_T 64, D_W 64 (then U' mid and lo, each half of the
-  // threads in the columns that it has read), D_Q 64, U' hi 32, U 32
-  constexpr uint32_t tS = tm, tDS = tm + 128, tDT = tm + 256, tDW = tm + 320, tDQ = tm + 384,
-                     tUw = tm + 448, tU = tm + 480;
+  // columns: S hi 64, S lo 64, D_S 128, D_T 2 x 64 (by the parity of the chunk; each half of the
+  // threads then puts U' hi and U into the columns that it has read), D_W 64 (then U' mid and lo,
+  // the same way), D_Q 64
+  constexpr uint32_t tS = tm, tDS = tm + 128, tDT = tm + 256, tDW = tm + 384, tDQ = tm + 448;
   volatile int* abort = &B.abort;
   const DevStatus st = ca.st;
 
   if (warp < 8) {
-    regs_raise<168>();
+    regs_raise<152>();
     // ---- the state: lane = value row v, 64 columns d of it -----------------------------------
     const int half = warp >> 2, v = 32 * (warp & 3) + lane;
     const uint32_t lb = static_cast<uint32_t>(32 * (warp & 3)) << 16;
@@ -905,11 +910,12 @@ __global__ void __launch_bounds__(kScanThreads, 1) k_delta_scan(DeltaChunkArgs c
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
       const float winv = inv * gate[kGateW];
+      const uint32_t dt = tDT + 64 * sg + lb + 32 * half;
       float u[32];
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
         uint32_t x[16], y[16];
-        if (!trans) tmem_ld16(tDT + lb + 32 * half + 16 * g, x);
+        if (!trans) tmem_ld16(dt + 16 * g, x);
         tmem_ld16(tDW + lb + 32 * half + 16 * g, y);
         tmem_wait_ld();
         reg_fence16(x);
@@ -926,8 +932,8 @@ __global__ void __launch_bounds__(kScanThreads, 1) k_delta_scan(DeltaChunkArgs c
           split3_bf16x2(w.x * p[0], w.y * p[1], &vh[2 * i], &vm[2 * i], &vl[2 * i]);
           split3_bf16x2(w.z * p[2], w.w * p[3], &vh[2 * i + 1], &vm[2 * i + 1], &vl[2 * i + 1]);
         }
-        // mid and lo take the columns of D_W that were just read
-        tmem_st8(tUw + lb + 16 * half + 8 * g, vh);
+        // hi takes columns of D_T, mid and lo those of D_W that were just read
+        tmem_st8(dt + 16 * g, vh);
         tmem_st8(tDW + lb + 32 * half + 16 * g, vm);
         tmem_st8(tDW + lb + 32 * half + 16 * g + 8, vl);
         signal(&B.uw_part[g]);
@@ -950,7 +956,8 @@ __global__ void __launch_bounds__(kScanThreads, 1) k_delta_scan(DeltaChunkArgs c
 #pragma unroll
         for (int i = 0; i < 16; ++i) w[i] = pack_f16x2(su * u[2 * i], su * u[2 * i + 1]);
         if (half == 0) B.uscale[c & 1][v] = iu;
-        tmem_st16(tU + lb + 16 * half, w);
+        tmem_st8(dt + 8, w);
+        tmem_st8(dt + 24, w + 8);
         signal(&B.u_full);
       }
       ok = mbar_wait(&B.ds, c & 1, abort, st, 332);
@@ -979,16 +986,17 @@ __global__ void __launch_bounds__(kScanThreads, 1) k_delta_scan(DeltaChunkArgs c
         p[i] = make_float4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]);
     }
   } else if (warp < 12) {
-    regs_lower<112>();
+    regs_raise<144>();
     // ---- outputs: lane = value v, 64 tokens --------------------------------------------------
     if (outputs) {
       const int v = 32 * (warp - 8) + lane;
       const uint32_t lb = static_cast<uint32_t>(32 * (warp - 8)) << 16;
-      unsigned char* mine = smem + kScanOut + 4096 * (warp - 8);   // [64 t][32 v] bf16
+      const int64_t step = static_cast<int64_t>(a.heads) * kGdnDim;
+      const uint32_t sel = (lane & 1) ? 0x3276 : 0x5410;
       for (int c = 0; c < nc; ++c) {
         const int sg = c & 1;
-        const float4* eg = reinterpret_cast<const float4*>(smem + kScanW + sg * kScanWBytes + 49152) + kGateQ / 4;
-        bool ok = mbar_wait(&B.full_w[sg], (c >> 1) & 1, abort, st, 333) &&
+        const float4* eg = reinterpret_cast<const float4*>(smem + kScanQ + sg * kScanQBytes + 24576) + kGateQ / 4;
+        bool ok = mbar_wait(&B.full_q[sg], (c >> 1) & 1, abort, st, 333) &&
                   mbar_wait(&B.qs, c & 1, abort, st, 334);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
@@ -1014,39 +1022,34 @@ __global__ void __launch_bounds__(kScanThreads, 1) k_delta_scan(DeltaChunkArgs c
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
         const float iu = B.uscale[c & 1][v];
+        const int64_t left = ntok - static_cast<int64_t>(c) * kGdnChunk;
+        const int n = static_cast<int>(left < kGdnChunk ? left : kGdnChunk);
+        // lanes in pairs: the even one stores both its own and its neighbour's value of token t,
+        // the odd one of token t + 1
+        __nv_bfloat16* op = a.out + ((t0 + static_cast<int64_t>(c) * kGdnChunk + (lane & 1)) * a.heads + h) * kGdnDim +
+                            32 * (warp - 8) + (lane & ~1);
 #pragma unroll
         for (int i0 = 0; i0 < 64; i0 += 16) {
           float x[16];
           tmem_ld16_at(tDQ + lb + i0, x);
+          if (i0 == 48) {   // all of D_Q has been read
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&B.o_free);
+          }
 #pragma unroll
           for (int i = 0; i < 16; i += 2) {
             const float2 e = *reinterpret_cast<const float2*>(reinterpret_cast<const float*>(gm) + i0 + i);
             const uint32_t w = pack_bf16x2(fmaf(iu * e.x, x[i], y[i0 + i]),
                                            fmaf(iu * e.y, x[i + 1], y[i0 + i + 1]));
-            *reinterpret_cast<uint16_t*>(mine + 64 * (i0 + i) + 2 * lane) = static_cast<uint16_t>(w);
-            *reinterpret_cast<uint16_t*>(mine + 64 * (i0 + i + 1) + 2 * lane) = static_cast<uint16_t>(w >> 16);
+            const uint32_t z = __shfl_xor_sync(0xffffffffu, w, 1);
+            const uint32_t both = __byte_perm(w, z, sel);
+            if (i0 + i + (lane & 1) < n) *reinterpret_cast<uint32_t*>(op) = both;
+            op += 2 * step;
           }
         }
-        tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&B.o_free);
-          mbar_arrive(&B.empty_w[sg]);
-        }
-        const int64_t left = ntok - static_cast<int64_t>(c) * kGdnChunk;
-        const int n = static_cast<int>(left < kGdnChunk ? left : kGdnChunk);
-        const int64_t step = static_cast<int64_t>(a.heads) * kGdnDim;
-        // four lanes to a token: its 32 values as 16-byte words
-        __nv_bfloat16* op = a.out + ((t0 + static_cast<int64_t>(c) * kGdnChunk) * a.heads + h) * kGdnDim +
-                            32 * (warp - 8) + 8 * (lane & 3);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int t = 8 * i + (lane >> 2);
-          if (t < n)
-            *reinterpret_cast<uint4*>(op + t * step) =
-                *reinterpret_cast<const uint4*>(mine + 64 * t + 16 * (lane & 3));
-        }
-        __syncwarp();   // the next chunk overwrites `mine`
+        if (lane == 0) mbar_arrive(&B.empty_q[sg]);
       }
     }
   } else {
@@ -1067,7 +1070,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) k_delta_scan(DeltaChunkArgs c
         for (int p = 0; p < 3; ++p)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            umma_ss(tDT, dm + ((kScanT + 24576 + 2048 * k) >> 4), dk + ((kScanT + 8192 * p + 32 * k) >> 4),
+            umma_ss(tDT + 64 * (c & 1), dm + ((kScanT + 24576 + 2048 * k) >> 4), dk + ((kScanT + 8192 * p + 32 * k) >> 4),
                     kIdTV, p + k > 0 ? 1u : 0u);
         umma_commit(&B.empty_t);
       }
@@ -1111,8 +1114,10 @@ __global__ void __launch_bounds__(kScanThreads, 1) k_delta_scan(DeltaChunkArgs c
         }
         __syncwarp();
       }
-      // D_S = U'^T K: hi, mid, lo of 16 tokens of each half at a time (mid and lo at 16-column
-      // strides)
+      // the next chunk's V^T T^T while U is formed (its columns are free: what the last chunk put
+      // there has been used, since its outputs and this chunk's S are there)
+      if (!trans && c + 1 < nc && !write_values(c + 1)) break;
+      // D_S = U'^T K: hi, mid, lo of 16 tokens of each half at a time
       for (int g = 0; g < 2 && ok; ++g) {
         ok = mbar_wait(&B.uw_part[g], c & 1, abort, st, 345);
         if (!ok) break;
@@ -1123,7 +1128,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) k_delta_scan(DeltaChunkArgs c
 #pragma unroll
             for (int kh = 0; kh < 2; ++kh) {
               const int k = g + 2 * kh;
-              umma_ts(tDS, p == 0 ? tUw + 8 * k : tDW + 16 * k + 8 * (p - 1),
+              umma_ts(tDS, p == 0 ? tDT + 64 * sg + 16 * k : tDW + 16 * k + 8 * (p - 1),
                       dm + sw + ((32768 + 2048 * k) >> 4), kIdDS, (g > 0 || p + kh > 0) ? 1u : 0u);
             }
           if (g == 1) {
@@ -1142,13 +1147,12 @@ __global__ void __launch_bounds__(kScanThreads, 1) k_delta_scan(DeltaChunkArgs c
           // D_Q = U^T M^T
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            umma_ts(tDQ, tU + 8 * k, dk + sq + ((16384 + 32 * k) >> 4), kIdF16, k > 0 ? 1u : 0u);
+            umma_ts(tDQ, tDT + 64 * sg + 16 * k + 8, dk + sq + ((16384 + 32 * k) >> 4), kIdF16, k > 0 ? 1u : 0u);
           umma_commit(&B.o);
           umma_commit(&B.empty_q[sg]);
         }
         __syncwarp();
       }
-      if (!trans && c + 1 < nc && !write_values(c + 1)) break;
     }
     __syncwarp();
     if (elect_one()) umma_commit(&B.mma_done);
@@ -1168,37 +1172,49 @@ __global__ void __launch_bounds__(kScanThreads, 1) k_delta_scan(DeltaChunkArgs c
       const bool ok = turn == 0 || mbar_wait(&empty[sg], (turn & 1) ^ 1, abort, st, 347);
       if (!__all_sync(0xffffffffu, ok)) break;
       unsigned char* stage = smem + (who == 0 ? kScanW + sg * kScanWBytes : who == 1 ? kScanT : kScanQ + sg * kScanQBytes);
+      const int64_t left = ntok - static_cast<int64_t>(c) * kGdnChunk;
+      const int n = static_cast<int>(left < kGdnChunk ? left : kGdnChunk);
+      const bool whole = n == kGdnChunk;
+      unsigned char* rows = stage + (who == 0 ? 32768 : 24576);   // K or V
       if (lane == 0) {
         const unsigned char* rec = ca.rec + ((rec0 + c0 + c) * ca.nheads + hl) * static_cast<int64_t>(kRecBytes);
         if (who == 0) {
-          mbar_arrive_expect_tx(&full[sg], 32768 + 1024);
+          mbar_arrive_expect_tx(&full[sg], 32768 + 1024 + (whole ? 16384 : 0));
           bulk_load(stage, rec + kRecW, 32768, &full[sg]);
           bulk_load(stage + 49152, rec + kRecGate, 1024, &full[sg]);
         } else if (who == 1) {
-          mbar_arrive_expect_tx(&full[sg], 24576);
+          mbar_arrive_expect_tx(&full[sg], 24576 + (whole ? 16384 : 0));
           bulk_load(stage, rec + kRecT, 24576, &full[sg]);
         } else {
-          mbar_arrive_expect_tx(&full[sg], 24576);
+          mbar_arrive_expect_tx(&full[sg], kScanQBytes);
           bulk_load(stage, rec + kRecQ, 16384, &full[sg]);
           bulk_load(stage + 16384, rec + kRecM, 8192, &full[sg]);
+          bulk_load(stage + 24576, rec + kRecGate, 1024, &full[sg]);
+        }
+        if (who < 2 && whole) {
+          const CUtensorMap* m = who == 0 ? &maps.k : &maps.v;
+          const int hh = who == 0 ? h / (a.heads / a.key_heads) : h;
+          const int tt = static_cast<int>(t0 + static_cast<int64_t>(c) * kGdnChunk);
+          tma_load_3d(rows, m, 0, hh, tt, &full[sg]);
+          tma_load_3d(rows + 8192, m, 64, hh, tt, &full[sg]);
         }
       }
       __syncwarp();
       ++issued;
       if (who < 2) {
-        const int64_t left = ntok - static_cast<int64_t>(c) * kGdnChunk;
-        const int n = static_cast<int>(left < kGdnChunk ? left : kGdnChunk);
-        const uint32_t to = smem_u32(stage) + (who == 0 ? 32768 : 24576);
-        const __nv_bfloat16* from = base + (t0 + static_cast<int64_t>(c) * kGdnChunk) * step;
-#pragma unroll 8
-        for (int e = lane; e < kGdnChunk * 16; e += 32) {
-          const int t = e >> 4, w = e & 15;
-          cp_async16(to + 8192 * (w >> 3) + tile_byte(t, 8 * (w & 7)),
-                     from + (t < n ? t : 0) * step + 8 * w, t < n);
+        if (!whole) {   // the rows behind the sequence's last token must be zero
+          const uint32_t to = smem_u32(rows);
+          const __nv_bfloat16* from = base + (t0 + static_cast<int64_t>(c) * kGdnChunk) * step;
+#pragma unroll 4
+          for (int e = lane; e < kGdnChunk * 16; e += 32) {
+            const int t = e >> 4, w = e & 15;
+            cp_async16(to + 8192 * (w >> 3) + tile_byte(t, 8 * (w & 7)),
+                       from + (t < n ? t : 0) * step + 8 * w, t < n);
+          }
+          cp_async_wait_all();
+          fence_proxy_async_smem();
+          __syncwarp();
         }
-        cp_async_wait_all();
-        fence_proxy_async_smem();
-        __syncwarp();
         if (lane == 0) mbar_arrive(&full[sg]);
       }
     }
