@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) k_delta_prep(DeltaChunkArgs c
       for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
     const uint32_t ap = isq ? sq : sk;
     const int ar = 16 * rb + (lane & 15), ac = 8 * (lane >> 4), br = lane & 7, bc = 8 * (lane >> 3);
-#pragma unroll
+#pragma unroll 1
     for (int k0 = 0; k0 < kGdnDim; k0 += 32) {
       const uint32_t panel = 8192 * (k0 >> 6);
       uint32_t fa[2][4];
@@ -633,9 +633,9 @@ __global__ void __launch_bounds__(kPrepThreads, 4) k_delta_prep(DeltaChunkArgs c
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
   const uint32_t wk = sk + 8192 * (warp >> 2);
-#pragma unroll
-  for (int ks = 0; ks < 4; ++ks) {
-    if (ks <= rb) {
+#pragma unroll 1
+  for (int ks = 0; ks <= rb; ++ks) {
+    {
       uint32_t fh[4], fm[4], fl[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -758,6 +758,21 @@ __device__ __forceinline__ void tmem_ld16_at(uint32_t taddr, float* f) {
   for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(r[i]);
 }
 
+// Bounded wait for the phase of the given parity.  Each try waits in hardware for a while; past
+// the limit (seconds) the site is noted for the CTA's other waits, which then give up too, and
+// for the status that the kernel reports at its end.  Small, since the kernel's loop has to stay
+// in the instruction cache.
+constexpr uint32_t kScanTries = 1u << 26;
+__device__ __forceinline__ bool scan_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                          int site) {
+  if (mbar_try_wait(bar, parity)) return true;
+#pragma unroll 1
+  for (uint32_t i = 0; i < kScanTries && *abort == 0; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  if (*abort == 0) *abort = site;
+  return false;
+}
+
 // K and V as [tokens][heads][128], boxes of 64 tokens x 64 columns of one head
 struct ScanMaps {
   CUtensorMap k, v;
@@ -840,10 +855,9 @@ __global__ void __launch_bounds__(kScanThreads, 1)
   // the same way), D_Q 64
   constexpr uint32_t tS = tm, tDS = tm + 128, tDT = tm + 256, tDW = tm + 384, tDQ = tm + 448;
   volatile int* abort = &B.abort;
-  const DevStatus st = ca.st;
 
   if (warp < 8) {
-    regs_raise<152>();
+    regs_raise<168>();
     // ---- the state: lane = value row v, 64 columns d of it -----------------------------------
     const int half = warp >> 2, v = 32 * (warp & 3) + lane;
     const uint32_t lb = static_cast<uint32_t>(32 * (warp & 3)) << 16;
@@ -875,108 +889,113 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     auto joined = [&](int phase) -> bool {   // the maxima of both halves of the rows are in place
       __syncwarp();
       if (lane == 0) mbar_arrive(&B.rows[warp & 3]);
-      return __all_sync(0xffffffffu, mbar_wait(&B.rows[warp & 3], phase & 1, abort, st, 337));
+      return __all_sync(0xffffffffu, scan_wait(&B.rows[warp & 3], phase & 1, abort, 337));
     };
-    auto put_part = [&](int g, float sc) {   // columns 16 g .. of this half, as fp16 parts
-      uint32_t vh[8], vl[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        split_f16x2(sc * s[16 * g + 2 * i], sc * s[16 * g + 2 * i + 1], &vh[i], &vl[i]);
-      tmem_st8(tS + lb + 32 * half + 8 * g, vh);
-      tmem_st8(tS + lb + 64 + 32 * half + 8 * g, vl);
-      signal(&B.s_part[g]);
-    };
-    auto largest = [&]() -> float {
-      float m[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int i = 0; i < 64; ++i) m[i & 3] = fmaxf(m[i & 3], fabsf(s[i]));
-      return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
-    };
-    float smax = largest();
-    B.smax[half][v] = smax;
-    bool ok = joined(0);
-    float inv;   // 1 over the scale of this row
-    if (ok) {
-      const float sc = row_scale(fmaxf(smax, B.smax[half ^ 1][v]), &inv);
-      if (half == 0) B.scale[0][v] = inv;
-#pragma unroll
-      for (int g = 0; g < 4; ++g) put_part(g, sc);
-    }
-    for (int c = 0; ok && c < nc; ++c) {
+    bool ok = true;
+    float inv = 1.f, smax = 0.f;   // 1 over the scale of this row of S; its largest entry (half)
+    // turn c: S0 of chunk c into U, then into S, which goes over as the S0 of chunk c + 1; turn -1
+    // only hands the first one over
+#pragma unroll 1
+    for (int c = -1; c < nc; ++c) {
       const int sg = c & 1;
-      const float* gate = reinterpret_cast<const float*>(smem + kScanW + sg * kScanWBytes + 49152);
-      ok = mbar_wait(&B.full_w[sg], (c >> 1) & 1, abort, st, 330) &&
-           mbar_wait(&B.d1, c & 1, abort, st, 331);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      tc_fence_after();
-      const float winv = inv * gate[kGateW];
-      const uint32_t dt = tDT + 64 * sg + lb + 32 * half;
-      float u[32];
+      const bool first = c < 0, more = c + 1 < nc;
+      {
+        float m[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        uint32_t x[16], y[16];
-        if (!trans) tmem_ld16(dt + 16 * g, x);
-        tmem_ld16(tDW + lb + 32 * half + 16 * g, y);
-        tmem_wait_ld();
-        reg_fence16(x);
-        reg_fence16(y);
-        uint32_t vh[8], vm[8], vl[8];
-        const float4* wk = reinterpret_cast<const float4*>(gate + kGateU + 32 * half + 16 * g);
+        for (int i = 0; i < 64; ++i) m[i & 3] = fmaxf(m[i & 3], fabsf(s[i]));
+        smax = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+      }
+      float gc = 1.f, sc = 1.f;
+      if (!first) {
+        const float* gate = reinterpret_cast<const float*>(smem + kScanW + sg * kScanWBytes + 49152);
+        ok = scan_wait(&B.full_w[sg], (c >> 1) & 1, abort, 330) &&
+             scan_wait(&B.d1, c & 1, abort, 331);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc_fence_after();
+        const float winv = inv * gate[kGateW];
+        const uint32_t dt = tDT + 64 * sg + lb + 32 * half;
+        float u[32];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float4 w = wk[i];
-          float* p = u + 16 * g + 4 * i;
+        for (int g = 0; g < 2; ++g) {
+          uint32_t x[16], y[16];
+          if (!trans) tmem_ld16(dt + 16 * g, x);
+          tmem_ld16(tDW + lb + 32 * half + 16 * g, y);
+          tmem_wait_ld();
+          reg_fence16(x);
+          reg_fence16(y);
+          uint32_t vh[8], vm[8], vl[8];
+          const float4* wk = reinterpret_cast<const float4*>(gate + kGateU + 32 * half + 16 * g);
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            p[e] = fmaf(winv, __uint_as_float(y[4 * i + e]), trans ? 0.f : __uint_as_float(x[4 * i + e]));
-          split3_bf16x2(w.x * p[0], w.y * p[1], &vh[2 * i], &vm[2 * i], &vl[2 * i]);
-          split3_bf16x2(w.z * p[2], w.w * p[3], &vh[2 * i + 1], &vm[2 * i + 1], &vl[2 * i + 1]);
+          for (int i = 0; i < 4; ++i) {
+            const float4 w = wk[i];
+            float* p = u + 16 * g + 4 * i;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              p[e] = fmaf(winv, __uint_as_float(y[4 * i + e]), trans ? 0.f : __uint_as_float(x[4 * i + e]));
+            split3_bf16x2(w.x * p[0], w.y * p[1], &vh[2 * i], &vm[2 * i], &vl[2 * i]);
+            split3_bf16x2(w.z * p[2], w.w * p[3], &vh[2 * i + 1], &vm[2 * i + 1], &vl[2 * i + 1]);
+          }
+          // hi takes columns of D_T, mid and lo those of D_W that were just read
+          tmem_st8(dt + 16 * g, vh);
+          tmem_st8(tDW + lb + 32 * half + 16 * g, vm);
+          tmem_st8(tDW + lb + 32 * half + 16 * g + 8, vl);
+          signal(&B.uw_part[g]);
         }
-        // hi takes columns of D_T, mid and lo those of D_W that were just read
-        tmem_st8(dt + 16 * g, vh);
-        tmem_st8(tDW + lb + 32 * half + 16 * g, vm);
-        tmem_st8(tDW + lb + 32 * half + 16 * g + 8, vl);
-        signal(&B.uw_part[g]);
-      }
-      float umax = 0.f;
+        float umax = 0.f;
 #pragma unroll
-      for (int i = 0; i < 32; ++i) umax = fmaxf(umax, fabsf(u[i]));
-      B.smax[half][v] = smax;
-      B.umax[half][v] = umax;
-      const float gc = gate[kGateC], kmax = gate[kGateK];
-      ok = joined(c + 1);
-      if (!ok) break;
-      if (lane == 0) mbar_arrive(&B.empty_w[sg]);
-      umax = fmaxf(umax, B.umax[half ^ 1][v]);
-      const float sc = row_scale(fmaf(gc, fmaxf(smax, B.smax[half ^ 1][v]), 64.f * kmax * umax), &inv);
-      if (outputs) {
-        float iu;
-        const float su = row_scale(umax, &iu);
-        uint32_t w[16];
+        for (int i = 0; i < 32; ++i) umax = fmaxf(umax, fabsf(u[i]));
+        B.smax[half][v] = smax;
+        B.umax[half][v] = umax;
+        gc = gate[kGateC];
+        const float kmax = gate[kGateK];
+        ok = joined(c + 1);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive(&B.empty_w[sg]);
+        umax = fmaxf(umax, B.umax[half ^ 1][v]);
+        sc = row_scale(fmaf(gc, fmaxf(smax, B.smax[half ^ 1][v]), 64.f * kmax * umax), &inv);
+        if (outputs) {
+          float iu;
+          const float su = row_scale(umax, &iu);
+          uint32_t w[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) w[i] = pack_f16x2(su * u[2 * i], su * u[2 * i + 1]);
-        if (half == 0) B.uscale[c & 1][v] = iu;
-        tmem_st8(dt + 8, w);
-        tmem_st8(dt + 24, w + 8);
-        signal(&B.u_full);
+          for (int i = 0; i < 16; ++i) w[i] = pack_f16x2(su * u[2 * i], su * u[2 * i + 1]);
+          if (half == 0) B.uscale[sg][v] = iu;
+          tmem_st8(dt + 8, w);
+          tmem_st8(dt + 24, w + 8);
+          signal(&B.u_full);
+        }
+        ok = scan_wait(&B.ds, c & 1, abort, 332);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc_fence_after();
+      } else {
+        B.smax[half][v] = smax;
+        ok = joined(0);
+        if (!ok) break;
+        sc = row_scale(fmaxf(smax, B.smax[half ^ 1][v]), &inv);
       }
-      ok = mbar_wait(&B.ds, c & 1, abort, st, 332);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      tc_fence_after();
-      const bool more = c + 1 < nc;
       if (more && half == 0) B.scale[(c + 1) & 1][v] = inv;
       uint32_t x[2][16];
-      tmem_ld16(tDS + lb + 64 * half, x[0]);
+      if (!first) tmem_ld16(tDS + lb + 64 * half, x[0]);
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
-        tmem_wait_ld();
-        reg_fence16(x[g & 1]);
-        if (g < 3) tmem_ld16(tDS + lb + 64 * half + 16 * (g + 1), x[(g + 1) & 1]);
+        if (!first) {
+          tmem_wait_ld();
+          reg_fence16(x[g & 1]);
+          if (g < 3) tmem_ld16(tDS + lb + 64 * half + 16 * (g + 1), x[(g + 1) & 1]);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) s[16 * g + i] = fmaf(gc, s[16 * g + i], __uint_as_float(x[g & 1][i]));
-        if (more) put_part(g, sc);
+          for (int i = 0; i < 16; ++i)
+            s[16 * g + i] = fmaf(gc, s[16 * g + i], __uint_as_float(x[g & 1][i]));
+        }
+        if (more) {   // columns 16 g .. of this half, as fp16 parts
+          uint32_t vh[8], vl[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            split_f16x2(sc * s[16 * g + 2 * i], sc * s[16 * g + 2 * i + 1], &vh[i], &vl[i]);
+          tmem_st8(tS + lb + 32 * half + 8 * g, vh);
+          tmem_st8(tS + lb + 64 + 32 * half + 8 * g, vl);
+          signal(&B.s_part[g]);
+        }
       }
-      smax = largest();
     }
     // in the outputs pass the joined states hold what the inner segments would write
     if (__all_sync(0xffffffffu, ok) && (mode == kScanEnds || last)) {
@@ -986,7 +1005,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
         p[i] = make_float4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]);
     }
   } else if (warp < 12) {
-    regs_raise<144>();
+    regs_raise<136>();
     // ---- outputs: lane = value v, 64 tokens --------------------------------------------------
     if (outputs) {
       const int v = 32 * (warp - 8) + lane;
@@ -996,8 +1015,8 @@ __global__ void __launch_bounds__(kScanThreads, 1)
       for (int c = 0; c < nc; ++c) {
         const int sg = c & 1;
         const float4* eg = reinterpret_cast<const float4*>(smem + kScanQ + sg * kScanQBytes + 24576) + kGateQ / 4;
-        bool ok = mbar_wait(&B.full_q[sg], (c >> 1) & 1, abort, st, 333) &&
-                  mbar_wait(&B.qs, c & 1, abort, st, 334);
+        bool ok = scan_wait(&B.full_q[sg], (c >> 1) & 1, abort, 333) &&
+                  scan_wait(&B.qs, c & 1, abort, 334);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
         const float inv = B.scale[c & 1][v];
@@ -1018,7 +1037,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&B.q_free);
-        ok = mbar_wait(&B.o, c & 1, abort, st, 335);
+        ok = scan_wait(&B.o, c & 1, abort, 335);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
         const float iu = B.uscale[c & 1][v];
@@ -1053,84 +1072,95 @@ __global__ void __launch_bounds__(kScanThreads, 1)
       }
     }
   } else {
-    regs_lower<64>();
+    regs_lower<40>();
     if (warp == 12) {
     // ---- products: the whole warp walks the loop, one elected lane issues ----------------------
     constexpr uint32_t kIdTV = idesc_bf16_f32(128, 64, 1, 0);   // A = V, tokens along its rows
     constexpr uint32_t kIdF16 = idesc_f16_f32(128, 64, 0, 0);
     constexpr uint32_t kIdDS = idesc_bf16_f32(128, 128, 0, 1);  // B = K, tokens along its rows
-    // descriptors; a step along a tile adds its bytes / 16
+    // Descriptors; a step along a tile adds its bytes / 16.  The loops stay loops: unrolled, this
+    // warp alone would fill the instruction cache.
     const uint64_t dk = smem_desc_sw128(smem_u32(smem), 0, 1024);        // rows of 128 bytes
     const uint64_t dm = smem_desc_sw128(smem_u32(smem), 8192, 1024);     // two column panels
-    auto write_values = [&](int c) -> bool {   // D_T = V^T T^T
-      if (!mbar_wait(&B.full_t, c & 1, abort, st, 340)) return false;
-      tc_fence_after();
-      if (elect_one()) {
-#pragma unroll
-        for (int p = 0; p < 3; ++p)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            umma_ss(tDT + 64 * (c & 1), dm + ((kScanT + 24576 + 2048 * k) >> 4), dk + ((kScanT + 8192 * p + 32 * k) >> 4),
-                    kIdTV, p + k > 0 ? 1u : 0u);
-        umma_commit(&B.empty_t);
-      }
-      __syncwarp();
-      return true;
-    };
-    bool ok = trans || write_values(0);
-    for (int c = 0; ok && c < nc; ++c) {
+    bool ok = true;
+    // turn c: the products of chunk c, then V^T T^T of chunk c + 1; turn -1 only the latter
+#pragma unroll 1
+    for (int c = -1; c < nc; ++c) {
       const int sg = c & 1;
       const uint32_t ph = (c >> 1) & 1;
       const uint64_t sw = (kScanW + sg * kScanWBytes) >> 4, sq = (kScanQ + sg * kScanQBytes) >> 4;
-      if (!mbar_wait(&B.full_w[sg], ph, abort, st, 342)) break;
-      // D_W = -S0 W^T: (hi, hi), (lo, hi), (hi, lo) of 16 columns of each half at a time
-      for (int g = 0; g < 4 && ok; ++g) {
-        ok = mbar_wait(&B.s_part[g], c & 1, abort, st, 341);
-        if (!ok) break;
-        tc_fence_after();
-        if (elect_one()) {
-#pragma unroll
-          for (int p = 0; p < 3; ++p)
-#pragma unroll
-            for (int kh = 0; kh < 2; ++kh)
-              umma_ts(tDW, tS + (p == 1 ? 64 : 0) + 32 * kh + 8 * g,
-                      dk + sw + (((p == 2 ? 16384 : 0) + 8192 * kh + 32 * g) >> 4), kIdF16,
-                      (g > 0 || p + kh > 0) ? 1u : 0u);
-          if (g == 3) umma_commit(&B.d1);   // covers D_T too
-        }
-        __syncwarp();
-      }
-      if (!ok) break;
-      if (outputs) {
-        if (!mbar_wait(&B.full_q[sg], ph, abort, st, 343)) break;
-        if (c > 0 && !mbar_wait(&B.o_free, (c - 1) & 1, abort, st, 344)) break;
-        tc_fence_after();
-        if (elect_one()) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            umma_ts(tDQ, tS + 8 * k, dk + sq + ((8192 * (k >> 2) + 32 * (k & 3)) >> 4), kIdF16,
-                    k > 0 ? 1u : 0u);
-          umma_commit(&B.qs);
-        }
-        __syncwarp();
-      }
-      // the next chunk's V^T T^T while U is formed (its columns are free: what the last chunk put
-      // there has been used, since its outputs and this chunk's S are there)
-      if (!trans && c + 1 < nc && !write_values(c + 1)) break;
-      // D_S = U'^T K: hi, mid, lo of 16 tokens of each half at a time
-      for (int g = 0; g < 2 && ok; ++g) {
-        ok = mbar_wait(&B.uw_part[g], c & 1, abort, st, 345);
-        if (!ok) break;
-        tc_fence_after();
-        if (elect_one()) {
-#pragma unroll
-          for (int p = 0; p < 3; ++p)
+      const uint32_t td = tDT + 64 * sg;
+      if (c >= 0) {
+        if (!scan_wait(&B.full_w[sg], ph, abort, 342)) break;
+        // D_W = -S0 W^T: (hi, hi), (lo, hi), (hi, lo) of 16 columns of each half at a time
+#pragma unroll 1
+        for (int g = 0; g < 4; ++g) {
+          ok = scan_wait(&B.s_part[g], c & 1, abort, 341);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t dw = dk + sw + 2 * g;
+            const uint32_t ts = tS + 8 * g;
 #pragma unroll
             for (int kh = 0; kh < 2; ++kh) {
-              const int k = g + 2 * kh;
-              umma_ts(tDS, p == 0 ? tDT + 64 * sg + 16 * k : tDW + 16 * k + 8 * (p - 1),
-                      dm + sw + ((32768 + 2048 * k) >> 4), kIdDS, (g > 0 || p + kh > 0) ? 1u : 0u);
+              umma_ts(tDW, ts + 32 * kh, dw + 512 * kh, kIdF16, g + kh > 0 ? 1u : 0u);
+              umma_ts(tDW, ts + 64 + 32 * kh, dw + 512 * kh, kIdF16, 1u);
+              umma_ts(tDW, ts + 32 * kh, dw + 1024 + 512 * kh, kIdF16, 1u);
             }
+            if (g == 3) umma_commit(&B.d1);   // covers D_T too
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (outputs) {
+          if (!scan_wait(&B.full_q[sg], ph, abort, 343)) break;
+          if (c > 0 && !scan_wait(&B.o_free, (c - 1) & 1, abort, 344)) break;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+              for (int kh = 0; kh < 2; ++kh)
+                umma_ts(tDQ, tS + 32 * kh + 8 * k, dk + sq + 512 * kh + 2 * k, kIdF16,
+                        k + kh > 0 ? 1u : 0u);
+            umma_commit(&B.qs);
+          }
+          __syncwarp();
+        }
+      }
+      // the next chunk's D_T = V^T T^T while U is formed (its columns are free: what the last chunk
+      // put there has been used, since its outputs and this chunk's S are there)
+      if (!trans && c + 1 < nc) {
+        if (!scan_wait(&B.full_t, (c + 1) & 1, abort, 340)) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t to = tDT + 64 * ((c + 1) & 1);
+#pragma unroll 1
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int p = 0; p < 3; ++p)
+              umma_ss(to, dm + ((kScanT + 24576) >> 4) + 128 * k, dk + (kScanT >> 4) + 512 * p + 2 * k,
+                      kIdTV, p + k > 0 ? 1u : 0u);
+          umma_commit(&B.empty_t);
+        }
+        __syncwarp();
+      }
+      if (c < 0) continue;
+      // D_S = U'^T K: hi, mid, lo of 16 tokens of each half at a time
+#pragma unroll 1
+      for (int g = 0; g < 2; ++g) {
+        ok = scan_wait(&B.uw_part[g], c & 1, abort, 345);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int kh = 0; kh < 2; ++kh) {
+            const uint32_t k = g + 2 * kh;
+            const uint64_t d = dm + sw + 2048 + 128 * k;
+            umma_ts(tDS, td + 16 * k, d, kIdDS, g + kh > 0 ? 1u : 0u);
+            umma_ts(tDS, tDW + 16 * k, d, kIdDS, 1u);
+            umma_ts(tDS, tDW + 16 * k + 8, d, kIdDS, 1u);
+          }
           if (g == 1) {
             umma_commit(&B.ds);
             umma_commit(&B.empty_w[sg]);
@@ -1140,14 +1170,14 @@ __global__ void __launch_bounds__(kScanThreads, 1)
       }
       if (!ok) break;
       if (outputs) {
-        if (!mbar_wait(&B.q_free, c & 1, abort, st, 346)) break;
-        if (!mbar_wait(&B.u_full, c & 1, abort, st, 348)) break;
+        if (!scan_wait(&B.q_free, c & 1, abort, 346)) break;
+        if (!scan_wait(&B.u_full, c & 1, abort, 348)) break;
         tc_fence_after();
         if (elect_one()) {
           // D_Q = U^T M^T
-#pragma unroll
+#pragma unroll 1
           for (int k = 0; k < 4; ++k)
-            umma_ts(tDQ, tDT + 64 * sg + 16 * k + 8, dk + sq + ((16384 + 32 * k) >> 4), kIdF16, k > 0 ? 1u : 0u);
+            umma_ts(tDQ, td + 16 * k + 8, dk + sq + 1024 + 2 * k, kIdF16, k > 0 ? 1u : 0u);
           umma_commit(&B.o);
           umma_commit(&B.empty_q[sg]);
         }
@@ -1169,7 +1199,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     int issued = 0;
     for (int c = 0; on && c < nc; ++c) {
       const int sg = c % stages, turn = c / stages;
-      const bool ok = turn == 0 || mbar_wait(&empty[sg], (turn & 1) ^ 1, abort, st, 347);
+      const bool ok = turn == 0 || scan_wait(&empty[sg], (turn & 1) ^ 1, abort, 347);
       if (!__all_sync(0xffffffffu, ok)) break;
       unsigned char* stage = smem + (who == 0 ? kScanW + sg * kScanWBytes : who == 1 ? kScanT : kScanQ + sg * kScanQBytes);
       const int64_t left = ntok - static_cast<int64_t>(c) * kGdnChunk;
@@ -1205,7 +1235,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
         if (!whole) {   // the rows behind the sequence's last token must be zero
           const uint32_t to = smem_u32(rows);
           const __nv_bfloat16* from = base + (t0 + static_cast<int64_t>(c) * kGdnChunk) * step;
-#pragma unroll 4
+#pragma unroll 1
           for (int e = lane; e < kGdnChunk * 16; e += 32) {
             const int t = e >> 4, w = e & 15;
             cp_async16(to + 8192 * (w >> 3) + tile_byte(t, 8 * (w & 7)),
@@ -1225,6 +1255,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (tid == 0 && *abort != 0) report_error(ca.st, kErrTimeout, *abort);
   if (warp == 12) {
     __syncwarp();
     tc_fence_after();
