@@ -1373,10 +1373,7 @@ extern "C" qsa_status qsa_gated_deltanet_extend(
     const uint64_t tok = static_cast<uint64_t>(a.d.tokens);
     const uint64_t kd[3] = {kGdnDim, static_cast<uint64_t>(key_heads), tok};
     const uint64_t ks[2] = {kGdnDim * 2, static_cast<uint64_t>(key_heads) * kGdnDim * 2};
-    const uint64_t vd[3] = {kGdnDim, static_cast<uint64_t>(heads), tok};
-    const uint64_t vs[2] = {kGdnDim * 2, static_cast<uint64_t>(heads) * kGdnDim * 2};
-    if (!make_tmap(&maps.k, k, 3, kd, ks, box) || !make_tmap(&maps.v, v, 3, vd, vs, box))
-      return QSA_ERR_CUDA;
+    if (!make_tmap(&maps.k, k, 3, kd, ks, box)) return QSA_ERR_CUDA;
   }
   const int prep_smem = static_cast<int>(sizeof(PrepSmem));
   if (!set_smem(k_delta_prep, prep_smem) || !set_smem(k_delta_scan, kScanSmemBytes))

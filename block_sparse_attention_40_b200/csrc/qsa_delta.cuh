@@ -190,12 +190,12 @@ __global__ void __launch_bounds__(kStepThreads) k_delta_step(DeltaArgs a) {
 
 // A record: operand tiles in the layout that the tensor core reads (rows of 128 bytes, 16-byte
 // words exchanged within 8 rows), then the gates.
-constexpr int kRecW = 0;                    // -W [64 t][128 d] fp16: hi (two 64-column panels), lo
-constexpr int kRecT = 32768;                // T [64 t][64 j] bf16: hi, mid, lo
-constexpr int kRecM = 57344;                // M [64 t][64 j] fp16, rows scaled
-constexpr int kRecQ = 65536;                // Q [64 t][128 d] fp16, rows scaled (two panels)
-constexpr int kRecGate = 81920;             // fp32 [256], as follows
-constexpr int kRecBytes = 82944;
+constexpr int kRecW = 0;                    // -W [64 t][128 d] fp16, two 64-column panels: hi, lo each
+constexpr int kRecU = 32768;                // T V [64 t][128 v] fp32
+constexpr int kRecM = 65536;                // M [64 t][64 j] fp16, rows scaled
+constexpr int kRecQ = 73728;                // Q [64 t][128 d] fp16, rows scaled (two panels)
+constexpr int kRecGate = 90112;             // fp32 [256], as follows
+constexpr int kRecBytes = 91136;
 constexpr int kGateQ = 0;                   // [64] e^g over the scale of the Q row
 constexpr int kGateU = 64;                  // [64] e^(g_C - g)
 constexpr int kGateC = 128;                 // e^(g_C)
@@ -311,9 +311,9 @@ __device__ __forceinline__ void bulk_store_wait() {
 }
 
 // ---- k_delta_prep: one CTA of 256 threads per (record, head) ---------------------------------
-// Bound by the latency of its steps, so four CTAs share an SM; the record leaves in pieces, each
-// by a bulk copy out of the space of an operand that is done with: Q becomes the scaled fp16 Q in
-// place, then holds M, then T hi and mid, then T lo; K and Tu become W.
+// Bound by its shared memory accesses and the latency of its steps, so four CTAs share an SM; the
+// record leaves in pieces, out of the space of an operand that is done with: Q becomes the scaled
+// fp16 Q in place, then holds M, then V; K and Tu become W.
 constexpr int kPrepThreads = 256;
 constexpr int kPrepLdA = kGdnChunk + 8;   // fp32 row stride of L / Tu: 8 rows x 4 pairs without conflicts
 struct PrepSmem {
@@ -564,96 +564,89 @@ __global__ void __launch_bounds__(kPrepThreads, 4) k_delta_prep(DeltaChunkArgs c
     if (lane == 0) S.kmax[warp - 2] = m;
   }
   __syncthreads();
+  // V in Q's and M's space (M has been read: the barrier)
+  for (int e = tid; e < kGdnChunk * 16; e += kPrepThreads) {
+    const int t = e >> 4, w = e & 15;
+    cp_async16(sq + 8192 * (w >> 3) + tile_byte(t, 8 * (w & 7)),
+               a.v + ((t0 + (t < n ? t : 0)) * a.heads + h) * kGdnDim + 8 * w, t < n);
+  }
   {
-    // four rows a warp, a column a lane; L21 T11 goes to the unused upper block
-    const int i0 = 4 * warp;
-    float y[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int k0 = 0; k0 < 32; k0 += 4) {
-      float t[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) t[k] = S.a[(k0 + k) * kPrepLdA + lane];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float4 l = *reinterpret_cast<const float4*>(&S.a[(32 + i0 + i) * kPrepLdA + k0]);
-        y[i] = fmaf(l.x, t[0], fmaf(l.y, t[1], fmaf(l.z, t[2], fmaf(l.w, t[3], y[i]))));
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) S.a[(i0 + i) * kPrepLdA + 32 + lane] = y[i];
-    __syncthreads();
-    float z[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int k0 = 0; k0 < 32; k0 += 4) {
-      float t[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) t[k] = S.a[(k0 + k) * kPrepLdA + 32 + lane];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float4 l = *reinterpret_cast<const float4*>(&S.a[(32 + i0 + i) * kPrepLdA + 32 + k0]);
-        z[i] = fmaf(l.x, t[0], fmaf(l.y, t[1], fmaf(l.z, t[2], fmaf(l.w, t[3], z[i]))));
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) S.a[(32 + i0 + i) * kPrepLdA + lane] = -z[i];
-  }
-  __syncthreads();
-  uint32_t t_lo[8];   // T lo of 16 columns of one row, until its space is free
-  const int tt = tid >> 2, tj = 16 * (tid & 3);
-  {
-    // T = Tu diag(beta)
-    const bool zero = tt < 32 && tj >= 32;
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      uint32_t vh[4], vm[4];
-#pragma unroll
-      for (int e = 0; e < 4; e += 2) {
-        const int j = tj + 8 * b + 2 * e;
-        float4 x = *reinterpret_cast<const float4*>(&S.a[tt * kPrepLdA + j]);
-        const float4 y = *reinterpret_cast<const float4*>(&S.beta[j]);
-        if (zero) x = make_float4(0.f, 0.f, 0.f, 0.f);
-        split3_bf16x2(x.x * y.x, x.y * y.y, &vh[e], &vm[e], &t_lo[4 * b + e]);
-        split3_bf16x2(x.z * y.z, x.w * y.w, &vh[e + 1], &vm[e + 1], &t_lo[4 * b + e + 1]);
-      }
-      const uint32_t at = tile_byte(tt, tj + 8 * b);
-      *reinterpret_cast<uint4*>(S.q + at) = make_uint4(vh[0], vh[1], vh[2], vh[3]);
-      *reinterpret_cast<uint4*>(S.q + 8192 + at) = make_uint4(vm[0], vm[1], vm[2], vm[3]);
-    }
-  }
-  fence_proxy_async_smem();
-  __syncthreads();
-  if (tid == 128) {
-    bulk_store(rec + kRecT, S.q, 16384);
-    bulk_store_wait();
-  }
-  __syncwarp();
-  // W = (Tu diag(beta e^g)) K: warp = 16 rows x 64 columns of K
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
-  const uint32_t wk = sk + 8192 * (warp >> 2);
+    // T21 = -T22 (L21 T11): two products of 32 x 32 x 32, a 16 x 8 tile a warp, operands in three
+    // bf16 parts; L21 T11 goes to the unused upper block
+    const int r0 = 16 * (warp & 1), c0 = 8 * (warp >> 1);
 #pragma unroll 1
-  for (int ks = 0; ks <= rb; ++ks) {
-    {
+    for (int step = 0; step < 2; ++step) {
+      const float* left = &S.a[(32 + r0) * kPrepLdA + (step ? 32 : 0)];
+      const float* right = &S.a[c0 + (step ? 32 : 0)];
+      float z[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k0 = 0; k0 < 32; k0 += 16) {
+        uint32_t x[3][4], y[3][2];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 v = *reinterpret_cast<const float2*>(
+              left + (gq + 8 * (e & 1)) * kPrepLdA + k0 + 2 * tq + 8 * (e >> 1));
+          split3_bf16x2(v.x, v.y, &x[0][e], &x[1][e], &x[2][e]);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float* p = right + (k0 + 2 * tq + 8 * e) * kPrepLdA + gq;
+          split3_bf16x2(p[0], p[kPrepLdA], &y[0][e], &y[1][e], &y[2][e]);
+        }
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+#pragma unroll
+          for (int j = 0; i + j < 3; ++j) delta_mma(z, x[i], y[j][0], y[j][1]);
+      }
+      const float sign = step ? -1.f : 1.f;
+      float* to = step ? &S.a[(32 + r0) * kPrepLdA + c0] : &S.a[r0 * kPrepLdA + 32 + c0];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        *reinterpret_cast<float2*>(to + (gq + 8 * i) * kPrepLdA + 2 * tq) =
+            make_float2(sign * z[2 * i], sign * z[2 * i + 1]);
+      if (!step) __syncthreads();
+    }
+  }
+  cp_async_wait_all();
+  __syncthreads();
+  // T V, T = Tu diag(beta), and then W = T diag(e^g) K: warp = 16 rows x 64 columns
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
+    const uint32_t src = (pass ? sk : sq) + 8192 * (warp >> 2);
+    const float* scale = pass ? S.beg : S.beta;
+#pragma unroll 1
+    for (int ks = 0; ks <= rb; ++ks) {
       uint32_t fh[4], fm[4], fl[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int t = (e & 1) ? tb : ta, j = 16 * ks + 2 * tq + 8 * (e >> 1);
         const float2 x = *reinterpret_cast<const float2*>(&S.a[t * kPrepLdA + j]);
-        const float2 y = *reinterpret_cast<const float2*>(&S.beg[j]);
+        const float2 y = *reinterpret_cast<const float2*>(&scale[j]);
         split3_bf16x2(x.x * y.x, x.y * y.y, &fh[e], &fm[e], &fl[e]);
       }
+      // rows 0..31 of Tu end at column 31: what lies beyond is L21 T11, which ks <= rb never reaches
 #pragma unroll
       for (int np = 0; np < 4; ++np) {
         uint32_t fb[4];
-        ldsm4_t(fb, wk + tile_byte(16 * ks + (lane & 15), 16 * np + 8 * (lane >> 4)));
+        ldsm4_t(fb, src + tile_byte(16 * ks + (lane & 15), 16 * np + 8 * (lane >> 4)));
         delta_mma(acc[2 * np], fh, fb[0], fb[1]);
         delta_mma(acc[2 * np + 1], fh, fb[2], fb[3]);
         delta_mma(acc[2 * np], fm, fb[0], fb[1]);
         delta_mma(acc[2 * np + 1], fm, fb[2], fb[3]);
         delta_mma(acc[2 * np], fl, fb[0], fb[1]);
         delta_mma(acc[2 * np + 1], fl, fb[2], fb[3]);
+      }
+    }
+    if (pass == 0) {
+      float* tv = reinterpret_cast<float*>(rec + kRecU) + 64 * (warp >> 2) + 2 * tq;
+#pragma unroll
+      for (int nt = 0; nt < 8; ++nt) {
+        *reinterpret_cast<float2*>(tv + ta * kGdnDim + 8 * nt) = make_float2(acc[nt][0], acc[nt][1]);
+        *reinterpret_cast<float2*>(tv + tb * kGdnDim + 8 * nt) = make_float2(acc[nt][2], acc[nt][3]);
       }
     }
   }
@@ -665,7 +658,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) k_delta_prep(DeltaChunkArgs c
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   if (lane == 0) S.wmax[warp] = m;
-  __syncthreads();   // also: K and Tu have been read, and T hi and mid are on their way
+  __syncthreads();   // also: K and Tu have been read
 #pragma unroll
   for (int i = 0; i < 8; ++i) m = fmaxf(m, S.wmax[i]);
   float inv_w;
@@ -674,27 +667,22 @@ __global__ void __launch_bounds__(kPrepThreads, 4) k_delta_prep(DeltaChunkArgs c
     gate[kGateK] = fmaxf(S.kmax[0], S.kmax[1]);
     gate[kGateW] = inv_w;
   }
-#pragma unroll
-  for (int b = 0; b < 2; ++b)
-    *reinterpret_cast<uint4*>(S.q + tile_byte(tt, tj + 8 * b)) =
-        make_uint4(t_lo[4 * b], t_lo[4 * b + 1], t_lo[4 * b + 2], t_lo[4 * b + 3]);
-  unsigned char* w = S.k + 8192 * (warp >> 2);   // on into Tu's space
+  unsigned char* w = S.k + 16384 * (warp >> 2);   // on into Tu's space
 #pragma unroll
   for (int nt = 0; nt < 8; ++nt) {
     uint32_t vh, vl;
     const int d = 8 * nt + 2 * tq;
     split_f16x2(sw * acc[nt][0], sw * acc[nt][1], &vh, &vl);
     *reinterpret_cast<uint32_t*>(w + tile_byte(ta, d)) = vh;
-    *reinterpret_cast<uint32_t*>(w + 16384 + tile_byte(ta, d)) = vl;
+    *reinterpret_cast<uint32_t*>(w + 8192 + tile_byte(ta, d)) = vl;
     split_f16x2(sw * acc[nt][2], sw * acc[nt][3], &vh, &vl);
     *reinterpret_cast<uint32_t*>(w + tile_byte(tb, d)) = vh;
-    *reinterpret_cast<uint32_t*>(w + 16384 + tile_byte(tb, d)) = vl;
+    *reinterpret_cast<uint32_t*>(w + 8192 + tile_byte(tb, d)) = vl;
   }
   fence_proxy_async_smem();
   __syncthreads();
   if (tid == 0) {
     bulk_store(rec + kRecW, S.k, 32768);
-    bulk_store(rec + kRecT + 16384, S.q, 8192);
     bulk_store(rec + kRecGate, S.gate, kRecBytes - kRecGate);
     bulk_store_wait();
   }
@@ -704,45 +692,61 @@ __global__ void __launch_bounds__(kPrepThreads, 4) k_delta_prep(DeltaChunkArgs c
 // With v along the 128 lanes of tensor memory, every operand that depends on the state is an A
 // operand in tensor memory, written there by the threads that computed it, and no result goes
 // back to shared memory:
-//     D_T [v][t] = V^T T^T          A = V (shared)
-//     D_W [v][t] = -S0 W^T          A = S0 (fp16 parts)
+//     D_W [v][t] = -S0 W^T          A = S0 (fp16 parts); S0 hi W hi^T and S0 hi W lo^T side by side
 //     D_Q [v][t] = S0 Q^T, then U^T M^T
-//     D_S [v][d] = U'^T K,  U' = diag(e^(g_C - g)) U,  U = D_T + D_W
-// Two warpgroups hold the fp32 state in registers (a lane has one v, 64 of its d's), form U and
-// U' and then S; a third writes the outputs.  Three warps load, each its own operands, whose
+//     D_S [v][d] = U'^T K,  U' = diag(e^(g_C - g)) U,  U = (T V)^T + D_W
+// Four warpgroups hold the fp32 state in registers (a lane has one v, 32 of its d's), form U and
+// U' and then S: what a chunk takes is their latency, and four warps a scheduler hide most of it.
+// Two write the outputs.  Three warps load, each its own operands, whose
 // space is free again as soon as their last product is done.  The chain of a chunk is S -> D_W ->
-// U' -> D_S -> S: S goes over in four parts and U' in two, so that the products of a part run
-// while the next one is converted.  S is scaled before it is known, by a bound on its rows:
+// U' -> D_S -> S: S goes over in two parts, so that the products of one run while the other is
+// converted.  S is scaled before it is known, by a bound on its rows:
 // |S| <= e^(g_C) max|S0| + 64 max|U| max|K|.
-constexpr int kScanThreads = 512;
+constexpr int kScanThreads = 896;
 constexpr int kScanW = 0;                               // [2] W, K, gates
 constexpr int kScanWBytes = 32768 + 16384 + 1024;
 constexpr int kScanQ = kScanW + 2 * kScanWBytes;        // [2] Q, M, the gates again (the outputs' warps read them late)
 constexpr int kScanQBytes = 16384 + 8192 + 1024;
-constexpr int kScanT = kScanQ + 2 * kScanQBytes;        // T, V
-constexpr int kScanTBytes = 24576 + 16384;
-constexpr int kScanBars = kScanT + kScanTBytes;
-constexpr int kScanSmemBytes = kScanBars + 5120;
+constexpr int kScanU = kScanQ + 2 * kScanQBytes;        // [2] T V
+constexpr int kScanUBytes = 32768;
+constexpr int kScanBars = kScanU + 2 * kScanUBytes;
+constexpr int kScanSmemBytes = kScanBars + 8192;
 static_assert(kScanSmemBytes <= 232448, "shared memory per CTA");
-static_assert(kScanWBytes % 1024 == 0 && kScanQBytes % 1024 == 0 && kScanTBytes % 1024 == 0, "tiles on 1 KB boundaries");
+static_assert(kScanWBytes % 1024 == 0 && kScanQBytes % 1024 == 0, "tiles on 1 KB boundaries");
 
 // what a launch does: the whole walk; or, for a sequence cut into segments, their states from
 // zero and their transitions (pass 0), then the outputs from the joined states (pass 1)
 constexpr int kScanWhole = 0, kScanEnds = 1, kScanOutputs = 2;
 
 struct ScanBars {
-  uint64_t full_t, empty_t, full_w[2], empty_w[2], full_q[2], empty_q[2];
-  uint64_t s_part[4], uw_part[2];   // 16 columns of S, 16 tokens of U', of either half
-  uint64_t d1, u_full, ds, qs, q_free, o, o_free, mma_done;
-  uint64_t rows[4];             // the two warps of 32 rows have their maxima in place
+  uint64_t full_w[2], empty_w[2], full_u[2], empty_u[2], full_q[2], empty_q[2];
+  uint64_t s_part[2];           // 16 columns of S of every quarter
+  uint64_t d1, uw_full, u_full, ds, qs, q_free, o, o_free, mma_done;
+  uint64_t rows[4];             // the four warps of 32 rows have their maxima in place
   uint32_t tmem;
   int abort;
-  // by row: 1 over the scales of S and U (by the parity of the chunk); the halves' largest |S|, |U|
+  // by row: 1 over the scales of S and U (by the parity of the chunk); the quarters' largest |S|, |U|
   float scale[2][kGdnDim], uscale[2][kGdnDim];
-  float smax[2][kGdnDim], umax[2][kGdnDim];
+  float smax[4][kGdnDim], umax[4][kGdnDim];
 };
-static_assert(sizeof(ScanBars) <= 5120, "barriers");
+static_assert(sizeof(ScanBars) <= 8192, "barriers");
 
+// 32 lanes x 32 bit, 8 (4) consecutive columns per thread
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                 "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+__device__ __forceinline__ void reg_fence8(uint32_t* r) {
+  asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+               "+r"(r[6]), "+r"(r[7]));
+}
 // Keeps the reads of a tcgen05.ld's 16 registers behind tcgen05.wait::ld.
 __device__ __forceinline__ void reg_fence16(uint32_t* r) {
   asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
@@ -773,9 +777,9 @@ __device__ __forceinline__ bool scan_wait(uint64_t* bar, uint32_t parity, volati
   return false;
 }
 
-// K and V as [tokens][heads][128], boxes of 64 tokens x 64 columns of one head
+// K as [tokens][key heads][128], boxes of 64 tokens x 64 columns of one head
 struct ScanMaps {
-  CUtensorMap k, v;
+  CUtensorMap k;
 };
 
 __global__ void __launch_bounds__(kScanThreads, 1)
@@ -821,27 +825,28 @@ __global__ void __launch_bounds__(kScanThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&B.full_w[i], 2);
-      mbar_init(&B.empty_w[i], 1 + 8);
+      mbar_init(&B.empty_w[i], 1 + 16);
+      mbar_init(&B.full_u[i], 1);
+      mbar_init(&B.empty_u[i], 16);
       mbar_init(&B.full_q[i], 1);
-      mbar_init(&B.empty_q[i], 1 + 4);
+      mbar_init(&B.empty_q[i], 1 + 8);
     }
-    mbar_init(&B.full_t, 2);
-    mbar_init(&B.empty_t, 1);
-    for (int i = 0; i < 4; ++i) mbar_init(&B.s_part[i], 8);
-    for (int i = 0; i < 2; ++i) mbar_init(&B.uw_part[i], 8);
+
+    for (int i = 0; i < 2; ++i) mbar_init(&B.s_part[i], 16);
+    mbar_init(&B.uw_full, 16);
     mbar_init(&B.d1, 1);
-    mbar_init(&B.u_full, 8);
+    mbar_init(&B.u_full, 16);
     mbar_init(&B.ds, 1);
     mbar_init(&B.qs, 1);
-    mbar_init(&B.q_free, 4);
+    mbar_init(&B.q_free, 8);
     mbar_init(&B.o, 1);
-    mbar_init(&B.o_free, 4);
+    mbar_init(&B.o_free, 8);
     mbar_init(&B.mma_done, 1);
-    for (int i = 0; i < 4; ++i) mbar_init(&B.rows[i], 2);
+    for (int i = 0; i < 4; ++i) mbar_init(&B.rows[i], 4);
     B.abort = 0;
     fence_mbar_init();
   }
-  if (warp == 12) {
+  if (warp == 24) {
     tmem_alloc(&B.tmem, 512);
     tmem_relinquish();
   }
@@ -850,34 +855,34 @@ __global__ void __launch_bounds__(kScanThreads, 1)
   tc_fence_after();
   // all 512 columns are this CTA's, so they start at 0: addresses are known to the compiler
   constexpr uint32_t tm = 0;
-  // columns: S hi 64, S lo 64, D_S 128, D_T 2 x 64 (by the parity of the chunk; each half of the
-  // threads then puts U' hi and U into the columns that it has read), D_W 64 (then U' mid and lo,
-  // the same way), D_Q 64
-  constexpr uint32_t tS = tm, tDS = tm + 128, tDT = tm + 256, tDW = tm + 384, tDQ = tm + 448;
+  // columns: S hi 64, S lo 64, D_S 128, D_W 64, its (hi, lo) part 64 (then U' mid and lo, each
+  // quarter of the threads in the columns that it has read), D_Q 64, U' hi 32, U 32
+  constexpr uint32_t tS = tm, tDS = tm + 128, tDW = tm + 256, tDQ = tm + 384, tUw = tm + 448,
+                     tU = tm + 480;
   volatile int* abort = &B.abort;
 
-  if (warp < 8) {
-    regs_raise<168>();
-    // ---- the state: lane = value row v, 64 columns d of it -----------------------------------
-    const int half = warp >> 2, v = 32 * (warp & 3) + lane;
+  if (warp < 16) {
+    regs_raise<80>();
+    // ---- the state: lane = value row v, 32 columns d of it -----------------------------------
+    const int quarter = warp >> 2, v = 32 * (warp & 3) + lane;
     const uint32_t lb = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    float s[64];
+    float s[32];
     if (trans) {
 #pragma unroll
-      for (int i = 0; i < 64; ++i) s[i] = 64 * half + i == v ? 1.f : 0.f;
+      for (int i = 0; i < 32; ++i) s[i] = 32 * quarter + i == v ? 1.f : 0.f;
     } else if (mode == kScanEnds && seg > 0) {
 #pragma unroll
-      for (int i = 0; i < 64; ++i) s[i] = 0.f;
+      for (int i = 0; i < 32; ++i) s[i] = 0.f;
     } else {
-      const float4* p = reinterpret_cast<const float4*>(src + v * kGdnDim + 64 * half);
+      const float4* p = reinterpret_cast<const float4*>(src + v * kGdnDim + 32 * quarter);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
+      for (int i = 0; i < 8; ++i) {
         const float4 x = p[i];
         s[4 * i] = x.x;
         s[4 * i + 1] = x.y;
         s[4 * i + 2] = x.z;
         s[4 * i + 3] = x.w;
-        if (mode == kScanEnds) reinterpret_cast<float4*>(kept + v * kGdnDim + 64 * half)[i] = x;
+        if (mode == kScanEnds) reinterpret_cast<float4*>(kept + v * kGdnDim + 32 * quarter)[i] = x;
       }
     }
     auto signal = [&](uint64_t* bar) {
@@ -886,13 +891,16 @@ __global__ void __launch_bounds__(kScanThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
     };
-    auto joined = [&](int phase) -> bool {   // the maxima of both halves of the rows are in place
+    auto joined = [&](int phase) -> bool {   // the maxima of all quarters of the rows are in place
       __syncwarp();
       if (lane == 0) mbar_arrive(&B.rows[warp & 3]);
       return __all_sync(0xffffffffu, scan_wait(&B.rows[warp & 3], phase & 1, abort, 337));
     };
+    auto row_max = [&](const float (*m)[kGdnDim]) -> float {
+      return fmaxf(fmaxf(m[0][v], m[1][v]), fmaxf(m[2][v], m[3][v]));
+    };
     bool ok = true;
-    float inv = 1.f, smax = 0.f;   // 1 over the scale of this row of S; its largest entry (half)
+    float inv = 1.f, smax = 0.f;   // 1 over the scale of this row of S; its largest entry (quarter)
     // turn c: S0 of chunk c into U, then into S, which goes over as the S0 of chunk c + 1; turn -1
     // only hands the first one over
 #pragma unroll 1
@@ -900,131 +908,141 @@ __global__ void __launch_bounds__(kScanThreads, 1)
       const int sg = c & 1;
       const bool first = c < 0, more = c + 1 < nc;
       {
-        float m[4] = {0.f, 0.f, 0.f, 0.f};
+        float m[2] = {0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < 64; ++i) m[i & 3] = fmaxf(m[i & 3], fabsf(s[i]));
-        smax = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+        for (int i = 0; i < 32; ++i) m[i & 1] = fmaxf(m[i & 1], fabsf(s[i]));
+        smax = fmaxf(m[0], m[1]);
       }
       float gc = 1.f, sc = 1.f;
       if (!first) {
         const float* gate = reinterpret_cast<const float*>(smem + kScanW + sg * kScanWBytes + 49152);
-        ok = scan_wait(&B.full_w[sg], (c >> 1) & 1, abort, 330) &&
+        float u[16];
+        if (trans) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) u[i] = 0.f;
+        } else {
+          ok = scan_wait(&B.full_u[sg], (c >> 1) & 1, abort, 338);
+          const float* tv = reinterpret_cast<const float*>(smem + kScanU + sg * kScanUBytes) + 16 * quarter * kGdnDim + v;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) u[i] = tv[i * kGdnDim];
+        }
+        ok = ok && scan_wait(&B.full_w[sg], (c >> 1) & 1, abort, 330) &&
              scan_wait(&B.d1, c & 1, abort, 331);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
         const float winv = inv * gate[kGateW];
-        const uint32_t dt = tDT + 64 * sg + lb + 32 * half;
-        float u[32];
+        const float4* wk = reinterpret_cast<const float4*>(gate + kGateU + 16 * quarter);
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          uint32_t x[16], y[16];
-          if (!trans) tmem_ld16(dt + 16 * g, x);
-          tmem_ld16(tDW + lb + 32 * half + 16 * g, y);
+        for (int b = 0; b < 2; ++b) {
+          uint32_t x[8], y[8], vh[4], vm[4], vl[4];
+          tmem_ld8(tDW + lb + 16 * quarter + 8 * b, y);
+          tmem_ld8(tDW + 64 + lb + 16 * quarter + 8 * b, x);
           tmem_wait_ld();
-          reg_fence16(x);
-          reg_fence16(y);
-          uint32_t vh[8], vm[8], vl[8];
-          const float4* wk = reinterpret_cast<const float4*>(gate + kGateU + 32 * half + 16 * g);
+          reg_fence8(x);
+          reg_fence8(y);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float4 w = wk[i];
-            float* p = u + 16 * g + 4 * i;
+          for (int i = 0; i < 2; ++i) {
+            const float4 w = wk[2 * b + i];
+            float* p = u + 8 * b + 4 * i;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              p[e] = fmaf(winv, __uint_as_float(y[4 * i + e]), trans ? 0.f : __uint_as_float(x[4 * i + e]));
+              p[e] = fmaf(winv, __uint_as_float(y[4 * i + e]) + __uint_as_float(x[4 * i + e]), p[e]);
             split3_bf16x2(w.x * p[0], w.y * p[1], &vh[2 * i], &vm[2 * i], &vl[2 * i]);
             split3_bf16x2(w.z * p[2], w.w * p[3], &vh[2 * i + 1], &vm[2 * i + 1], &vl[2 * i + 1]);
           }
-          // hi takes columns of D_T, mid and lo those of D_W that were just read
-          tmem_st8(dt + 16 * g, vh);
-          tmem_st8(tDW + lb + 32 * half + 16 * g, vm);
-          tmem_st8(tDW + lb + 32 * half + 16 * g + 8, vl);
-          signal(&B.uw_part[g]);
+          // mid and lo take columns of D_W that were just read
+          tmem_st4(tUw + lb + 8 * quarter + 4 * b, vh);
+          tmem_st4(tDW + lb + 16 * quarter + 4 * b, vm);
+          tmem_st4(tDW + 64 + lb + 16 * quarter + 4 * b, vl);
         }
+        signal(&B.uw_full);
         float umax = 0.f;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) umax = fmaxf(umax, fabsf(u[i]));
-        B.smax[half][v] = smax;
-        B.umax[half][v] = umax;
+        for (int i = 0; i < 16; ++i) umax = fmaxf(umax, fabsf(u[i]));
+        B.smax[quarter][v] = smax;
+        B.umax[quarter][v] = umax;
         gc = gate[kGateC];
         const float kmax = gate[kGateK];
         ok = joined(c + 1);
         if (!ok) break;
-        if (lane == 0) mbar_arrive(&B.empty_w[sg]);
-        umax = fmaxf(umax, B.umax[half ^ 1][v]);
-        sc = row_scale(fmaf(gc, fmaxf(smax, B.smax[half ^ 1][v]), 64.f * kmax * umax), &inv);
+        if (lane == 0) {
+          mbar_arrive(&B.empty_w[sg]);
+          if (!trans) mbar_arrive(&B.empty_u[sg]);
+        }
+        umax = row_max(B.umax);
+        sc = row_scale(fmaf(gc, row_max(B.smax), 64.f * kmax * umax), &inv);
         if (outputs) {
           float iu;
           const float su = row_scale(umax, &iu);
-          uint32_t w[16];
+          uint32_t w[8];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) w[i] = pack_f16x2(su * u[2 * i], su * u[2 * i + 1]);
-          if (half == 0) B.uscale[sg][v] = iu;
-          tmem_st8(dt + 8, w);
-          tmem_st8(dt + 24, w + 8);
+          for (int i = 0; i < 8; ++i) w[i] = pack_f16x2(su * u[2 * i], su * u[2 * i + 1]);
+          if (quarter == 0) B.uscale[sg][v] = iu;
+          tmem_st8(tU + lb + 8 * quarter, w);
           signal(&B.u_full);
         }
         ok = scan_wait(&B.ds, c & 1, abort, 332);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
       } else {
-        B.smax[half][v] = smax;
+        B.smax[quarter][v] = smax;
         ok = joined(0);
         if (!ok) break;
-        sc = row_scale(fmaxf(smax, B.smax[half ^ 1][v]), &inv);
+        sc = row_scale(row_max(B.smax), &inv);
       }
-      if (more && half == 0) B.scale[(c + 1) & 1][v] = inv;
-      uint32_t x[2][16];
-      if (!first) tmem_ld16(tDS + lb + 64 * half, x[0]);
+      if (more && quarter == 0) B.scale[(c + 1) & 1][v] = inv;
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
+      for (int g = 0; g < 2; ++g) {
         if (!first) {
+          uint32_t x[16];
+          tmem_ld16(tDS + lb + 32 * quarter + 16 * g, x);
           tmem_wait_ld();
-          reg_fence16(x[g & 1]);
-          if (g < 3) tmem_ld16(tDS + lb + 64 * half + 16 * (g + 1), x[(g + 1) & 1]);
+          reg_fence16(x);
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            s[16 * g + i] = fmaf(gc, s[16 * g + i], __uint_as_float(x[g & 1][i]));
+            s[16 * g + i] = fmaf(gc, s[16 * g + i], __uint_as_float(x[i]));
         }
-        if (more) {   // columns 16 g .. of this half, as fp16 parts
+        if (more) {   // columns 16 g .. of this quarter, as fp16 parts
           uint32_t vh[8], vl[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             split_f16x2(sc * s[16 * g + 2 * i], sc * s[16 * g + 2 * i + 1], &vh[i], &vl[i]);
-          tmem_st8(tS + lb + 32 * half + 8 * g, vh);
-          tmem_st8(tS + lb + 64 + 32 * half + 8 * g, vl);
+          tmem_st8(tS + lb + 16 * quarter + 8 * g, vh);
+          tmem_st8(tS + lb + 64 + 16 * quarter + 8 * g, vl);
           signal(&B.s_part[g]);
         }
       }
     }
     // in the outputs pass the joined states hold what the inner segments would write
     if (__all_sync(0xffffffffu, ok) && (mode == kScanEnds || last)) {
-      float4* p = reinterpret_cast<float4*>(dst + v * kGdnDim + 64 * half);
+      float4* p = reinterpret_cast<float4*>(dst + v * kGdnDim + 32 * quarter);
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
+      for (int i = 0; i < 8; ++i)
         p[i] = make_float4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]);
     }
-  } else if (warp < 12) {
-    regs_raise<136>();
-    // ---- outputs: lane = value v, 64 tokens --------------------------------------------------
+  } else if (warp < 24) {
+    regs_lower<72>();
+    // ---- outputs: lane = value v, 32 tokens --------------------------------------------------
     if (outputs) {
-      const int v = 32 * (warp - 8) + lane;
-      const uint32_t lb = static_cast<uint32_t>(32 * (warp - 8)) << 16;
+      const int half = (warp - 16) >> 2, v = 32 * (warp & 3) + lane;
+      const uint32_t lb = static_cast<uint32_t>(32 * (warp & 3)) << 16;
       const int64_t step = static_cast<int64_t>(a.heads) * kGdnDim;
       const uint32_t sel = (lane & 1) ? 0x3276 : 0x5410;
+#pragma unroll 1
       for (int c = 0; c < nc; ++c) {
         const int sg = c & 1;
-        const float4* eg = reinterpret_cast<const float4*>(smem + kScanQ + sg * kScanQBytes + 24576) + kGateQ / 4;
+        const float* gate = reinterpret_cast<const float*>(smem + kScanQ + sg * kScanQBytes + 24576);
+        const float4* eg = reinterpret_cast<const float4*>(gate + kGateQ + 32 * half);
+        const float2* gm = reinterpret_cast<const float2*>(gate + kGateM + 32 * half);
         bool ok = scan_wait(&B.full_q[sg], (c >> 1) & 1, abort, 333) &&
                   scan_wait(&B.qs, c & 1, abort, 334);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
-        const float inv = B.scale[c & 1][v];
-        const float4* gm = eg + (kGateM - kGateQ) / 4;
-        float y[64];
+        const float inv = B.scale[sg][v];
+        float y[32];
 #pragma unroll
-        for (int i0 = 0; i0 < 64; i0 += 16) {
-          tmem_ld16_at(tDQ + lb + i0, y + i0);
+        for (int i0 = 0; i0 < 32; i0 += 16) {
+          tmem_ld16_at(tDQ + lb + 32 * half + i0, y + i0);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float4 e = eg[i0 / 4 + i];
@@ -1040,30 +1058,30 @@ __global__ void __launch_bounds__(kScanThreads, 1)
         ok = scan_wait(&B.o, c & 1, abort, 335);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
-        const float iu = B.uscale[c & 1][v];
-        const int64_t left = ntok - static_cast<int64_t>(c) * kGdnChunk;
-        const int n = static_cast<int>(left < kGdnChunk ? left : kGdnChunk);
+        const float iu = B.uscale[sg][v];
+        const int64_t left = ntok - static_cast<int64_t>(c) * kGdnChunk - 32 * half - (lane & 1);
+        const int n = static_cast<int>(left < kGdnChunk ? left : kGdnChunk);   // mine: tokens i < n
         // lanes in pairs: the even one stores both its own and its neighbour's value of token t,
         // the odd one of token t + 1
-        __nv_bfloat16* op = a.out + ((t0 + static_cast<int64_t>(c) * kGdnChunk + (lane & 1)) * a.heads + h) * kGdnDim +
-                            32 * (warp - 8) + (lane & ~1);
+        __nv_bfloat16* op = a.out + ((t0 + static_cast<int64_t>(c) * kGdnChunk + 32 * half + (lane & 1)) * a.heads + h) * kGdnDim +
+                            (v & ~1);
 #pragma unroll
-        for (int i0 = 0; i0 < 64; i0 += 16) {
+        for (int i0 = 0; i0 < 32; i0 += 16) {
           float x[16];
-          tmem_ld16_at(tDQ + lb + i0, x);
-          if (i0 == 48) {   // all of D_Q has been read
+          tmem_ld16_at(tDQ + lb + 32 * half + i0, x);
+          if (i0 == 16) {   // D_Q has been read
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&B.o_free);
           }
 #pragma unroll
           for (int i = 0; i < 16; i += 2) {
-            const float2 e = *reinterpret_cast<const float2*>(reinterpret_cast<const float*>(gm) + i0 + i);
+            const float2 e = gm[(i0 + i) / 2];
             const uint32_t w = pack_bf16x2(fmaf(iu * e.x, x[i], y[i0 + i]),
                                            fmaf(iu * e.y, x[i + 1], y[i0 + i + 1]));
             const uint32_t z = __shfl_xor_sync(0xffffffffu, w, 1);
             const uint32_t both = __byte_perm(w, z, sel);
-            if (i0 + i + (lane & 1) < n) *reinterpret_cast<uint32_t*>(op) = both;
+            if (i0 + i < n) *reinterpret_cast<uint32_t*>(op) = both;
             op += 2 * step;
           }
         }
@@ -1073,41 +1091,41 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     }
   } else {
     regs_lower<40>();
-    if (warp == 12) {
+    if (warp == 24) {
     // ---- products: the whole warp walks the loop, one elected lane issues ----------------------
-    constexpr uint32_t kIdTV = idesc_bf16_f32(128, 64, 1, 0);   // A = V, tokens along its rows
     constexpr uint32_t kIdF16 = idesc_f16_f32(128, 64, 0, 0);
+    constexpr uint32_t kIdF16x2 = idesc_f16_f32(128, 128, 0, 0);   // W's hi and lo rows at once
     constexpr uint32_t kIdDS = idesc_bf16_f32(128, 128, 0, 1);  // B = K, tokens along its rows
     // Descriptors; a step along a tile adds its bytes / 16.  The loops stay loops: unrolled, this
     // warp alone would fill the instruction cache.
     const uint64_t dk = smem_desc_sw128(smem_u32(smem), 0, 1024);        // rows of 128 bytes
     const uint64_t dm = smem_desc_sw128(smem_u32(smem), 8192, 1024);     // two column panels
     bool ok = true;
-    // turn c: the products of chunk c, then V^T T^T of chunk c + 1; turn -1 only the latter
 #pragma unroll 1
-    for (int c = -1; c < nc; ++c) {
+    for (int c = 0; c < nc; ++c) {
       const int sg = c & 1;
       const uint32_t ph = (c >> 1) & 1;
       const uint64_t sw = (kScanW + sg * kScanWBytes) >> 4, sq = (kScanQ + sg * kScanQBytes) >> 4;
-      const uint32_t td = tDT + 64 * sg;
-      if (c >= 0) {
+      {
         if (!scan_wait(&B.full_w[sg], ph, abort, 342)) break;
-        // D_W = -S0 W^T: (hi, hi), (lo, hi), (hi, lo) of 16 columns of each half at a time
+        // D_W = -S0 W^T: (hi, hi and lo), (lo, hi) of 16 columns of each quarter at a time
 #pragma unroll 1
-        for (int g = 0; g < 4; ++g) {
+        for (int g = 0; g < 2; ++g) {
           ok = scan_wait(&B.s_part[g], c & 1, abort, 341);
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
-            const uint64_t dw = dk + sw + 2 * g;
-            const uint32_t ts = tS + 8 * g;
-#pragma unroll
+#pragma unroll 1
             for (int kh = 0; kh < 2; ++kh) {
-              umma_ts(tDW, ts + 32 * kh, dw + 512 * kh, kIdF16, g + kh > 0 ? 1u : 0u);
-              umma_ts(tDW, ts + 64 + 32 * kh, dw + 512 * kh, kIdF16, 1u);
-              umma_ts(tDW, ts + 32 * kh, dw + 1024 + 512 * kh, kIdF16, 1u);
+              const uint64_t dw = dk + sw + 1024 * kh + 2 * g;
+              const uint32_t ts = tS + 32 * kh + 8 * g;
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                umma_ts(tDW, ts + 16 * q, dw + 4 * q, kIdF16x2, g + kh + q > 0 ? 1u : 0u);
+                umma_ts(tDW, ts + 64 + 16 * q, dw + 4 * q, kIdF16, 1u);
+              }
             }
-            if (g == 3) umma_commit(&B.d1);   // covers D_T too
+            if (g == 1) umma_commit(&B.d1);
           }
           __syncwarp();
         }
@@ -1128,47 +1146,21 @@ __global__ void __launch_bounds__(kScanThreads, 1)
           __syncwarp();
         }
       }
-      // the next chunk's D_T = V^T T^T while U is formed (its columns are free: what the last chunk
-      // put there has been used, since its outputs and this chunk's S are there)
-      if (!trans && c + 1 < nc) {
-        if (!scan_wait(&B.full_t, (c + 1) & 1, abort, 340)) break;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint32_t to = tDT + 64 * ((c + 1) & 1);
+      if (!scan_wait(&B.uw_full, c & 1, abort, 345)) break;
+      tc_fence_after();
+      if (elect_one()) {
+        // D_S = U'^T K: hi, mid, lo
 #pragma unroll 1
-          for (int k = 0; k < 4; ++k)
-#pragma unroll
-            for (int p = 0; p < 3; ++p)
-              umma_ss(to, dm + ((kScanT + 24576) >> 4) + 128 * k, dk + (kScanT >> 4) + 512 * p + 2 * k,
-                      kIdTV, p + k > 0 ? 1u : 0u);
-          umma_commit(&B.empty_t);
+        for (int k = 0; k < 4; ++k) {
+          const uint64_t d = dm + sw + 2048 + 128 * k;
+          umma_ts(tDS, tUw + 8 * k, d, kIdDS, k > 0 ? 1u : 0u);
+          umma_ts(tDS, tDW + 16 * k, d, kIdDS, 1u);
+          umma_ts(tDS, tDW + 64 + 16 * k, d, kIdDS, 1u);
         }
-        __syncwarp();
+        umma_commit(&B.ds);
+        umma_commit(&B.empty_w[sg]);
       }
-      if (c < 0) continue;
-      // D_S = U'^T K: hi, mid, lo of 16 tokens of each half at a time
-#pragma unroll 1
-      for (int g = 0; g < 2; ++g) {
-        ok = scan_wait(&B.uw_part[g], c & 1, abort, 345);
-        if (!ok) break;
-        tc_fence_after();
-        if (elect_one()) {
-#pragma unroll
-          for (int kh = 0; kh < 2; ++kh) {
-            const uint32_t k = g + 2 * kh;
-            const uint64_t d = dm + sw + 2048 + 128 * k;
-            umma_ts(tDS, td + 16 * k, d, kIdDS, g + kh > 0 ? 1u : 0u);
-            umma_ts(tDS, tDW + 16 * k, d, kIdDS, 1u);
-            umma_ts(tDS, tDW + 16 * k + 8, d, kIdDS, 1u);
-          }
-          if (g == 1) {
-            umma_commit(&B.ds);
-            umma_commit(&B.empty_w[sg]);
-          }
-        }
-        __syncwarp();
-      }
-      if (!ok) break;
+      __syncwarp();
       if (outputs) {
         if (!scan_wait(&B.q_free, c & 1, abort, 346)) break;
         if (!scan_wait(&B.u_full, c & 1, abort, 348)) break;
@@ -1177,7 +1169,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
           // D_Q = U^T M^T
 #pragma unroll 1
           for (int k = 0; k < 4; ++k)
-            umma_ts(tDQ, td + 16 * k + 8, dk + sq + 1024 + 2 * k, kIdF16, k > 0 ? 1u : 0u);
+            umma_ts(tDQ, tU + 8 * k, dk + sq + 1024 + 2 * k, kIdF16, k > 0 ? 1u : 0u);
           umma_commit(&B.o);
           umma_commit(&B.empty_q[sg]);
         }
@@ -1189,52 +1181,50 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     mbar_drain(&B.mma_done, 0);
     __syncwarp();
   } else {
-    // ---- loads: warp 13: W, K and the gates; 14: T and V; 15: Q and M ---------------------------
-    const int who = warp - 13, stages = who == 1 ? 1 : 2;
-    uint64_t* full = who == 0 ? B.full_w : who == 1 ? &B.full_t : B.full_q;
-    uint64_t* empty = who == 0 ? B.empty_w : who == 1 ? &B.empty_t : B.empty_q;
+    // ---- loads: warp 25: W, K and the gates; 26: T V; 27: Q, M and the gates -------------------
+    const int who = warp - 25;
+    uint64_t* full = who == 0 ? B.full_w : who == 1 ? B.full_u : B.full_q;
+    uint64_t* empty = who == 0 ? B.empty_w : who == 1 ? B.empty_u : B.empty_q;
     const bool on = who == 0 || (who == 1 ? !trans : outputs);
-    const __nv_bfloat16* base = who == 0 ? a.k + h / (a.heads / a.key_heads) * kGdnDim : a.v + h * kGdnDim;
-    const int64_t step = static_cast<int64_t>(who == 0 ? a.key_heads : a.heads) * kGdnDim;
+    const int kh = h / (a.heads / a.key_heads);
     int issued = 0;
+#pragma unroll 1
     for (int c = 0; on && c < nc; ++c) {
-      const int sg = c % stages, turn = c / stages;
-      const bool ok = turn == 0 || scan_wait(&empty[sg], (turn & 1) ^ 1, abort, 347);
+      const int sg = c & 1;
+      const bool ok = c < 2 || scan_wait(&empty[sg], ((c >> 1) & 1) ^ 1, abort, 347);
       if (!__all_sync(0xffffffffu, ok)) break;
-      unsigned char* stage = smem + (who == 0 ? kScanW + sg * kScanWBytes : who == 1 ? kScanT : kScanQ + sg * kScanQBytes);
+      const int64_t at = t0 + static_cast<int64_t>(c) * kGdnChunk;
       const int64_t left = ntok - static_cast<int64_t>(c) * kGdnChunk;
       const int n = static_cast<int>(left < kGdnChunk ? left : kGdnChunk);
       const bool whole = n == kGdnChunk;
-      unsigned char* rows = stage + (who == 0 ? 32768 : 24576);   // K or V
+      unsigned char* stage = smem + (who == 0 ? kScanW + sg * kScanWBytes : who == 1 ? kScanU + sg * kScanUBytes : kScanQ + sg * kScanQBytes);
       if (lane == 0) {
         const unsigned char* rec = ca.rec + ((rec0 + c0 + c) * ca.nheads + hl) * static_cast<int64_t>(kRecBytes);
         if (who == 0) {
           mbar_arrive_expect_tx(&full[sg], 32768 + 1024 + (whole ? 16384 : 0));
           bulk_load(stage, rec + kRecW, 32768, &full[sg]);
           bulk_load(stage + 49152, rec + kRecGate, 1024, &full[sg]);
+          if (whole) {
+            tma_load_3d(stage + 32768, &maps.k, 0, kh, static_cast<int>(at), &full[sg]);
+            tma_load_3d(stage + 32768 + 8192, &maps.k, 64, kh, static_cast<int>(at), &full[sg]);
+          }
         } else if (who == 1) {
-          mbar_arrive_expect_tx(&full[sg], 24576 + (whole ? 16384 : 0));
-          bulk_load(stage, rec + kRecT, 24576, &full[sg]);
+          mbar_arrive_expect_tx(&full[sg], kScanUBytes);
+          bulk_load(stage, rec + kRecU, kScanUBytes, &full[sg]);
         } else {
           mbar_arrive_expect_tx(&full[sg], kScanQBytes);
           bulk_load(stage, rec + kRecQ, 16384, &full[sg]);
           bulk_load(stage + 16384, rec + kRecM, 8192, &full[sg]);
           bulk_load(stage + 24576, rec + kRecGate, 1024, &full[sg]);
         }
-        if (who < 2 && whole) {
-          const CUtensorMap* m = who == 0 ? &maps.k : &maps.v;
-          const int hh = who == 0 ? h / (a.heads / a.key_heads) : h;
-          const int tt = static_cast<int>(t0 + static_cast<int64_t>(c) * kGdnChunk);
-          tma_load_3d(rows, m, 0, hh, tt, &full[sg]);
-          tma_load_3d(rows + 8192, m, 64, hh, tt, &full[sg]);
-        }
       }
       __syncwarp();
       ++issued;
-      if (who < 2) {
+      if (who == 0) {
         if (!whole) {   // the rows behind the sequence's last token must be zero
-          const uint32_t to = smem_u32(rows);
-          const __nv_bfloat16* from = base + (t0 + static_cast<int64_t>(c) * kGdnChunk) * step;
+          const uint32_t to = smem_u32(stage + 32768);
+          const __nv_bfloat16* from = a.k + (at * a.key_heads + kh) * kGdnDim;
+          const int64_t step = static_cast<int64_t>(a.key_heads) * kGdnDim;
 #pragma unroll 1
           for (int e = lane; e < kGdnChunk * 16; e += 32) {
             const int t = e >> 4, w = e & 15;
@@ -1249,14 +1239,13 @@ __global__ void __launch_bounds__(kScanThreads, 1)
       }
     }
     if (lane == 0 && *abort)   // no copy may land after the CTA is gone
-      for (int c = issued > stages ? issued - stages : 0; c < issued; ++c)
-        mbar_drain(&full[c % stages], (c / stages) & 1);
+      for (int c = issued > 2 ? issued - 2 : 0; c < issued; ++c) mbar_drain(&full[c & 1], (c >> 1) & 1);
     }
   }
   tc_fence_before();
   __syncthreads();
   if (tid == 0 && *abort != 0) report_error(ca.st, kErrTimeout, *abort);
-  if (warp == 12) {
+  if (warp == 24) {
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tm, 512);
