@@ -264,6 +264,22 @@ __device__ __forceinline__ float row_scale(float m, float* inverse) {
   return __uint_as_float((261u - e) << 23);
 }
 
+// the larger magnitudes of two pairs of bf16
+__device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t m, uint32_t x) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(x & 0x7fff7fffu));
+  return r;
+}
+// a pair of bf16 times a power of two (as bf16), in fp16
+__device__ __forceinline__ uint32_t scale_to_f16x2(uint32_t x, uint16_t s) {
+  float lo = 0.f, hi = 0.f;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tfma.rn.f32.bf16 %0, l, %3, %0;\n\t"
+      "fma.rn.f32.bf16 %1, h, %3, %1;\n\t}"
+      : "+f"(lo), "+f"(hi)
+      : "r"(x), "h"(s));
+  return pack_f16x2(lo, hi);
+}
+
 __device__ __forceinline__ void ldsm4(uint32_t* r, uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -401,9 +417,11 @@ __global__ void __launch_bounds__(kPrepThreads, 4) k_delta_prep(DeltaChunkArgs c
   }
   cp_async_wait_all();
   __syncthreads();
-  const int rb = warp & 3;                       // 16 rows
-  const int ta = 16 * rb + gq, tb = ta + 8;
   const bool isq = warp >= 4;
+  // 16 rows; the causal mask leaves rb + 1 parts of four, so that the two warps of a scheduler
+  // take rb and 3 - rb
+  int rb = isq ? 3 - (warp & 3) : warp & 3;
+  int ta = 16 * rb + gq, tb = ta + 8;
   float acc[8][4];
   {
     // K K^T (warps 0..3) and Q K^T (4..7), the columns that the causal mask keeps
@@ -460,31 +478,24 @@ __global__ void __launch_bounds__(kPrepThreads, 4) k_delta_prep(DeltaChunkArgs c
     // Q as fp16 with scaled rows, in place (half a row a thread); then M in its space
     const int t = (tid - 128) >> 1, half = tid & 1;
     unsigned char* p = S.q + 8192 * half;
-    float m = 0.f;
+    uint32_t m2 = 0u;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       // the two panels' words of a row lie in the same banks: the halves take them in turn
       const uint4 x = *reinterpret_cast<const uint4*>(p + tile_byte(t, 8 * (i ^ (4 * half))));
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        m = fmaxf(m, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
+      m2 = max_abs_bf16x2(max_abs_bf16x2(m2, x.x), x.y);
+      m2 = max_abs_bf16x2(max_abs_bf16x2(m2, x.z), x.w);
     }
+    float m = fmaxf(__uint_as_float(m2 << 16), __uint_as_float(m2 & 0xffff0000u));
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
     float inv;
-    const float sc = row_scale(m, &inv);
+    const uint16_t sc = static_cast<uint16_t>(__float_as_uint(row_scale(m, &inv)) >> 16);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       uint4* at = reinterpret_cast<uint4*>(p + tile_byte(t, 8 * (i ^ (4 * half))));
       const uint4 x = *at;
-      uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const __half2 y = __floats2half2_rn(__uint_as_float(w[e] << 16) * sc,
-                                            __uint_as_float(w[e] & 0xffff0000u) * sc);
-        w[e] = *reinterpret_cast<const uint32_t*>(&y);
-      }
-      *at = make_uint4(w[0], w[1], w[2], w[3]);
+      *at = make_uint4(scale_to_f16x2(x.x, sc), scale_to_f16x2(x.y, sc), scale_to_f16x2(x.z, sc),
+                       scale_to_f16x2(x.w, sc));
     }
     if (half == 0) gate[kGateQ + t] = S.eg[t] * inv;
     fence_proxy_async_smem();
@@ -523,10 +534,10 @@ __global__ void __launch_bounds__(kPrepThreads, 4) k_delta_prep(DeltaChunkArgs c
       bulk_store(rec + kRecM, S.q, 8192);
       bulk_store_wait();
     }
-  } else if (warp < 2) {
+  } else if (const int part = warp ^ (2 * (blockIdx.x & 1)); part < 2) {
     // Tu = (I + L)^-1 in place, by halves: the two 32 x 32 diagonal blocks by forward
     // substitution (a warp each, a column a lane), then the block below them, -T22 (L21 T11)
-    const int o = 32 * warp;
+    const int o = 32 * part;
     float u[32];
 #pragma unroll
     for (int t = 0; t < 32; ++t) {
@@ -549,19 +560,18 @@ __global__ void __launch_bounds__(kPrepThreads, 4) k_delta_prep(DeltaChunkArgs c
     for (int t = 0; t < 32; ++t) S.a[(o + t) * kPrepLdA + o + lane] = u[t];
   } else {
     // the largest |K|: one row a lane
-    const int t = tid - 64;
-    float m = 0.f;
+    const int t = 32 * (part - 2) + lane;
+    uint32_t m2 = 0u;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const uint4 x = *reinterpret_cast<const uint4*>(S.k + 8192 * (i >> 3) + tile_byte(t, 8 * (i & 7)));
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        m = fmaxf(m, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
+      m2 = max_abs_bf16x2(max_abs_bf16x2(m2, x.x), x.y);
+      m2 = max_abs_bf16x2(max_abs_bf16x2(m2, x.z), x.w);
     }
+    float m = fmaxf(__uint_as_float(m2 << 16), __uint_as_float(m2 & 0xffff0000u));
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (lane == 0) S.kmax[warp - 2] = m;
+    if (lane == 0) S.kmax[part - 2] = m;
   }
   __syncthreads();
   // V in Q's and M's space (M has been read: the barrier)
@@ -612,6 +622,9 @@ __global__ void __launch_bounds__(kPrepThreads, 4) k_delta_prep(DeltaChunkArgs c
   // T V, T = Tu diag(beta), and then W = T diag(e^g) K: warp = 16 rows x 64 columns
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
+    rb = pass ? 3 - (warp & 3) : warp & 3;
+    ta = 16 * rb + gq;
+    tb = ta + 8;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
