@@ -339,7 +339,7 @@ struct PrepSmem {
   float gate[256];
   float g_hi[kGdnChunk], g_lo[kGdnChunk]; // running log gate in base 2, as a sum
   float beta[kGdnChunk], eg[kGdnChunk], beg[kGdnChunk];   // beta, e^g, their product
-  float wmax[8], kmax[2];
+  float wmax[8], kmax[4];
 };
 static_assert(16384 + 4 * kGdnChunk * kPrepLdA >= 32768, "W fits");
 static_assert(sizeof(PrepSmem) <= 55 * 1024, "four CTAs an SM");
@@ -348,6 +348,33 @@ __device__ __forceinline__ float exp2_approx(float x) {   // 2 ulp; -inf gives 0
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// z += left (16 x 16) right (16 x 8) of S.a, operands in three bf16 parts
+__device__ __forceinline__ void prep_mma3(float* z, const float* left, const float* right, int gq,
+                                          int tq) {
+  uint32_t x[3][4], y[3][2];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 v = *reinterpret_cast<const float2*>(left + (gq + 8 * (e & 1)) * kPrepLdA + 2 * tq +
+                                                      8 * (e >> 1));
+    split3_bf16x2(v.x, v.y, &x[0][e], &x[1][e], &x[2][e]);
+  }
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const float* p = right + (2 * tq + 8 * e) * kPrepLdA + gq;
+    split3_bf16x2(p[0], p[kPrepLdA], &y[0][e], &y[1][e], &y[2][e]);
+  }
+#pragma unroll
+  for (int i = 0; i < 3; ++i)
+#pragma unroll
+    for (int j = 0; i + j < 3; ++j) delta_mma(z, x[i], y[j][0], y[j][1]);
+}
+__device__ __forceinline__ void prep_put(float* to, const float* z, float sign, int gq, int tq) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    *reinterpret_cast<float2*>(to + (gq + 8 * i) * kPrepLdA + 2 * tq) =
+        make_float2(sign * z[2 * i], sign * z[2 * i + 1]);
 }
 
 __global__ void __launch_bounds__(kPrepThreads, 4) k_delta_prep(DeltaChunkArgs ca) {
@@ -534,44 +561,61 @@ __global__ void __launch_bounds__(kPrepThreads, 4) k_delta_prep(DeltaChunkArgs c
       bulk_store(rec + kRecM, S.q, 8192);
       bulk_store_wait();
     }
-  } else if (const int part = warp ^ (2 * (blockIdx.x & 1)); part < 2) {
-    // Tu = (I + L)^-1 in place, by halves: the two 32 x 32 diagonal blocks by forward
-    // substitution (a warp each, a column a lane), then the block below them, -T22 (L21 T11)
-    const int o = 32 * part;
-    float u[32];
+    __syncwarp();
+  } else {
+    // Tu = (I + L)^-1 in place.  The four 16 x 16 diagonal blocks by forward substitution, a block
+    // a warp, a column a lane (both halves of the warp alike); then twice by halves, the block
+    // below the diagonal being -T22 (L21 T11).  Upper blocks hold what was in the way: they are
+    // zero in Tu, and nothing reads them as Tu.
+    const int o = 16 * warp;
+    float u[16];
 #pragma unroll
-    for (int t = 0; t < 32; ++t) {
-      float x[4] = {t == lane ? 1.f : 0.f, 0.f, 0.f, 0.f};
+    for (int t = 0; t < 16; ++t) {
+      float x[2] = {t == (lane & 15) ? 1.f : 0.f, 0.f};
       const float* row = &S.a[(o + t) * kPrepLdA + o];
 #pragma unroll
       for (int j = 0; j + 4 <= t; j += 4) {
         const float4 l = *reinterpret_cast<const float4*>(row + j);
         x[0] = fmaf(-l.x, u[j], x[0]);
         x[1] = fmaf(-l.y, u[j + 1], x[1]);
-        x[2] = fmaf(-l.z, u[j + 2], x[2]);
-        x[3] = fmaf(-l.w, u[j + 3], x[3]);
+        x[0] = fmaf(-l.z, u[j + 2], x[0]);
+        x[1] = fmaf(-l.w, u[j + 3], x[1]);
       }
 #pragma unroll
-      for (int j = t & ~3; j < t; ++j) x[j & 3] = fmaf(-row[j], u[j], x[j & 3]);
-      u[t] = (x[0] + x[1]) + (x[2] + x[3]);
+      for (int j = t & ~3; j < t; ++j) x[j & 1] = fmaf(-row[j], u[j], x[j & 1]);
+      u[t] = x[0] + x[1];
     }
     __syncwarp();
+    if (lane < 16)
 #pragma unroll
-    for (int t = 0; t < 32; ++t) S.a[(o + t) * kPrepLdA + o + lane] = u[t];
-  } else {
-    // the largest |K|: one row a lane
-    const int t = 32 * (part - 2) + lane;
-    uint32_t m2 = 0u;
+      for (int t = 0; t < 16; ++t) S.a[(o + t) * kPrepLdA + o + lane] = u[t];
+    // the largest |K|: half a row a lane
+    {
+      uint32_t m2 = 0u;
+      const unsigned char* p = S.k + 8192 * (lane & 1);
+      const int t = o + (lane >> 1);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const uint4 x = *reinterpret_cast<const uint4*>(S.k + 8192 * (i >> 3) + tile_byte(t, 8 * (i & 7)));
-      m2 = max_abs_bf16x2(max_abs_bf16x2(m2, x.x), x.y);
-      m2 = max_abs_bf16x2(max_abs_bf16x2(m2, x.z), x.w);
+      for (int i = 0; i < 8; ++i) {
+        const uint4 x = *reinterpret_cast<const uint4*>(p + tile_byte(t, 8 * (i ^ (4 * (lane & 1)))));
+        m2 = max_abs_bf16x2(max_abs_bf16x2(m2, x.x), x.y);
+        m2 = max_abs_bf16x2(max_abs_bf16x2(m2, x.z), x.w);
+      }
+      float m = fmaxf(__uint_as_float(m2 << 16), __uint_as_float(m2 & 0xffff0000u));
+#pragma unroll
+      for (int i = 1; i < 32; i <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
+      if (lane == 0) S.kmax[warp] = m;
     }
-    float m = fmaxf(__uint_as_float(m2 << 16), __uint_as_float(m2 & 0xffff0000u));
+    named_barrier_sync(2, 128);
+    // 16 -> 32: two blocks, two tiles of 8 columns each
+    const int d = 32 * (warp >> 1), c8 = 8 * (warp & 1);
+    float z[4] = {0.f, 0.f, 0.f, 0.f};
+    prep_mma3(z, &S.a[(d + 16) * kPrepLdA + d], &S.a[d * kPrepLdA + d + c8], gq, tq);
+    prep_put(&S.a[d * kPrepLdA + d + 16 + c8], z, 1.f, gq, tq);
+    named_barrier_sync(2, 128);
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (lane == 0) S.kmax[part - 2] = m;
+    for (int e = 0; e < 4; ++e) z[e] = 0.f;
+    prep_mma3(z, &S.a[(d + 16) * kPrepLdA + d + 16], &S.a[d * kPrepLdA + d + 16 + c8], gq, tq);
+    prep_put(&S.a[(d + 16) * kPrepLdA + d + c8], z, -1.f, gq, tq);
   }
   __syncthreads();
   // V in Q's and M's space (M has been read: the barrier)
@@ -581,41 +625,21 @@ __global__ void __launch_bounds__(kPrepThreads, 4) k_delta_prep(DeltaChunkArgs c
                a.v + ((t0 + (t < n ? t : 0)) * a.heads + h) * kGdnDim + 8 * w, t < n);
   }
   {
-    // T21 = -T22 (L21 T11): two products of 32 x 32 x 32, a 16 x 8 tile a warp, operands in three
-    // bf16 parts; L21 T11 goes to the unused upper block
+    // 32 -> 64: T21 = -T22 (L21 T11), a 16 x 8 tile a warp; T11 and T22 are zero above their
+    // diagonal
     const int r0 = 16 * (warp & 1), c0 = 8 * (warp >> 1);
+    float z[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
-    for (int step = 0; step < 2; ++step) {
-      const float* left = &S.a[(32 + r0) * kPrepLdA + (step ? 32 : 0)];
-      const float* right = &S.a[c0 + (step ? 32 : 0)];
-      float z[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int k0 = c0 & 16; k0 < 32; k0 += 16)
+      prep_mma3(z, &S.a[(32 + r0) * kPrepLdA + k0], &S.a[k0 * kPrepLdA + c0], gq, tq);
+    prep_put(&S.a[r0 * kPrepLdA + 32 + c0], z, 1.f, gq, tq);
+    __syncthreads();
 #pragma unroll
-      for (int k0 = 0; k0 < 32; k0 += 16) {
-        uint32_t x[3][4], y[3][2];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 v = *reinterpret_cast<const float2*>(
-              left + (gq + 8 * (e & 1)) * kPrepLdA + k0 + 2 * tq + 8 * (e >> 1));
-          split3_bf16x2(v.x, v.y, &x[0][e], &x[1][e], &x[2][e]);
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float* p = right + (k0 + 2 * tq + 8 * e) * kPrepLdA + gq;
-          split3_bf16x2(p[0], p[kPrepLdA], &y[0][e], &y[1][e], &y[2][e]);
-        }
-#pragma unroll
-        for (int i = 0; i < 3; ++i)
-#pragma unroll
-          for (int j = 0; i + j < 3; ++j) delta_mma(z, x[i], y[j][0], y[j][1]);
-      }
-      const float sign = step ? -1.f : 1.f;
-      float* to = step ? &S.a[(32 + r0) * kPrepLdA + c0] : &S.a[r0 * kPrepLdA + 32 + c0];
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        *reinterpret_cast<float2*>(to + (gq + 8 * i) * kPrepLdA + 2 * tq) =
-            make_float2(sign * z[2 * i], sign * z[2 * i + 1]);
-      if (!step) __syncthreads();
-    }
+    for (int e = 0; e < 4; ++e) z[e] = 0.f;
+#pragma unroll 1
+    for (int k0 = 0; k0 <= r0; k0 += 16)
+      prep_mma3(z, &S.a[(32 + r0) * kPrepLdA + 32 + k0], &S.a[k0 * kPrepLdA + 32 + c0], gq, tq);
+    prep_put(&S.a[(32 + r0) * kPrepLdA + c0], z, -1.f, gq, tq);
   }
   cp_async_wait_all();
   __syncthreads();
@@ -641,7 +665,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) k_delta_prep(DeltaChunkArgs c
         const float2 y = *reinterpret_cast<const float2*>(&scale[j]);
         split3_bf16x2(x.x * y.x, x.y * y.y, &fh[e], &fm[e], &fl[e]);
       }
-      // rows 0..31 of Tu end at column 31: what lies beyond is L21 T11, which ks <= rb never reaches
+      // ks <= rb: never a block above the diagonal
 #pragma unroll
       for (int np = 0; np < 4; ++np) {
         uint32_t fb[4];
@@ -677,7 +701,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) k_delta_prep(DeltaChunkArgs c
   float inv_w;
   const float sw = -row_scale(m, &inv_w);
   if (tid == 0) {
-    gate[kGateK] = fmaxf(S.kmax[0], S.kmax[1]);
+    gate[kGateK] = fmaxf(fmaxf(S.kmax[0], S.kmax[1]), fmaxf(S.kmax[2], S.kmax[3]));
     gate[kGateW] = inv_w;
   }
   unsigned char* w = S.k + 16384 * (warp >> 2);   // on into Tu's space
