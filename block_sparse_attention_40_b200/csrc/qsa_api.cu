@@ -3,6 +3,7 @@
 // contract of every entry point are in include/qsa.h.
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdio>
 #include <cstring>
 #include <mutex>
@@ -1276,6 +1277,13 @@ struct ExtendPlan {
 
 constexpr int64_t kRecordBudget = int64_t(1) << 32;
 
+// Rows of a state that a CTA of the join takes: as few as leave the grid in one wave.
+int join_rows(int64_t heads_seqs) {
+  int rows = 4;
+  while (rows < 16 && heads_seqs * (kGdnDim / rows) > num_sms()) rows *= 2;
+  return rows;
+}
+
 void extend_plan(const int32_t* h_cu, int32_t num_seqs, int32_t heads, ExtendPlan* p) {
   const int64_t tokens = h_cu[num_seqs];
   p->records = tokens / kGdnChunk + num_seqs;
@@ -1290,14 +1298,18 @@ void extend_plan(const int32_t* h_cu, int32_t num_seqs, int32_t heads, ExtendPla
     p->max_chunks = std::max(p->max_chunks, nc);
     total += nc;
   }
-  // Time of a launch, in chunks: its longest walk, or all walks over the SMs.  Cut, the walks
-  // but the last segment's run twice more without outputs (states and transitions, about 0.8
-  // of a chunk's time each), and the join takes about half a chunk's time per segment.
+  // Microseconds of the scan, uncut and cut into about k segments: the longest walk, or all walks
+  // in waves over the SMs, at what a chunk was measured to take (2.65 with outputs, 2.4 without),
+  // and what a launch and a step of the join were.  Cut, all segments but the last run first
+  // without outputs (from zero, and their transitions), then all run with outputs.
   const double sms = num_sms();
-  auto spread = [&](double longest, double all) { return std::max(longest, all / sms); };
-  double best = spread(double(p->max_chunks), double(total) * hp);
+  // (a CTA takes 8 until its first chunk)
+  auto waves_of = [&](double l, double all, double chunk) {
+    return std::ceil(std::max(1.0, all / sms / l)) * (8 + chunk * l);
+  };
+  double best = 10 + 2.65 * std::max(double(p->max_chunks), double(total) * hp / sms);
   int64_t L = std::max<int64_t>(1, p->max_chunks);
-  for (int64_t k = 3; k <= 256 && k <= p->max_chunks / 2; k += 1 + k / 16) {
+  for (int64_t k = 3; k <= 512 && k <= p->max_chunks / 2; k += 1 + k / 16) {
     const int64_t l = (p->max_chunks + k - 1) / k;
     double inner = 0;
     for (int32_t i = 0; i < num_seqs; ++i) {
@@ -1305,9 +1317,11 @@ void extend_plan(const int32_t* h_cu, int32_t num_seqs, int32_t heads, ExtendPla
       const int64_t segs = (nc + l - 1) / l;
       if (segs > 1) inner += double((2 * segs - 3) * l);
     }
-    const double t = 0.8 * spread(double(l), inner * hp) + 0.5 * double(k) + 4 +
-                     spread(double(l), double(total) * hp);
-    if (t < 0.9 * best) {
+    const int rows = join_rows(int64_t(num_seqs) * hp);
+    const double waves = std::ceil(double(num_seqs) * hp * (kGdnDim / rows) / sms);
+    const double t = waves_of(double(l), inner * hp, 2.4) + waves * (6 + double(k) * 0.9) + 8 +
+                     waves_of(double(l), double(total) * hp, 2.65);
+    if (t < best) {
       best = t;
       L = l;
     }
@@ -1376,7 +1390,9 @@ extern "C" qsa_status qsa_gated_deltanet_extend(
     if (!make_tmap(&maps.k, k, 3, kd, ks, box)) return QSA_ERR_CUDA;
   }
   const int prep_smem = static_cast<int>(sizeof(PrepSmem));
-  if (!set_smem(k_delta_prep, prep_smem) || !set_smem(k_delta_scan, kScanSmemBytes))
+  if (!set_smem(k_delta_prep, prep_smem) || !set_smem(k_delta_scan, kScanSmemBytes) ||
+      !set_smem(k_delta_join<4>, join_smem_bytes(4)) || !set_smem(k_delta_join<8>, join_smem_bytes(8)) ||
+      !set_smem(k_delta_join<16>, join_smem_bytes(16)))
     return QSA_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   for (int32_t h0 = 0; h0 < heads; h0 += p.pass_heads) {
@@ -1384,20 +1400,19 @@ extern "C" qsa_status qsa_gated_deltanet_extend(
     a.nheads = std::min(p.pass_heads, heads - h0);
     k_delta_prep<<<dim3(static_cast<unsigned>(p.records), a.nheads), kPrepThreads, prep_smem, s>>>(a);
     QSA_CHECK_LAUNCH();
+    // each of these sets up while the one before it finishes
     if (p.segs > 1) {
-      k_delta_scan<<<dim3(a.nheads, num_seqs, 2 * (p.segs - 1)), kScanThreads, kScanSmemBytes, s>>>(
-          maps, a, kScanEnds);
-      QSA_CHECK_LAUNCH();
+      QSA_CHECK_PDL(launch_pdl(k_delta_scan, dim3(a.nheads, num_seqs, 2 * (p.segs - 1)),
+                               dim3(kScanThreads), kScanSmemBytes, s, maps, a, kScanEnds));
       if (p.segs > 2) {
-        if (!set_smem(k_delta_join, kJoinSmemBytes)) return QSA_ERR_CUDA;
-        k_delta_join<<<dim3(a.nheads, num_seqs, kGdnDim / kJoinRows), kGdnDim, kJoinSmemBytes,
-                       s>>>(a);
-        QSA_CHECK_LAUNCH();
+        const int rows = join_rows(int64_t(a.nheads) * num_seqs);
+        QSA_CHECK_PDL(launch_pdl(rows == 4 ? k_delta_join<4> : rows == 8 ? k_delta_join<8> : k_delta_join<16>,
+                                 dim3(a.nheads, num_seqs, kGdnDim / rows), dim3(kJoinThreads),
+                                 join_smem_bytes(rows), s, a));
       }
     }
-    k_delta_scan<<<dim3(a.nheads, num_seqs, p.segs), kScanThreads, kScanSmemBytes, s>>>(
-        maps, a, p.segs > 1 ? kScanOutputs : kScanWhole);
-    QSA_CHECK_LAUNCH();
+    QSA_CHECK_PDL(launch_pdl(k_delta_scan, dim3(a.nheads, num_seqs, p.segs), dim3(kScanThreads),
+                             kScanSmemBytes, s, maps, a, p.segs > 1 ? kScanOutputs : kScanWhole));
   }
   return QSA_OK;
 }

@@ -383,6 +383,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) k_delta_prep(DeltaChunkArgs c
   const DeltaArgs& a = ca.d;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, tq = lane & 3;
   const int64_t r = blockIdx.x;
+  pdl_trigger();   // the scan sets up while the last of these run
   // the last sequence whose first record is not past r, 256 candidates at a time
   int seq = 0;
   for (int step = a.rows > kPrepThreads ? kPrepThreads : 1; step > 0; step = step > 1 ? 1 : 0) {
@@ -826,6 +827,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
   const DeltaArgs& a = ca.d;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int hl = blockIdx.x, h = ca.head0 + hl, row = blockIdx.y;
+  pdl_trigger();
   // pass 0 has two CTAs a segment: states from zero, and transitions
   const bool trans = mode == kScanEnds && (blockIdx.z & 1);
   const int seg = mode == kScanEnds ? blockIdx.z >> 1 : blockIdx.z;
@@ -837,11 +839,15 @@ __global__ void __launch_bounds__(kScanThreads, 1)
   const int nc = static_cast<int>(c1 - c0);
   const bool last = c1 == chunks;
   const int slot = a.slots != nullptr ? a.slots[row] : row;
-  if (nc <= 0 || slot < 0 || slot >= a.num_slots) return;
-  if (mode == kScanEnds && (last || (trans && seg == 0))) return;
-  if (delta_slot_taken(a, row, slot)) return;
-  if ((smem_u32(smem) & 1023u) != 0) {   // the tiles need it; the runtime places them so
+  bool idle = nc <= 0 || slot < 0 || slot >= a.num_slots ||
+              (mode == kScanEnds && (last || (trans && seg == 0)));
+  if (!idle) idle = delta_slot_taken(a, row, slot);
+  if (!idle && (smem_u32(smem) & 1023u) != 0) {   // the tiles need it; the runtime places them so
     if (tid == 0) report_error(ca.st, kErrDevice, 320);
+    idle = true;
+  }
+  if (idle) {
+    pdl_wait();   // every CTA waits: the kernels after this one count on all before it
     return;
   }
   const bool outputs = mode != kScanEnds;
@@ -890,6 +896,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  pdl_wait();
   // all 512 columns are this CTA's, so they start at 0: addresses are known to the compiler
   constexpr uint32_t tm = 0;
   // columns: S hi 64, S lo 64, D_S 128, D_W 64, its (hi, lo) part 64 (then U' mid and lo, each
@@ -1290,66 +1297,109 @@ __global__ void __launch_bounds__(kScanThreads, 1)
 }
 
 // Joins the segments of a sequence: entered with E (the state at its start), a segment ends with
-// E P + S.  Rows of the state are independent: a CTA takes four of them through the segments in
-// order, a thread one column.  Bound by the latency of a step (512 multiply-adds a thread, P from
-// shared memory); the P of the next two segments are on their way meanwhile.
-constexpr int kJoinRows = 4;
-constexpr int kJoinStages = 3;
-constexpr int kJoinSmemBytes = kJoinStages * kGdnDim * kGdnDim * 4;
+// E P + S.  Rows of the state are independent: a CTA takes kRows of them through the segments in
+// order.  A warp takes 32 of the 128 terms of every product and a lane four columns, so that P
+// leaves shared memory once (64 KB, 512 cycles, which is what a step of four or eight rows is
+// bound by); the warps' parts are added in order.  The P of the next segments are on their way.
+constexpr int kJoinThreads = 128;
+constexpr int join_stages(int rows) { return rows > 8 ? 2 : 3; }
+constexpr int join_smem_bytes(int rows) {
+  return join_stages(rows) * kGdnDim * kGdnDim * 4 + 5 * rows * kGdnDim * 4;
+}
 
-// grid (heads of the pass, sequences, 128 / kJoinRows), 128 threads
-__global__ void __launch_bounds__(kGdnDim) k_delta_join(DeltaChunkArgs ca) {
-  extern __shared__ __align__(128) float join_p[];   // [stages][128][128]
-  __shared__ __align__(16) float e[kJoinRows][kGdnDim];
+// grid (heads of the pass, sequences, 128 / kRows)
+template <int kRows>
+__global__ void __launch_bounds__(kJoinThreads) k_delta_join(DeltaChunkArgs ca) {
+  constexpr int kStages = join_stages(kRows), kTile = kGdnDim * kGdnDim;
+  extern __shared__ __align__(128) float join_sh[];   // P [stages][128][128], E, the warps' parts
+  __shared__ uint64_t full[kStages];
+  __shared__ int abort_flag;
+  float* e = join_sh + kStages * kTile;               // [rows][128]
+  float* part = e + kRows * kGdnDim;                  // [4][rows][128]
   const DeltaArgs& a = ca.d;
-  const int row = blockIdx.y, hl = blockIdx.x, d = threadIdx.x, v0 = blockIdx.z * kJoinRows;
+  const int row = blockIdx.y, hl = blockIdx.x, d = threadIdx.x, v0 = blockIdx.z * kRows;
+  const int warp = d >> 5, lane = d & 31;
+  pdl_trigger();
   int64_t len;
   const int64_t begin = delta_row_tokens(a, row, &len);
   const int64_t chunks = (len + kGdnChunk - 1) / kGdnChunk;
   const int64_t segs = (chunks + ca.seg_chunks - 1) / ca.seg_chunks;
+  if (d == 0) {
+    for (int i = 0; i < kStages; ++i) mbar_init(&full[i], 1);
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  pdl_wait();
   if (segs < 3) return;
-  const int64_t tile = static_cast<int64_t>(kGdnDim) * kGdnDim, stride = ca.nheads * tile;
-  const int64_t at = ((delta_first_record(begin, row) / ca.seg_chunks + row) * ca.nheads + hl) * tile;
+  volatile int* abort = &abort_flag;
+  const int64_t stride = static_cast<int64_t>(ca.nheads) * kTile;
+  const int64_t at = ((delta_first_record(begin, row) / ca.seg_chunks + row) * ca.nheads + hl) * kTile;
   float* s = ca.seg_state + at + v0 * kGdnDim + d;
   const float* p = ca.seg_trans + at;
-  auto fetch = [&](int64_t g) {   // segment g's transition (one group a call, empty past the end)
-    if (g + 1 < segs) {
-      const uint32_t to = smem_u32(join_p + (g % kJoinStages) * tile);
-      for (int i = d; i < kGdnDim * kGdnDim / 4; i += kGdnDim)
-        cp_async16(to + 16 * i, p + g * stride + 4 * i, true);
+  auto fetch = [&](int64_t g) {   // segment g's transition
+    if (d == 0 && g + 1 < segs) {
+      uint64_t* bar = &full[(g - 1) % kStages];
+      mbar_arrive_expect_tx(bar, kTile * 4);
+      bulk_load(join_sh + ((g - 1) % kStages) * kTile, p + g * stride, kTile * 4, bar);
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  fetch(1);
-  fetch(2);
+  int64_t fetched = 0;   // segments 1 .. fetched are on their way or here
+  for (int g = 1; g <= kStages; ++g) fetch(fetched = g);
+  float next[kRows];   // the next segment's S
 #pragma unroll
-  for (int i = 0; i < kJoinRows; ++i) e[i][d] = s[i * kGdnDim];
+  for (int i = 0; i < kRows; ++i) {
+    e[i * kGdnDim + d] = s[i * kGdnDim];
+    next[i] = s[stride + i * kGdnDim];
+  }
+  __syncthreads();
+  bool ok = true;
   for (int64_t g = 1; g + 1 < segs; ++g) {
     s += stride;
-    float acc[kJoinRows];
+    float own[kRows];
 #pragma unroll
-    for (int i = 0; i < kJoinRows; ++i) acc[i] = s[i * kGdnDim];
-    asm volatile("cp.async.wait_group 1;" ::: "memory");
-    __syncthreads();   // this segment's P and E are in place, the last one's are done with
-    fetch(g + 2);
-    const float* pg = join_p + (g % kJoinStages) * tile + d;
-#pragma unroll 8
-    for (int k = 0; k < kGdnDim; k += 4) {
-      float x[4];
+    for (int i = 0; i < kRows; ++i) {
+      own[i] = next[i];
+      if (g + 2 < segs) next[i] = s[stride + i * kGdnDim];
+    }
+    ok = scan_wait(&full[(g - 1) % kStages], ((g - 1) / kStages) & 1, abort, 350);
+    if (__syncthreads_or(!ok)) break;
+    const float* pg = join_sh + ((g - 1) % kStages) * kTile + 32 * warp * kGdnDim + 4 * lane;
+    float4 acc[kRows];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] = pg[(k + j) * kGdnDim];
+    for (int i = 0; i < kRows; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+    for (int k = 0; k < 32; k += 4) {
+      float4 x[4];
 #pragma unroll
-      for (int i = 0; i < kJoinRows; ++i) {
-        const float4 y = *reinterpret_cast<const float4*>(&e[i][k]);
-        acc[i] = fmaf(y.x, x[0], fmaf(y.y, x[1], fmaf(y.z, x[2], fmaf(y.w, x[3], acc[i]))));
+      for (int j = 0; j < 4; ++j) x[j] = *reinterpret_cast<const float4*>(pg + (k + j) * kGdnDim);
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const float4 y = *reinterpret_cast<const float4*>(e + i * kGdnDim + 32 * warp + k);
+        acc[i].x = fmaf(y.x, x[0].x, fmaf(y.y, x[1].x, fmaf(y.z, x[2].x, fmaf(y.w, x[3].x, acc[i].x))));
+        acc[i].y = fmaf(y.x, x[0].y, fmaf(y.y, x[1].y, fmaf(y.z, x[2].y, fmaf(y.w, x[3].y, acc[i].y))));
+        acc[i].z = fmaf(y.x, x[0].z, fmaf(y.y, x[1].z, fmaf(y.z, x[2].z, fmaf(y.w, x[3].z, acc[i].z))));
+        acc[i].w = fmaf(y.x, x[0].w, fmaf(y.y, x[1].w, fmaf(y.z, x[2].w, fmaf(y.w, x[3].w, acc[i].w))));
       }
     }
-    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kJoinRows; ++i) {
-      e[i][d] = acc[i];
-      s[i * kGdnDim] = acc[i];
+    for (int i = 0; i < kRows; ++i)
+      *reinterpret_cast<float4*>(part + (warp * kRows + i) * kGdnDim + 4 * lane) = acc[i];
+    __syncthreads();   // P and E are done with, the parts are in place
+    fetch(fetched = g + kStages);
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const float* q = part + i * kGdnDim + d;
+      const float x = own[i] + ((q[0] + q[kRows * kGdnDim]) + (q[2 * kRows * kGdnDim] + q[3 * kRows * kGdnDim]));
+      e[i * kGdnDim + d] = x;
+      s[i * kGdnDim] = x;
     }
+    // (the next turn's barrier puts E in place before it is read)
+  }
+  if (d == 0 && *abort) {   // no copy may land after the CTA is gone
+    report_error(ca.st, kErrTimeout, 350);
+    for (int64_t g = fetched > kStages ? fetched - kStages + 1 : 1; g <= fetched && g + 1 < segs; ++g)
+      mbar_drain(&full[(g - 1) % kStages], ((g - 1) / kStages) & 1);
   }
 }
 
