@@ -32,6 +32,7 @@ struct DeltaArgs {
   int32_t num_slots;
   int32_t rows;
   int64_t tokens;           // rows of q, k, v and out
+  int32_t short_len;        // with cu: rows of at most this many tokens are taken token by token
   int32_t heads, key_heads;
   float* states;            // [num_slots][heads][128][128]
   __nv_bfloat16* out;       // [tokens][heads][128]
@@ -86,7 +87,7 @@ __global__ void __launch_bounds__(kStepThreads) k_delta_step(DeltaArgs a) {
   int64_t n;
   const int64_t t0 = delta_row_tokens(a, r, &n);
   const int slot = a.slots != nullptr ? a.slots[r] : r;
-  if (n <= 0 || slot < 0 || slot >= a.num_slots) return;
+  if (n <= 0 || (a.cu != nullptr && n > a.short_len) || slot < 0 || slot >= a.num_slots) return;
   const int kh = h / (a.heads / a.key_heads);
   float* st = a.states +
               ((static_cast<int64_t>(slot) * a.heads + h) * kGdnDim + v0) * kGdnDim + 4 * l8;
@@ -395,7 +396,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) k_delta_prep(DeltaChunkArgs c
   int64_t len;
   const int64_t begin = delta_row_tokens(a, seq, &len);
   const int64_t c = r - delta_first_record(begin, seq);
-  if (c < 0 || c * kGdnChunk >= len) return;
+  if (c < 0 || c * kGdnChunk >= len || len <= a.short_len) return;
   const int64_t t0 = begin + c * kGdnChunk;
   const int n = static_cast<int>(len - c * kGdnChunk < kGdnChunk ? len - c * kGdnChunk : kGdnChunk);
   const int h = ca.head0 + blockIdx.y, kh = h / (a.heads / a.key_heads);
@@ -839,7 +840,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
   const int nc = static_cast<int>(c1 - c0);
   const bool last = c1 == chunks;
   const int slot = a.slots != nullptr ? a.slots[row] : row;
-  bool idle = nc <= 0 || slot < 0 || slot >= a.num_slots ||
+  bool idle = nc <= 0 || len <= a.short_len || slot < 0 || slot >= a.num_slots ||
               (mode == kScanEnds && (last || (trans && seg == 0)));
   if (!idle) idle = delta_slot_taken(a, row, slot);
   if (!idle && (smem_u32(smem) & 1023u) != 0) {   // the tiles need it; the runtime places them so
