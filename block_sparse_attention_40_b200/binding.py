@@ -757,6 +757,8 @@ class DeltaExtend:
                              f"{self.heads}")
         if out is None:
             out = torch.empty_like(v)
+        if self.T == 0:
+            return out
         with _on(index):
             r = self.lib.qsa_gated_deltanet_extend(
                 q.data_ptr(), k.data_ptr(), v.data_ptr(), log_alpha.data_ptr(), beta.data_ptr(),
@@ -793,6 +795,8 @@ def gated_deltanet_step(q, k, v, log_alpha, beta, states, slots=None, counts=Non
         _is(counts, "counts", torch.int32, (B,), index)
     if out is None:
         out = torch.empty_like(v) if slots is None and counts is None else torch.zeros_like(v)
+    if B * n == 0:
+        return out
     with _on(index):
         r = load().qsa_gated_deltanet_step(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), log_alpha.data_ptr(), beta.data_ptr(), B, n,

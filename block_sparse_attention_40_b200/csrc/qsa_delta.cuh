@@ -200,7 +200,7 @@ constexpr int kRecBytes = 91136;
 constexpr int kGateQ = 0;                   // [64] e^g over the scale of the Q row
 constexpr int kGateU = 64;                  // [64] e^(g_C - g)
 constexpr int kGateC = 128;                 // e^(g_C)
-constexpr int kGateK = 129;                 // the largest |K|
+constexpr int kGateK = 129;                 // the largest |K|, times that of e^(g_C - g) where above 1
 constexpr int kGateW = 130;                 // 1 over the scale of W
 constexpr int kGateM = 192;                 // [64] 1 over the scale of the M row
 
@@ -340,7 +340,7 @@ struct PrepSmem {
   float gate[256];
   float g_hi[kGdnChunk], g_lo[kGdnChunk]; // running log gate in base 2, as a sum
   float beta[kGdnChunk], eg[kGdnChunk], beg[kGdnChunk];   // beta, e^g, their product
-  float wmax[8], kmax[4];
+  float wmax[8], kmax[4], umax;
 };
 static_assert(16384 + 4 * kGdnChunk * kPrepLdA >= 32768, "W fits");
 static_assert(sizeof(PrepSmem) <= 55 * 1024, "four CTAs an SM");
@@ -442,7 +442,14 @@ __global__ void __launch_bounds__(kPrepThreads, 4) k_delta_prep(DeltaChunkArgs c
       S.beg[t] = bt[i] * S.eg[t];
       gate[kGateU + t] = exp2f(static_cast<float>(gc - g2[i]));
     }
-    if (lane == 0) gate[kGateC] = exp2f(static_cast<float>(gc));
+    // gates above one make U' larger than U
+    float grow = fmaxf(gate[kGateU + 2 * lane], gate[kGateU + 2 * lane + 1]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) grow = fmaxf(grow, __shfl_xor_sync(0xffffffffu, grow, o));
+    if (lane == 0) {
+      gate[kGateC] = exp2f(static_cast<float>(gc));
+      S.umax = fmaxf(grow, 1.f);
+    }
   }
   cp_async_wait_all();
   __syncthreads();
@@ -703,7 +710,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) k_delta_prep(DeltaChunkArgs c
   float inv_w;
   const float sw = -row_scale(m, &inv_w);
   if (tid == 0) {
-    gate[kGateK] = fmaxf(fmaxf(S.kmax[0], S.kmax[1]), fmaxf(S.kmax[2], S.kmax[3]));
+    gate[kGateK] = S.umax * fmaxf(fmaxf(S.kmax[0], S.kmax[1]), fmaxf(S.kmax[2], S.kmax[3]));
     gate[kGateW] = inv_w;
   }
   unsigned char* w = S.k + 16384 * (warp >> 2);   // on into Tu's space
@@ -740,7 +747,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) k_delta_prep(DeltaChunkArgs c
 // space is free again as soon as their last product is done.  The chain of a chunk is S -> D_W ->
 // U' -> D_S -> S: S goes over in two parts, so that the products of one run while the other is
 // converted.  S is scaled before it is known, by a bound on its rows:
-// |S| <= e^(g_C) max|S0| + 64 max|U| max|K|.
+// |S| <= e^(g_C) max|S0| + 64 max|U| max|K| max(1, e^(g_C - g)).
 constexpr int kScanThreads = 896;
 constexpr int kScanW = 0;                               // [2] W, K, gates
 constexpr int kScanWBytes = 32768 + 16384 + 1024;

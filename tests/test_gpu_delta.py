@@ -211,6 +211,163 @@ def test_extend_contexts_in_two_graphs():
         assert torch.equal(states, want) and torch.equal(out, ref)
 
 
+# ---- sequences cut into segments, scales, neighbours -------------------------------------------
+@pytest.mark.parametrize("lens,heads", [([20000], 1), ([5000, 3100], 8), ([2500] * 3 + [40, 700], 4)])
+def test_extend_long_sequences_are_cut(lens, heads):
+    # long walks with few heads: segments from zero, transitions, joins over 4, 16 and 8 rows
+    _check_extend(lens, heads, heads, seed=40, gate=(0.97, 1.0))
+
+
+def test_extend_long_sequence_equals_its_pieces():
+    # the outputs' tolerance twice: either side is off by as much
+    T, heads = 9000, 2
+    w, states = _draw([T], heads, 1, 1, seed=41)
+    args = (w.q, w.k, w.v, w.log_alpha, w.beta)
+    one, two = states.clone(), states.clone()
+    a = qsa.gated_deltanet_extend(*args, [0, T], one)
+    b = torch.cat([qsa.gated_deltanet_extend(*[x[i:i + 1500] for x in args], [0, 1500], two)
+                   for i in range(0, T, 1500)])
+    torch.cuda.synchronize()
+    norm = max(one.norm(dim=-1).max().item(), states.norm(dim=-1).max().item())
+    assert (one - two).abs().max().item() <= 2 * STATE_TOL * norm
+    tol = 2.0 ** -7 * a.float().abs() + 2 * (STATE_TOL + 2.0 ** -10) * norm
+    assert torch.all((a.float() - b.float()).abs() <= tol)
+
+
+def test_extend_twice_is_the_same_bits():
+    w, states = _draw([3000, 40, 700], 4, 2, 3, seed=42)
+    ctx = qsa.DeltaExtend(w.cu_seqlens, 4, DEV, 2)
+    runs = []
+    for _ in range(2):
+        st = states.clone()
+        runs.append((ctx.run(w.q, w.k, w.v, w.log_alpha, w.beta, st).clone(), st))
+    assert torch.equal(runs[0][0], runs[1][0]) and torch.equal(runs[0][1], runs[1][1])
+
+
+@pytest.mark.parametrize("lens", [[1] * 40 + [100], [16, 3, 9] * 12 + [300, 64], [32, 31, 1], [7]])
+def test_extend_short_pieces(lens):
+    # token by token alone, or beside longer ones where there are many
+    _check_extend(lens, 6, 2, seed=43)
+
+
+def test_extend_no_tokens():
+    states = torch.ones((3, 2, 128, 128), device=DEV)
+    x = torch.empty((0, 2, 128), dtype=torch.bfloat16, device=DEV)
+    g = torch.empty((0, 2), device=DEV)
+    assert qsa.gated_deltanet_extend(x, x, x, g, g, [0, 0, 0], states).shape == (0, 2, 128)
+    out = qsa.gated_deltanet_step(x[None], x[None], x[None], g[None], g[None], states)
+    assert out.shape == (1, 0, 2, 128) and torch.all(states == 1)
+
+
+def test_extend_gates_above_one():
+    # alpha in (1, 1.02): what a token writes grows on its way to the chunk's end.  The recurrence
+    # multiplies every error by the same alphas as the state, so tolerances stay relative to it.
+    w, states = _draw([150], 2, 2, 1, seed=44)
+    w.log_alpha.uniform_(0.0, 0.02, generator=torch.Generator(device=DEV).manual_seed(45))
+    start = states.clone()
+    out = qsa.gated_deltanet_extend(w.q, w.k, w.v, w.log_alpha, w.beta, w.cu_seqlens, states)
+    torch.cuda.synchronize()
+    _compare(out, states[0], w, 0, 150, start[0], True)
+
+
+@pytest.mark.parametrize("scale", [1e-20, 1e-5, 1e6, 1e25])
+def test_extend_and_step_of_any_size(scale):
+    # the rule is linear in (v, S): powers of ten in, the same powers out.  The scale is a power of
+    # two, so that the unscaled run is the exact reference up to the roundings that the tolerances
+    # of _compare count for each of the two.
+    s = 2.0 ** round(np.log2(scale))
+    w, states = _draw([200], 2, 1, 1, seed=46)
+    small, big = states.clone(), states * s
+    args = (w.q, w.k)
+    a = qsa.gated_deltanet_extend(*args, w.v, w.log_alpha, w.beta, w.cu_seqlens, small)
+    b = qsa.gated_deltanet_extend(*args, (w.v.float() * s).to(torch.bfloat16), w.log_alpha, w.beta,
+                                  w.cu_seqlens, big)
+    torch.cuda.synchronize()
+    norm = small.norm(dim=-1).max().item()
+    assert (big / s - small).abs().max().item() <= 2 * STATE_TOL * norm
+    tol = 2.0 ** -7 * a.float().abs() + 2 * (STATE_TOL + 2.0 ** -10) * norm
+    assert torch.all((b.float() / s - a.float()).abs() <= tol)
+    x = [y[None, :3].contiguous() for y in (w.q, w.k, w.v, w.log_alpha, w.beta)]
+    p, q = states.clone(), states * s
+    qsa.gated_deltanet_step(*x, p)
+    x[2] = (x[2].float() * s).to(torch.bfloat16)
+    qsa.gated_deltanet_step(*x, q)
+    assert (q / s - p).abs().max().item() <= 2 * STATE_TOL * norm
+
+
+def test_extend_neighbours_stay_apart():
+    # NaN in one sequence reaches no other one, whatever shares its last chunk's rows
+    lens = [70, 100, 33, 65]
+    w, states = _draw(lens, 2, 2, 4, seed=47)
+    clean, dirty = states.clone(), states.clone()
+    a = qsa.gated_deltanet_extend(w.q, w.k, w.v, w.log_alpha, w.beta, w.cu_seqlens, clean)
+    bad = [x.clone() for x in (w.q, w.k, w.v)]
+    for x in bad:
+        x[70:170] = float("nan")
+    dirty[1] = float("inf")
+    b = qsa.gated_deltanet_extend(*bad, w.log_alpha, w.beta, w.cu_seqlens, dirty)
+    torch.cuda.synchronize()
+    assert torch.equal(a[:70], b[:70]) and torch.equal(a[170:], b[170:])
+    for s in (0, 2, 3):
+        assert torch.equal(clean[s], dirty[s])
+
+
+def test_extend_heads_in_passes():
+    # more records than one pass holds (4 GB): heads run in passes, each like heads alone
+    lens, heads = [60000, 70000, 60001], 16
+    w, states = _draw(lens, heads, heads, 3, seed=48, gate=(0.95, 1.0))
+    ctx = qsa.DeltaExtend(w.cu_seqlens, heads, DEV)
+    assert ctx.ws.numel() < sum(lens) // 64 * heads * 91136
+    got = states.clone()
+    out = ctx.run(w.q, w.k, w.v, w.log_alpha, w.beta, got)
+    torch.cuda.synchronize()
+    assert ctx.device_error() == ("QSA_OK", 0)
+    norm = got.norm(dim=-1).max().item()
+    for h in (0, 8, 15):
+        one = states[:, h:h + 1].contiguous()
+        x = [y[:, h:h + 1].contiguous() for y in (w.q, w.k, w.v, w.log_alpha, w.beta)]
+        alone = qsa.gated_deltanet_extend(*x, w.cu_seqlens, one)
+        assert (one - got[:, h:h + 1]).abs().max().item() <= 2 * STATE_TOL * norm
+        a = alone[:, 0].float()
+        tol = 2.0 ** -7 * a.abs() + 2 * (STATE_TOL + 2.0 ** -10) * norm
+        assert torch.all((a - out[:, h].float()).abs() <= tol)
+
+
+def test_extend_cut_sequence_in_a_graph_on_another_stream():
+    w, states = _draw([4000], 2, 2, 1, seed=49)
+    args = (w.q, w.k, w.v, w.log_alpha, w.beta)
+    ctx = qsa.DeltaExtend(w.cu_seqlens, 2, DEV)
+    want, start = states.clone(), states.clone()
+    ref = [ctx.run(*args, want) for _ in range(3)][-1]
+    torch.cuda.synchronize()
+    out = torch.empty_like(w.v)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        ctx.run(*args, states, out=out)
+    assert torch.equal(states, start)
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(states, want) and torch.equal(out, ref)
+
+
+def test_extend_reports_timeouts_as_ok_when_there_are_none():
+    # many contexts one after the other on one stream, their launches overlapping
+    ctxs = []
+    for seed in range(6):
+        w, states = _draw([130 + 64 * seed, 20], 2, 2, 2, seed=50 + seed)
+        ctx = qsa.DeltaExtend(w.cu_seqlens, 2, DEV)
+        start = states.clone()
+        ctxs.append((ctx, w, states, start, ctx.run(w.q, w.k, w.v, w.log_alpha, w.beta, states)))
+    torch.cuda.synchronize()
+    for ctx, w, states, start, out in ctxs:
+        assert ctx.device_error() == ("QSA_OK", 0)
+        n = int(w.cu_seqlens[1])
+        _compare(out[:n], states[0], w, 0, n, start[0], True)
+
+
 def test_binding_refusals():
     w, states = _draw([10], 4, 2, 1, seed=37)
     ctx = qsa.DeltaExtend([0, 10], 4, DEV, 2)

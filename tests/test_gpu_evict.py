@@ -207,6 +207,36 @@ def test_evict_long_row_and_many_rows():
     _check_evict([600 + 7 * i for i in range(70)], 1536, 512, 100, 1, 8, seed=51)
 
 
+@pytest.mark.parametrize("kind", ["plain", "ties", "zero"])
+def test_evict_row_over_a_cluster(kind):
+    # rows of 40,001 blocks: several CTAs each, parts that start at odd places, a short row beside
+    _check_evict([160007, 40], 160012, 0, 20001, 3, 77, kind=kind, seed=52)
+
+
+def test_evict_keeps_nearly_all_or_nearly_nothing():
+    _check_evict([60003], 60004, 512, 14999, 0, 0, seed=53)
+    _check_evict([60003], 60004, 0, 1, 0, 1, seed=54)
+    _check_evict([60003], 60004, 0, 17, 16, 0, seed=55)
+
+
+def test_evict_twice_in_a_row():
+    # the second cut finds the first one's lengths, weights and flags
+    cache = _cache([6001, 300, 2000], 6004, 0, seed=56)
+    mass = _mass((3, 1501), 57, "plain").to(DEV)
+    keys = [cache.kv_rows(b, 0, 6000)[0].clone() for b in range(3)]
+    first = qsa.Evictor(cache, 700, 1, 5, mass=mass)
+    k1 = first.evict(with_kept=True).cpu().numpy()
+    second = qsa.Evictor(cache, 300, 0, 2, mass=mass)
+    k2 = second.evict(with_kept=True).cpu().numpy()
+    torch.cuda.synchronize()
+    assert first.device_error() == second.device_error() == ("QSA_OK", 0)
+    assert cache.h_len == [1201, 300, 1200] and cache.len.tolist() == cache.h_len
+    for b in (0, 2):
+        old = [k1[b, i] if k1[b, i] >= 0 else i for i in k2[b] if i >= 0]
+        tok = torch.tensor([4 * i + j for i in old for j in range(4)], device=DEV)
+        assert torch.equal(cache.kv_rows(b, 0, 1200)[0], keys[b][tok])
+
+
 def test_evict_touches_nothing_else():
     # blocks behind the new length and other sequences' pages keep their bytes
     cache, pools = _check_evict([1000, 50], 1024, 0, 60, 1, 4)
