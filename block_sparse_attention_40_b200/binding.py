@@ -666,30 +666,44 @@ def _is(t, name, dtype, shape, index):
     raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
 
 
-def _raw_stream(index: int) -> int:
-    return torch._C._cuda_getCurrentRawStream(index)
-
-
-class _on:
-    """`with torch.cuda.device(index)` that does nothing where index is current already."""
-
-    def __init__(self, index: int):
-        self.index = index
-
-    def __enter__(self):
-        self.before = torch._C._cuda_getDevice()
-        if self.before != self.index:
-            torch._C._cuda_setDevice(self.index)
-
-    def __exit__(self, *exc):
-        if self.before != self.index:
-            torch._C._cuda_setDevice(self.before)
+def _call(name: str, index: int, *args):
+    """The library call `name` on CUDA device `index`, on its current stream; raises on a status."""
+    before = torch._C._cuda_getDevice()
+    if before != index:
+        torch._C._cuda_setDevice(index)
+    r = getattr(_lib or load(), name)(*args, torch._C._cuda_getCurrentRawStream(index))
+    if before != index:
+        torch._C._cuda_setDevice(before)
+    if r:
+        raise QSAError(name, r)
 
 
 def _delta_shapes(q, k, v, log_alpha, beta, states, slots, out, lead, rows, index):
     """Checks of the tensors that extend and step share; `lead`: the leading dimensions of the
     token tensors.  Returns (key_heads, heads)."""
     nd = len(lead)
+    try:   # all well: nothing but comparisons
+        shape, keys, bf, f32 = v.shape, q.shape, torch.bfloat16, torch.float32
+        H, Hk, D = shape[nd], keys[nd], HEAD_DIM
+        gates = shape[:nd + 1]
+        pool = states.shape
+        if (v.dtype is bf and q.dtype is bf and k.dtype is bf and log_alpha.dtype is f32
+                and beta.dtype is f32 and states.dtype is f32 and shape[:nd] == lead
+                and keys[:nd] == lead and shape[nd + 1:] == (D,) and keys[nd + 1:] == (D,)
+                and k.shape == keys and log_alpha.shape == gates and beta.shape == gates
+                and Hk > 0 and H % Hk == 0 and pool[1:] == (H, D, D)
+                and v.get_device() == q.get_device() == k.get_device() == log_alpha.get_device()
+                == beta.get_device() == states.get_device() == index >= 0
+                and v.is_contiguous() and q.is_contiguous() and k.is_contiguous()
+                and log_alpha.is_contiguous() and beta.is_contiguous() and states.is_contiguous()
+                and (pool[0] >= rows if slots is None else
+                     slots.dtype is torch.int32 and slots.shape == (rows,)
+                     and slots.get_device() == index and slots.is_contiguous())
+                and (out is None or out.dtype is bf and out.shape == shape
+                     and out.get_device() == index and out.is_contiguous())):
+            return Hk, H
+    except (AttributeError, IndexError, TypeError):
+        pass
     for name, t in (("v", v), ("q", q)):
         if not isinstance(t, torch.Tensor) or t.dim() != nd + 2:
             _need(t, name, torch.bfloat16, None, nd + 2)
@@ -759,14 +773,10 @@ class DeltaExtend:
             out = torch.empty_like(v)
         if self.T == 0:
             return out
-        with _on(index):
-            r = self.lib.qsa_gated_deltanet_extend(
-                q.data_ptr(), k.data_ptr(), v.data_ptr(), log_alpha.data_ptr(), beta.data_ptr(),
-                self.d_cu.data_ptr(), self.h_cu.data_ptr(), self.num_seqs, Hk, H,
-                states.data_ptr(), states.shape[0], _addr(slots), out.data_ptr(),
-                self.ws.data_ptr(), self.ws.numel(), _raw_stream(index))
-        if r:
-            raise QSAError("qsa_gated_deltanet_extend", r)
+        _call("qsa_gated_deltanet_extend", index, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+              log_alpha.data_ptr(), beta.data_ptr(), self.d_cu.data_ptr(), self.h_cu.data_ptr(),
+              self.num_seqs, Hk, H, states.data_ptr(), states.shape[0], _addr(slots),
+              out.data_ptr(), self.ws.data_ptr(), self.ws.numel())
         return out
 
     def device_error(self):
@@ -797,13 +807,9 @@ def gated_deltanet_step(q, k, v, log_alpha, beta, states, slots=None, counts=Non
         out = torch.empty_like(v) if slots is None and counts is None else torch.zeros_like(v)
     if B * n == 0:
         return out
-    with _on(index):
-        r = load().qsa_gated_deltanet_step(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), log_alpha.data_ptr(), beta.data_ptr(), B, n,
-            _addr(counts), Hk, H, states.data_ptr(), states.shape[0], _addr(slots),
-            out.data_ptr(), _raw_stream(index))
-    if r:
-        raise QSAError("qsa_gated_deltanet_step", r)
+    _call("qsa_gated_deltanet_step", index, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          log_alpha.data_ptr(), beta.data_ptr(), B, n, _addr(counts), Hk, H, states.data_ptr(),
+          states.shape[0], _addr(slots), out.data_ptr())
     return out
 
 
@@ -825,8 +831,7 @@ class Evictor:
         if n == 0:
             raise QSAError("qsa_evict_workspace_size", 1)
         paged = "_paged" if self._paged else ""
-        self._accumulate = getattr(self.lib, "qsa_accumulate_weights" + paged)
-        self._evict = getattr(self.lib, "qsa_evict" + paged)
+        self._accumulate, self._evict = "qsa_accumulate_weights" + paged, "qsa_evict" + paged
         shape = (cache.batch, cache.capacity // BLOCK)
         dev = cache.len.device
         if mass is None:
@@ -847,13 +852,9 @@ class Evictor:
         _is(sel_idx, "sel_idx", torch.int32, (B, sel_idx.shape[1]), index)
         _is(sel_cnt, "sel_cnt", torch.int32, (B,), index)
         desc = self.cache.desc()
-        with _on(index):
-            r = self._accumulate(
-                q.data_ptr(), ctypes.byref(desc), sel_idx.data_ptr(), sel_cnt.data_ptr(),
-                sel_idx.shape[1], self.mass.data_ptr(), self.ws.data_ptr(), self.ws.numel(),
-                _raw_stream(index))
-        if r:
-            raise QSAError(self._accumulate.__name__, r)
+        _call(self._accumulate, index, q.data_ptr(), ctypes.byref(desc), sel_idx.data_ptr(),
+              sel_cnt.data_ptr(), sel_idx.shape[1], self.mass.data_ptr(), self.ws.data_ptr(),
+              self.ws.numel())
         return self.mass
 
     def evict(self, with_kept: bool = False):
@@ -864,12 +865,8 @@ class Evictor:
         kept = (torch.empty((self.cache.batch, self.keep), dtype=torch.int32,
                             device=self.mass.device) if with_kept else None)
         desc = self.cache.desc()
-        with _on(index):
-            r = self._evict(
-                ctypes.byref(desc), self.mass.data_ptr(), self.keep, self.sinks, self.recent,
-                _addr(kept), self.ws.data_ptr(), self.ws.numel(), _raw_stream(index))
-        if r:
-            raise QSAError(self._evict.__name__, r)
+        _call(self._evict, index, ctypes.byref(desc), self.mass.data_ptr(), self.keep, self.sinks,
+              self.recent, _addr(kept), self.ws.data_ptr(), self.ws.numel())
         self.cache.h_len = [BLOCK * self.keep + n % BLOCK if n // BLOCK > self.keep else n
                             for n in self.cache.h_len]
         return kept
