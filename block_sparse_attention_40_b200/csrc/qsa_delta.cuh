@@ -227,6 +227,11 @@ struct DeltaChunkArgs {
   DevStatus st;
 };
 
+// Instruction descriptor: kind::f16 with f16 A/B, fp32 D, dense.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int a_mn_major, int b_mn_major) {
+  return idesc_bf16_f32(M, N, a_mn_major, b_mn_major) & ~((1u << 7) | (1u << 10));
+}
+
 // x -= lo(h), y -= hi(h): one mixed-precision instruction each
 __device__ __forceinline__ void take_bf16x2(uint32_t h, float* x, float* y) {
   asm("{\n\t.reg .b16 l, h, m;\n\tmov.b32 {l, h}, %2;\n\tmov.b16 m, 0xBF80;\n\t"

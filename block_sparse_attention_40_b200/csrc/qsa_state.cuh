@@ -1,0 +1,436 @@
+// qsa_state.cuh -- C ABI of the two memories of a decoding hybrid stack: the gated delta rule from
+// and to a pool of states (extend, step), and eviction from a decode cache by accumulated attention
+// weight.  Included behind qsa_api.cu, whose helpers (workspace carving, cache views, launches)
+// it uses.
+
+#pragma once
+
+#include <cmath>
+
+#include "qsa_delta.cuh"
+#include "qsa_evict.cuh"
+
+namespace {
+// Launches a kernel in clusters of c CTAs along x.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, int c,
+                           cudaStream_t s, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = c;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+}  // namespace
+
+// ---- the gated delta rule from and to a pool of states ---------------------------------------
+namespace {
+// Arguments that extend and step share.
+qsa_status delta_args(const void* q, const void* k, const void* v, const float* log_alpha,
+                      const float* beta, int32_t rows, int32_t key_heads, int32_t heads,
+                      float* states, int32_t num_slots, const int32_t* slots, void* out,
+                      DeltaArgs* a) {
+  for (const void* p : {q, k, v, static_cast<const void*>(states), static_cast<const void*>(out)}) {
+    if (!p) return QSA_ERR_INVALID_ARG;
+    if (!aligned16(p)) return QSA_ERR_ALIGNMENT;
+  }
+  if (!log_alpha || !beta) return QSA_ERR_INVALID_ARG;
+  for (const void* p : {static_cast<const void*>(log_alpha), static_cast<const void*>(beta),
+                        static_cast<const void*>(slots)})
+    if (reinterpret_cast<uintptr_t>(p) % 4 != 0) return QSA_ERR_ALIGNMENT;
+  if (rows < 1 || rows > 65535 || heads < 1 || heads > 256 || key_heads < 1 ||
+      heads % key_heads != 0 || num_slots < 1)
+    return QSA_ERR_INVALID_ARG;
+  if (!slots && num_slots < rows) return QSA_ERR_INVALID_ARG;
+  a->q = static_cast<const __nv_bfloat16*>(q);
+  a->k = static_cast<const __nv_bfloat16*>(k);
+  a->v = static_cast<const __nv_bfloat16*>(v);
+  a->log_alpha = log_alpha;
+  a->beta = beta;
+  a->slots = slots;
+  a->num_slots = num_slots;
+  a->rows = rows;
+  a->heads = heads;
+  a->key_heads = key_heads;
+  a->states = states;
+  a->out = static_cast<__nv_bfloat16*>(out);
+  return QSA_OK;
+}
+
+qsa_status launch_delta_step(const DeltaArgs& a, cudaStream_t s) {
+  k_delta_step<2><<<dim3(a.heads, a.rows, 4), kStepThreads, 0, s>>>(a);
+  QSA_CHECK_LAUNCH();
+  return QSA_OK;
+}
+
+qsa_status extend_check_cu(const int32_t* h_cu, int32_t num_seqs) {
+  if (!h_cu || num_seqs < 1 || num_seqs > 65535 || h_cu[0] != 0) return QSA_ERR_INVALID_ARG;
+  for (int32_t i = 0; i < num_seqs; ++i)
+    if (h_cu[i + 1] < h_cu[i]) return QSA_ERR_INVALID_ARG;
+  return QSA_OK;
+}
+
+// How a call of extend runs: heads in passes that keep the records within a budget, and long
+// sequences cut into segments of seg_chunks chunks where that fills the SMs better.
+struct ExtendPlan {
+  int64_t records = 0, max_chunks = 0, seg_slots = 0;
+  int32_t pass_heads = 1, seg_chunks = 1, segs = 1;
+  int32_t short_len = 0;   // pieces of at most this many tokens go token by token
+  size_t o_rec = 0, o_state = 0, o_trans = 0, total = 0;
+};
+
+// Where a call has no longer pieces than 32 tokens, all go token by token (a piece of 30 tokens x 4
+// heads: 12.5 us against 26.6 by chunks).  Beside longer pieces, those of at most 16 do where
+// they would fill the SMs by themselves, since a walk by chunks holds an SM for 10 us (48 pieces of
+// 1 to 64 tokens x 16 heads: 95 us against 132); fewer ride along (7 pieces, one of 1 token, x 4
+// heads: 65.6 us against 69.7 with a launch more).
+constexpr int32_t kShortAll = 32, kShortMany = 16;
+constexpr int64_t kRecordBudget = int64_t(1) << 32;
+
+// Rows of a state that a CTA of the join takes: as few as leave the grid in one wave.
+int join_rows(int64_t heads_seqs) {
+  int rows = 4;
+  while (rows < 16 && heads_seqs * (kGdnDim / rows) > num_sms()) rows *= 2;
+  return rows;
+}
+
+void extend_plan(const int32_t* h_cu, int32_t num_seqs, int32_t heads, ExtendPlan* p) {
+  const int64_t tokens = h_cu[num_seqs];
+  p->records = tokens / kGdnChunk + num_seqs;
+  const int64_t per_head = p->records * kRecBytes;
+  int64_t hp = std::max<int64_t>(1, std::min<int64_t>(heads, kRecordBudget / per_head));
+  const int64_t passes = (heads + hp - 1) / hp;
+  hp = (heads + passes - 1) / passes;
+  p->pass_heads = static_cast<int32_t>(hp);
+  int64_t short_rows = 0, longest = 0;
+  for (int32_t i = 0; i < num_seqs; ++i) {
+    const int64_t len = int64_t(h_cu[i + 1]) - h_cu[i];
+    longest = std::max(longest, len);
+    short_rows += len > 0 && len <= kShortMany;
+  }
+  p->short_len = longest <= kShortAll ? kShortAll
+                 : short_rows * heads >= num_sms() ? kShortMany : 0;
+  int64_t total = 0;
+  for (int32_t i = 0; i < num_seqs; ++i) {
+    const int64_t len = int64_t(h_cu[i + 1]) - h_cu[i];
+    if (len <= p->short_len) continue;
+    const int64_t nc = (len + kGdnChunk - 1) / kGdnChunk;
+    p->max_chunks = std::max(p->max_chunks, nc);
+    total += nc;
+  }
+  // Microseconds of the scan, uncut and cut into about k segments: the longest walk, or all walks
+  // in waves over the SMs, at what a chunk was measured to take (2.65 with outputs, 2.4 without),
+  // and what a launch and a step of the join were.  Cut, all segments but the last run first
+  // without outputs (from zero, and their transitions), then all run with outputs.
+  const double sms = num_sms();
+  // (a CTA takes 8 until its first chunk)
+  auto waves_of = [&](double l, double all, double chunk) {
+    return std::ceil(std::max(1.0, all / sms / l)) * (8 + chunk * l);
+  };
+  double best = 10 + 2.65 * std::max(double(p->max_chunks), double(total) * hp / sms);
+  int64_t L = std::max<int64_t>(1, p->max_chunks);
+  for (int64_t k = 3; k <= 512 && k <= p->max_chunks / 2; k += 1 + k / 16) {
+    const int64_t l = (p->max_chunks + k - 1) / k;
+    double inner = 0;
+    for (int32_t i = 0; i < num_seqs; ++i) {
+      const int64_t nc = (int64_t(h_cu[i + 1]) - h_cu[i] + kGdnChunk - 1) / kGdnChunk;
+      const int64_t segs = (nc + l - 1) / l;
+      if (segs > 1) inner += double((2 * segs - 3) * l);
+    }
+    const int rows = join_rows(int64_t(num_seqs) * hp);
+    const double waves = std::ceil(double(num_seqs) * hp * (kGdnDim / rows) / sms);
+    const double t = waves_of(double(l), inner * hp, 2.4) + waves * (6 + double(k) * 0.9) + 8 +
+                     waves_of(double(l), double(total) * hp, 2.65);
+    if (t < best) {
+      best = t;
+      L = l;
+    }
+  }
+  p->seg_chunks = static_cast<int32_t>(L);
+  p->segs = static_cast<int32_t>((p->max_chunks + L - 1) / L);
+  Carver cv;
+  p->o_rec = cv.take(static_cast<size_t>(per_head * hp));
+  if (p->segs > 1) {
+    p->seg_slots = p->records / L + num_seqs;
+    const size_t bytes = static_cast<size_t>(p->seg_slots) * hp * kGdnDim * kGdnDim * 4;
+    p->o_state = cv.take(bytes);
+    p->o_trans = cv.take(bytes);
+  }
+  p->total = cv.off;
+}
+}  // namespace
+
+extern "C" size_t qsa_gated_deltanet_extend_workspace_size(const int32_t* h_cu_seqlens,
+                                                           int32_t num_seqs, int32_t key_heads,
+                                                           int32_t heads) {
+  if (extend_check_cu(h_cu_seqlens, num_seqs) != QSA_OK || heads < 1 || heads > 256 ||
+      key_heads < 1 || heads % key_heads != 0)
+    return 0;
+  ExtendPlan p;
+  extend_plan(h_cu_seqlens, num_seqs, heads, &p);
+  return p.total;
+}
+
+extern "C" qsa_status qsa_gated_deltanet_extend(
+    const void* q, const void* k, const void* v, const float* log_alpha, const float* beta,
+    const int32_t* d_cu_seqlens, const int32_t* h_cu_seqlens, int32_t num_seqs, int32_t key_heads,
+    int32_t heads, float* states, int32_t num_slots, const int32_t* slots, void* out,
+    void* workspace, size_t ws_bytes, qsa_stream_t stream) {
+  DeltaChunkArgs a{};
+  qsa_status st = extend_check_cu(h_cu_seqlens, num_seqs);
+  if (st == QSA_OK)
+    st = delta_args(q, k, v, log_alpha, beta, num_seqs, key_heads, heads, states, num_slots, slots,
+                    out, &a.d);
+  if (st != QSA_OK) return st;
+  if (!d_cu_seqlens || !workspace) return QSA_ERR_INVALID_ARG;
+  if (!aligned16(workspace) || reinterpret_cast<uintptr_t>(d_cu_seqlens) % 4 != 0)
+    return QSA_ERR_ALIGNMENT;
+  ExtendPlan p;
+  extend_plan(h_cu_seqlens, num_seqs, heads, &p);
+  if (ws_bytes < p.total) return QSA_ERR_WORKSPACE;
+  a.d.cu = d_cu_seqlens;
+  a.d.tokens = h_cu_seqlens[num_seqs];
+  a.d.short_len = p.short_len;
+  if (a.d.tokens == 0) return QSA_OK;
+  if (p.short_len > 0) {
+    st = launch_delta_step(a.d, reinterpret_cast<cudaStream_t>(stream));
+    if (st != QSA_OK) return st;
+  }
+  if (p.max_chunks == 0) return QSA_OK;
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  a.rec = ws + p.o_rec;
+  a.records = p.records;
+  a.seg_chunks = p.seg_chunks;
+  a.seg_slots = p.seg_slots;
+  if (p.segs > 1) {
+    a.seg_state = reinterpret_cast<float*>(ws + p.o_state);
+    a.seg_trans = reinterpret_cast<float*>(ws + p.o_trans);
+  }
+  a.st = dev_status(workspace);
+  ScanMaps maps;
+  {
+    const uint32_t box[3] = {64, 1, kGdnChunk};
+    const uint64_t tok = static_cast<uint64_t>(a.d.tokens);
+    const uint64_t kd[3] = {kGdnDim, static_cast<uint64_t>(key_heads), tok};
+    const uint64_t ks[2] = {kGdnDim * 2, static_cast<uint64_t>(key_heads) * kGdnDim * 2};
+    if (!make_tmap(&maps.k, k, 3, kd, ks, box)) return QSA_ERR_CUDA;
+  }
+  const int prep_smem = static_cast<int>(sizeof(PrepSmem));
+  if (!set_smem(k_delta_prep, prep_smem) || !set_smem(k_delta_scan, kScanSmemBytes) ||
+      !set_smem(k_delta_join<4>, join_smem_bytes(4)) || !set_smem(k_delta_join<8>, join_smem_bytes(8)) ||
+      !set_smem(k_delta_join<16>, join_smem_bytes(16)))
+    return QSA_ERR_CUDA;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  for (int32_t h0 = 0; h0 < heads; h0 += p.pass_heads) {
+    a.head0 = h0;
+    a.nheads = std::min(p.pass_heads, heads - h0);
+    k_delta_prep<<<dim3(static_cast<unsigned>(p.records), a.nheads), kPrepThreads, prep_smem, s>>>(a);
+    QSA_CHECK_LAUNCH();
+    // each of these sets up while the one before it finishes
+    if (p.segs > 1) {
+      QSA_CHECK_PDL(launch_pdl(k_delta_scan, dim3(a.nheads, num_seqs, 2 * (p.segs - 1)),
+                               dim3(kScanThreads), kScanSmemBytes, s, maps, a, kScanEnds));
+      if (p.segs > 2) {
+        const int rows = join_rows(int64_t(a.nheads) * num_seqs);
+        QSA_CHECK_PDL(launch_pdl(rows == 4 ? k_delta_join<4> : rows == 8 ? k_delta_join<8> : k_delta_join<16>,
+                                 dim3(a.nheads, num_seqs, kGdnDim / rows), dim3(kJoinThreads),
+                                 join_smem_bytes(rows), s, a));
+      }
+    }
+    QSA_CHECK_PDL(launch_pdl(k_delta_scan, dim3(a.nheads, num_seqs, p.segs), dim3(kScanThreads),
+                             kScanSmemBytes, s, maps, a, p.segs > 1 ? kScanOutputs : kScanWhole));
+  }
+  return QSA_OK;
+}
+
+extern "C" qsa_status qsa_gated_deltanet_step(const void* q, const void* k, const void* v,
+                                              const float* log_alpha, const float* beta,
+                                              int32_t batch, int32_t n_new, const int32_t* counts,
+                                              int32_t key_heads, int32_t heads, float* states,
+                                              int32_t num_slots, const int32_t* slots, void* out,
+                                              qsa_stream_t stream) {
+  DeltaArgs a{};
+  const qsa_status st = delta_args(q, k, v, log_alpha, beta, batch, key_heads, heads, states,
+                                   num_slots, slots, out, &a);
+  if (st != QSA_OK) return st;
+  if (n_new < 0) return QSA_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(counts) % 4 != 0) return QSA_ERR_ALIGNMENT;
+  if (n_new == 0) return QSA_OK;
+  a.n_new = n_new;
+  a.counts = counts;
+  a.tokens = static_cast<int64_t>(batch) * n_new;
+  return launch_delta_step(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+// ---- eviction by accumulated attention weight --------------------------------------------------
+namespace {
+qsa_status check_cache_geom(const qsa_cache* c) {
+  if (!c || c->batch <= 0 || c->batch > 65535 || c->capacity <= 0 || c->capacity % 4 != 0 ||
+      c->capacity > QSA_MAX_SEQ_LEN)
+    return QSA_ERR_INVALID_ARG;
+  return QSA_OK;
+}
+
+qsa_status weights_impl(const void* q, const CacheView& view, const int32_t* sel_idx,
+                        const int32_t* sel_cnt, int32_t topk, float* mass, void* workspace,
+                        size_t ws_bytes, qsa_stream_t stream) {
+  const qsa_cache* c = view.c;
+  qsa_status st = check_cache_geom(c);
+  if (st != QSA_OK) return st;
+  st = check_prefill_ptrs({q, c->k_blocks, c->len, sel_idx, sel_cnt, mass, workspace});
+  if (st != QSA_OK) return st;
+  if (topk < 1 || topk > QSA_MAX_TOPK) return QSA_ERR_INVALID_ARG;
+  if (ws_bytes < QSA_WS_HEADER_BYTES) return QSA_ERR_WORKSPACE;
+  WeightArgs a{};
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.k_blocks = static_cast<const __nv_bfloat16*>(c->k_blocks);
+  a.len = c->len;
+  a.idx = sel_idx;
+  a.cnt = sel_cnt;
+  a.topk = topk;
+  a.cap_blocks = c->capacity / kBlock;
+  a.mass = mass;
+  a.pg = view.pg;
+  a.st = dev_status(workspace);
+  // as many CTAs to a sequence as keep the grid within two CTAs an SM
+  // (and at least a tile to a warp)
+  int cluster = kWtMaxCluster;
+  while (cluster > 1 && (int64_t(cluster) * c->batch > 2 * num_sms() ||
+                         wt_tiles_per_cta(topk, cluster) < kWtWarps / 2))
+    cluster /= 2;
+  if (cudaFuncSetAttribute(k_block_weights, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+      cudaSuccess)
+    return QSA_ERR_CUDA;
+  const int smem = wt_smem_bytes(topk, cluster);
+  if (!set_smem(k_block_weights, smem)) return QSA_ERR_CUDA;
+  QSA_CHECK_PDL(launch_cluster(k_block_weights, dim3(cluster, c->batch), dim3(kWtThreads), smem,
+                               cluster, reinterpret_cast<cudaStream_t>(stream), a));
+  return QSA_OK;
+}
+
+struct EvictGeom {
+  size_t o_meta = 0, o_src = 0, o_loaded = 0, o_before = 0, o_ticket = 0, total = 0;
+  int32_t tiles = 0;
+};
+
+qsa_status evict_geom(const qsa_cache* c, int32_t keep, int32_t sinks, int32_t recent,
+                      EvictGeom* g) {
+  const qsa_status st = check_cache_geom(c);
+  if (st != QSA_OK) return st;
+  if (keep < 1 || keep > QSA_MAX_SEQ_LEN / 4 || sinks < 0 || recent < 0 || sinks > keep ||
+      recent > keep - sinks)
+    return QSA_ERR_INVALID_ARG;
+  Carver cv;
+  g->o_meta = cv.take(static_cast<size_t>(c->batch) * sizeof(EvictMeta));
+  g->o_src = cv.take(static_cast<size_t>(c->batch) * (static_cast<size_t>(keep) + 1) * 4);
+  // a cache that cannot hold more than keep complete blocks has nothing to move
+  g->tiles = c->capacity / kBlock > keep ? keep / kMvPlaces + 1 : 0;
+  g->o_loaded = cv.take(static_cast<size_t>(c->batch) * g->tiles * 4);
+  g->o_before = cv.take(static_cast<size_t>(c->batch) * (g->tiles + 1) * 4);
+  g->o_ticket = cv.take(4);
+  g->total = cv.off;
+  return QSA_OK;
+}
+
+qsa_status evict_impl(const CacheView& view, float* mass, int32_t keep, int32_t sinks,
+                      int32_t recent, int32_t* kept, void* workspace, size_t ws_bytes,
+                      qsa_stream_t stream) {
+  const qsa_cache* c = view.c;
+  EvictGeom g;
+  qsa_status st = evict_geom(c, keep, sinks, recent, &g);
+  if (st != QSA_OK) return st;
+  st = check_prefill_ptrs({c->k_blocks, c->v_blocks, c->kbar, c->len, mass, workspace});
+  if (st != QSA_OK) return st;
+  if (kept && !aligned16(kept)) return QSA_ERR_ALIGNMENT;
+  if (ws_bytes < g.total) return QSA_ERR_WORKSPACE;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  EvictArgs a{};
+  a.len = c->len;
+  a.mass = mass;
+  a.cap_blocks = c->capacity / kBlock;
+  a.batch = c->batch;
+  a.keep = keep;
+  a.sinks = sinks;
+  a.recent = recent;
+  a.kept = kept;
+  a.src = reinterpret_cast<int32_t*>(ws + g.o_src);
+  a.meta = reinterpret_cast<EvictMeta*>(ws + g.o_meta);
+  a.k_blocks = static_cast<uint4*>(c->k_blocks);
+  a.v_blocks = static_cast<uint4*>(c->v_blocks);
+  a.kbar = static_cast<uint4*>(c->kbar);
+  a.pg = view.pg;
+  a.st = dev_status(workspace);
+  a.tiles = g.tiles;
+  a.loaded = reinterpret_cast<int32_t*>(ws + g.o_loaded);
+  a.before = reinterpret_cast<int32_t*>(ws + g.o_before);
+  a.ticket = reinterpret_cast<int32_t*>(ws + g.o_ticket);
+  // as many CTAs to a sequence as the SMs hold, with at least 4,096 weights each (a batch of four
+  // per thread): below that the cluster's barriers cost more than its reads
+  int cluster = kEvMaxCluster;
+  while (cluster > 1 && (int64_t(cluster) * c->batch > num_sms() ||
+                         a.cap_blocks / cluster < kEvThreads * kEvBatch))
+    cluster /= 2;
+  if (cudaFuncSetAttribute(k_evict_select, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+    return QSA_ERR_CUDA;
+  QSA_CHECK_PDL(launch_cluster(k_evict_select, dim3(cluster, c->batch), dim3(kEvThreads), 0, cluster, s, a));
+  if (g.tiles > 0)
+    QSA_CHECK_PDL(launch_pdl(k_evict_move, dim3(static_cast<unsigned>(g.tiles) * c->batch),
+                             dim3(kMvThreads), 0, s, a));
+  return QSA_OK;
+}
+}  // namespace
+
+extern "C" {
+
+qsa_status qsa_accumulate_weights(const void* q, const qsa_cache* cache, const int32_t* sel_idx,
+                                  const int32_t* sel_cnt, int32_t topk, float* mass,
+                                  void* workspace, size_t ws_bytes, qsa_stream_t stream) {
+  if (!cache) return QSA_ERR_INVALID_ARG;
+  return weights_impl(q, contiguous_view(cache), sel_idx, sel_cnt, topk, mass, workspace, ws_bytes,
+                      stream);
+}
+
+qsa_status qsa_accumulate_weights_paged(const void* q, const qsa_paged_cache* cache,
+                                        const int32_t* sel_idx, const int32_t* sel_cnt,
+                                        int32_t topk, float* mass, void* workspace,
+                                        size_t ws_bytes, qsa_stream_t stream) {
+  CacheView view;
+  const qsa_status st = paged_view(cache, &view);
+  if (st != QSA_OK) return st;
+  return weights_impl(q, view, sel_idx, sel_cnt, topk, mass, workspace, ws_bytes, stream);
+}
+
+size_t qsa_evict_workspace_size(const qsa_cache* cache, int32_t keep_blocks, int32_t sink_blocks,
+                                int32_t recent_blocks) {
+  EvictGeom g;
+  return evict_geom(cache, keep_blocks, sink_blocks, recent_blocks, &g) == QSA_OK ? g.total : 0;
+}
+
+qsa_status qsa_evict(const qsa_cache* cache, float* mass, int32_t keep_blocks, int32_t sink_blocks,
+                     int32_t recent_blocks, int32_t* kept, void* workspace, size_t ws_bytes,
+                     qsa_stream_t stream) {
+  if (!cache) return QSA_ERR_INVALID_ARG;
+  return evict_impl(contiguous_view(cache), mass, keep_blocks, sink_blocks, recent_blocks, kept,
+                    workspace, ws_bytes, stream);
+}
+
+qsa_status qsa_evict_paged(const qsa_paged_cache* cache, float* mass, int32_t keep_blocks,
+                           int32_t sink_blocks, int32_t recent_blocks, int32_t* kept,
+                           void* workspace, size_t ws_bytes, qsa_stream_t stream) {
+  CacheView view;
+  const qsa_status st = paged_view(cache, &view);
+  if (st != QSA_OK) return st;
+  return evict_impl(view, mass, keep_blocks, sink_blocks, recent_blocks, kept, workspace, ws_bytes,
+                    stream);
+}
+
+}  // extern "C"
