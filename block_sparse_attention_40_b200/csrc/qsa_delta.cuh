@@ -1,5 +1,6 @@
 // qsa_delta.cuh -- the gated delta rule from and to a pool of states: token by token for
-// decoding rows.  (The layer over whole sequences from a zero state is in qsa_gdn.cuh.)
+// decoding rows, in chunks for pieces of prompts.  (The layer over whole sequences from a zero
+// state is in qsa_gdn.cuh.)
 //
 // Per row (sequence) and value head, with the state S (d_v x d_k, fp32) kept in a slot of a
 // caller-owned pool [slots][heads][128 (v)][128 (k)]:
@@ -75,8 +76,10 @@ __device__ __forceinline__ void unpack_bf16x2(uint32_t w, float* f) {
 // threads holds 16 * RV rows and the grid (heads, rows, 128 / (16 RV)) covers S.  The state
 // stays in registers over a row's tokens: it is read once and written once.  With
 // o = a S q + u (k.q), u = beta (v - a S k), both dots of a token come from the old state in one
-// pass, and the reductions are three shuffles.  Bound by the state's bytes: 128 KB per (row,
-// head) against about 4.5 KB of everything else at one token.
+// pass, and the reductions are three shuffles.  A token's inputs are fetched while the one before
+// it is taken.  Bound by the state's bytes: 128 KB per (row, head) against about 4.5 KB of
+// everything else at one token.  64 rows x 32 heads x 1 token: 45 us, 6.0 TB/s, 92% of the measured
+// copy rate; 24 rows of up to 5 tokens x 16 heads: 10.3 us (its states' bytes take 6.9).
 constexpr int kStepThreads = 128;
 
 template <int RV>
@@ -177,9 +180,13 @@ __global__ void __launch_bounds__(kStepThreads) k_delta_step(DeltaArgs a) {
 //     T = Tu diag(beta),   W = T diag(e^g) K,   U = T V - W S0^T      (what the tokens write)
 //     O = diag(e^g) Q S0^T + M U,   M_tj = e^(g_t - g_j) q_t.k_j  for j <= t
 //     S = e^(g_C) S0 + (diag(e^(g_C - g)) U)^T K.
-// T, W and M do not depend on the state: k_delta_prep forms them for every chunk and head at
+// T V, W and M do not depend on the state: k_delta_prep forms them for every chunk and head at
 // once and leaves them in a record; k_delta_scan walks the chunks in order with two dependent
-// products a chunk (W S0^T, then U^T K) on the tcgen05 tensor cores.
+// products a chunk (W S0^T, then U^T K) on the tcgen05 tensor cores.  Where the walks do not fill
+// the SMs, sequences are cut into segments: a segment is affine in the state it is entered with,
+// E -> E P + S, so a first pass of the scan finds S (from zero) and P (from the identity, without
+// writes) of all segments at once, k_delta_join takes the states through them, and a second pass
+// writes the outputs.
 //
 // q, k and v are bf16 and exact as operands; the fp32 operands go in as parts.  What a token
 // writes carries T and U straight into the state: three bf16 parts each, x = hi + mid + lo to
@@ -333,9 +340,13 @@ __device__ __forceinline__ void bulk_store_wait() {
 }
 
 // ---- k_delta_prep: one CTA of 256 threads per (record, head) ---------------------------------
-// Bound by its shared memory accesses and the latency of its steps, so four CTAs share an SM; the
-// record leaves in pieces, out of the space of an operand that is done with: Q becomes the scaled
-// fp16 Q in place, then holds M, then V; K and Tu become W.
+// Warp MMAs, since the parts between the products (decays, the inverse by 16 x 16 blocks, the
+// splits into parts) outweigh them and take registers, and since with four CTAs an SM the phases
+// of one fill the gaps of another.  The record leaves in pieces, out of the space of an operand
+// that is done with: Q becomes the scaled fp16 Q in place, then holds M, then V; K and Tu become W.
+// 16,384 chunks (8 x 8,192 tokens x 16 heads): 580 us, 5.2 us of an SM a chunk, bound by shared
+// memory (68% of its cycles; instructions issue in 54%; three CTAs an SM take as long); the bytes
+// (48 KB in, 89 KB out) would take 343 us.
 constexpr int kPrepThreads = 256;
 constexpr int kPrepLdA = kGdnChunk + 8;   // fp32 row stride of L / Tu: 8 rows x 4 pairs without conflicts
 struct PrepSmem {
@@ -747,12 +758,19 @@ __global__ void __launch_bounds__(kPrepThreads, 4) k_delta_prep(DeltaChunkArgs c
 //     D_Q [v][t] = S0 Q^T, then U^T M^T
 //     D_S [v][d] = U'^T K,  U' = diag(e^(g_C - g)) U,  U = (T V)^T + D_W
 // Four warpgroups hold the fp32 state in registers (a lane has one v, 32 of its d's), form U and
-// U' and then S: what a chunk takes is their latency, and four warps a scheduler hide most of it.
-// Two write the outputs.  Three warps load, each its own operands, whose
-// space is free again as soon as their last product is done.  The chain of a chunk is S -> D_W ->
-// U' -> D_S -> S: S goes over in two parts, so that the products of one run while the other is
-// converted.  S is scaled before it is known, by a bound on its rows:
-// |S| <= e^(g_C) max|S0| + 64 max|U| max|K| max(1, e^(g_C - g)).
+// U' and then S; two write the outputs; one warp issues the products and three load, each its own
+// operands, whose space is free again as soon as their last product is done.
+//
+// Bound by the chain of a chunk, S -> D_W -> U' -> D_S -> S, 4,700 cycles (2.65 us): about 1,000
+// for D_W (16 products of 128 x 64 or 128 x 128 x 16), 1,150 for U', 1,000 for D_S (12 of 128 x 128
+// x 16), 1,600 for S, most of whose conversion is instruction issue (two products' parts, 5 to 9
+// instructions an element).  S goes over in two parts, so that the products of one run while the
+// other is converted; S is scaled before it is known, by a bound on its rows,
+// |S| <= e^(g_C) max|S0| + 64 max|U| max|K| max(1, e^(g_C - g)); what only the outputs need (D_Q)
+// runs in the gaps.  A form without W (X = V - e^g K S0^T, U = T X) would read 32 KB less a chunk
+// and have one more product and conversion in the chain.  8 x 8,192 tokens x 16 heads: 387 us on 128
+// SMs (121 KB a chunk: 5.1 TB/s); the same walk with fp32 state in shared memory and warp MMAs
+// (k_gated_deltanet, preparation included) takes 2.6 ms.
 constexpr int kScanThreads = 896;
 constexpr int kScanW = 0;                               // [2] W, K, gates
 constexpr int kScanWBytes = 32768 + 16384 + 1024;
@@ -1313,7 +1331,8 @@ __global__ void __launch_bounds__(kScanThreads, 1)
 // E P + S.  Rows of the state are independent: a CTA takes kRows of them through the segments in
 // order.  A warp takes 32 of the 128 terms of every product and a lane four columns, so that P
 // leaves shared memory once (64 KB, 512 cycles, which is what a step of four or eight rows is
-// bound by); the warps' parts are added in order.  The P of the next segments are on their way.
+// bound by); the warps' parts are added in order.  The P of the next segments are on their way: at
+// one head its 64 KB a step (1.0 us measured) are what an SM takes in from L2.
 constexpr int kJoinThreads = 128;
 constexpr int join_stages(int rows) { return rows > 8 ? 2 : 3; }
 constexpr int join_smem_bytes(int rows) {
