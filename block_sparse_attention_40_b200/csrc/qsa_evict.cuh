@@ -28,12 +28,10 @@ namespace qsa {
 // leaves one number, the log2 of the sum of its 4 exponentials, in shared memory; the heads'
 // totals are then joined over the CTA and the cluster (distributed shared memory) in a fixed
 // order, and each block's weight is the sum over heads of 2^(block's log-sum - head's total): one
-// pass over the keys and no second launch.  64 sequences of 32K tokens, 4,096-token pages: 19.5 us,
-// 3.5 TB/s (the keys would take 10.4); one sequence: 10.4 us, all latency (idx -> page -> keys,
-// two barriers of the cluster).
-constexpr int kWtThreads = 256;
-constexpr int kWtWarps = kWtThreads / 32;
-constexpr int kWtMaxCluster = 16;
+// pass over the keys and no second launch.  64 sequences of 32K tokens, 4,096-token pages: 19.0 us,
+// 3.6 TB/s (the keys would take 10.4); one sequence: 9 us, all latency (idx -> page -> keys, two
+// barriers of the cluster).
+constexpr int kWtMaxCluster = 8;
 
 struct WeightArgs {
   const __nv_bfloat16* q;         // [B][24][128]
@@ -78,7 +76,9 @@ __host__ __device__ constexpr int wt_smem_bytes(int topk, int c) {
 }
 
 // grid (C, B), clusters of (C, 1, 1)
+template <int kWtThreads>
 __global__ void __launch_bounds__(kWtThreads) k_block_weights(WeightArgs a) {
+  constexpr int kWtWarps = kWtThreads / 32;
   namespace cg = cooperative_groups;
   cg::cluster_group cl = cg::this_cluster();
   extern __shared__ float lse_sh[];                   // [local item][25]
