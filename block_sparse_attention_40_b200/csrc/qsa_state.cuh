@@ -374,10 +374,12 @@ qsa_status evict_impl(const CacheView& view, float* mass, int32_t keep, int32_t 
   a.loaded = reinterpret_cast<int32_t*>(ws + g.o_loaded);
   a.before = reinterpret_cast<int32_t*>(ws + g.o_before);
   a.ticket = reinterpret_cast<int32_t*>(ws + g.o_ticket);
-  // as many CTAs to a sequence as the SMs hold, with at least 4,096 weights each (a batch of four
-  // per thread): below that the cluster's barriers cost more than its reads
+  // As many CTAs to a sequence as the SMs hold, with at least 4,096 weights each (four a thread):
+  // below that the cluster's barriers cost more than its reads.  A CTA fills an SM, and a GPC has
+  // room for one cluster of 16, so those are for few sequences (four of 262,140 tokens cut to almost
+  // all: 112 us against 117 with eight; eight: 213 against 199).
   int cluster = kEvMaxCluster;
-  while (cluster > 1 && (int64_t(cluster) * c->batch > num_sms() ||
+  while (cluster > 1 && (int64_t(cluster) * c->batch > (cluster > 8 ? num_sms() / 2 : num_sms()) ||
                          a.cap_blocks / cluster < kEvThreads * kEvBatch))
     cluster /= 2;
   if (cudaFuncSetAttribute(k_evict_select, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
