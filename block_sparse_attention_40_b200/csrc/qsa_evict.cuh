@@ -374,11 +374,13 @@ __global__ void __launch_bounds__(kEvThreads, 1) k_evict_select(EvictArgs a) {
   int32_t* kept = a.kept != nullptr ? a.kept + static_cast<int64_t>(b) * a.keep : nullptr;
   const int gtid = rank * kEvThreads + tid, gthreads = C * kEvThreads;
   for (int i = gtid; i < a.tiles; i += gthreads) a.loaded[static_cast<int64_t>(b) * a.tiles + i] = 0;
-  if (gtid == 0) before[a.tiles] = a.keep + 1;   // where the sequence ends below
+  // (a sequence that ends below the tiles' end: no block of it writes the last entry)
+  if (gtid == 0 && nb < a.tiles * kMvPlaces) before[a.tiles] = a.keep + 1;
   if (b == 0 && gtid == 0) *a.ticket = 0;
-  if (len < 0 || nb > a.cap_blocks || nb <= a.keep) {   // nothing to cut (or a length out of range)
+  const bool bad = len < 0 || len > a.cap_blocks * kBlock;
+  if (bad || nb <= a.keep) {   // nothing to cut (or a length out of range)
     if (gtid == 0) {
-      if (len < 0 || nb > a.cap_blocks) report_error(a.st, kErrDevice, 310);
+      if (bad) report_error(a.st, kErrDevice, 310);
       a.meta[b] = EvictMeta{0, 0, 0, 0};
     }
     if (kept != nullptr)

@@ -261,6 +261,23 @@ def test_evict_lengths_out_of_range_are_recorded():
     assert int(cache.len[1]) == 40
 
 
+def test_evict_length_inside_the_block_behind_the_capacity():
+    # 512 tokens fit: 513 would have an incomplete block of their own behind the last row's end
+    for length in (511, 512, 513, 515):
+        cache = _cache([300, 400], 512, 0, seed=65)
+        ev = qsa.Evictor(cache, 10)
+        cache.len[1] = length
+        k = cache.k_blocks.clone()
+        ev.evict()
+        assert int(cache.len[0]) == 40
+        if length <= 512:
+            assert ev.device_error() == ("QSA_OK", 0)
+            assert int(cache.len[1]) == 40 + length % 4
+        else:
+            assert ev.device_error() == ("QSA_ERR_DEVICE", 310)
+            assert int(cache.len[1]) == length and torch.equal(cache.k_blocks[1], k[1])
+
+
 def test_evict_bad_page_is_not_followed():
     cache = _cache([1000], 1024, 512, seed=61)
     other = [p for p in range(cache.pool_pages) if p not in cache.page_table.flatten().tolist()]
