@@ -65,6 +65,26 @@ qsa_status delta_args(const void* q, const void* k, const void* v, const float* 
   return QSA_OK;
 }
 
+// What a call writes (out, the pool) and what it reads must not overlap: CTAs write outputs and
+// states while others still read.  out may be v itself: every value is read by the CTA that
+// replaces it, or in a launch before.
+bool delta_overlaps(const DeltaArgs& a) {
+  struct Range {
+    uintptr_t p, n;
+  };
+  auto range = [](const void* p, int64_t n) { return Range{reinterpret_cast<uintptr_t>(p), static_cast<uintptr_t>(n)}; };
+  auto meet = [](Range x, Range y) { return x.p < y.p + y.n && y.p < x.p + x.n; };
+  const int64_t keys = a.tokens * a.key_heads * kGdnDim * 2, vals = a.tokens * a.heads * kGdnDim * 2;
+  const Range out = range(a.out, vals);
+  const Range pool = range(a.states, int64_t(a.num_slots) * a.heads * kGdnDim * kGdnDim * 4);
+  if (meet(out, pool) || (a.out != a.v && meet(out, range(a.v, vals)))) return true;
+  const Range in[] = {range(a.q, keys), range(a.k, keys), range(a.log_alpha, a.tokens * a.heads * 4),
+                      range(a.beta, a.tokens * a.heads * 4)};
+  for (const Range& r : in)
+    if (meet(out, r) || meet(pool, r)) return true;
+  return meet(pool, range(a.v, vals));
+}
+
 qsa_status launch_delta_step(const DeltaArgs& a, cudaStream_t s) {
   k_delta_step<2><<<dim3(a.heads, a.rows, 4), kStepThreads, 0, s>>>(a);
   QSA_CHECK_LAUNCH();
@@ -137,7 +157,9 @@ void extend_plan(const int32_t* h_cu, int32_t num_seqs, int32_t heads, ExtendPla
   };
   double best = 10 + 2.65 * std::max(double(p->max_chunks), double(total) * hp / sms);
   int64_t L = std::max<int64_t>(1, p->max_chunks);
-  for (int64_t k = 3; k <= 512 && k <= p->max_chunks / 2; k += 1 + k / 16) {
+  // where all walks together bound the uncut call, a cut only adds to them
+  const int64_t cuts = double(total) * hp >= double(p->max_chunks) * sms ? 0 : 512;
+  for (int64_t k = 3; k <= cuts && k <= p->max_chunks / 2; k += 1 + k / 16) {
     const int64_t l = (p->max_chunks + k - 1) / k;
     double inner = 0;
     for (int32_t i = 0; i < num_seqs; ++i) {
@@ -200,6 +222,7 @@ extern "C" qsa_status qsa_gated_deltanet_extend(
   a.d.tokens = h_cu_seqlens[num_seqs];
   a.d.short_len = p.short_len;
   if (a.d.tokens == 0) return QSA_OK;
+  if (delta_overlaps(a.d)) return QSA_ERR_INVALID_ARG;
   if (p.short_len > 0) {
     st = launch_delta_step(a.d, reinterpret_cast<cudaStream_t>(stream));
     if (st != QSA_OK) return st;
@@ -267,6 +290,7 @@ extern "C" qsa_status qsa_gated_deltanet_step(const void* q, const void* k, cons
   a.n_new = n_new;
   a.counts = counts;
   a.tokens = static_cast<int64_t>(batch) * n_new;
+  if (delta_overlaps(a)) return QSA_ERR_INVALID_ARG;
   return launch_delta_step(a, reinterpret_cast<cudaStream_t>(stream));
 }
 

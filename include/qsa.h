@@ -427,6 +427,8 @@ QSA_API qsa_status qsa_gated_deltanet(const void *q, const void *k, const void *
  *   log_alpha, beta  fp32 [tokens][heads]
  * heads 1..256, a multiple of key_heads: value head h reads key head h / (heads / key_heads).
  * The arithmetic keeps about fp32 accuracy in the states; out is rounded once to bf16.
+ * out may be v itself; otherwise neither out nor states overlaps an input or the other
+ * (QSA_ERR_INVALID_ARG).
  *
  * qsa_gated_deltanet_extend takes packed sequences as qsa_gated_deltanet does (d_cu_seqlens,
  * h_cu_seqlens, num_seqs; sequences may be empty), in chunks, with scratch space of

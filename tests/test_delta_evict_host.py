@@ -70,6 +70,28 @@ def test_step_refusals(kw, want):
     assert _step(**kw) == want
 
 
+# (64 tokens x 4 heads: 64 KB of v and out, 32 KB of q and k, 1 KB of gates, 768 KB of states)
+@pytest.mark.parametrize("field,at", [
+    ("q", 0x200000), ("k", 0x200000 + 65536 - 16), ("v", 0x200000 + 16), ("la", 0x200000 + 4),
+    ("beta", 0x200000 - 1020), ("states", 0x200000 - 786432 + 16), ("q", 0x800000 + 786432 - 16),
+    ("v", 0x800000 - 65536 + 16), ("la", 0x800000), ("out", 0x800000)])
+@pytest.mark.parametrize("call", ["extend", "step"])
+def test_delta_overlaps_are_refused(call, field, at):
+    p = dict(q=0x2000000, k=0x2100000, v=0x2200000, la=0x2300000, beta=0x2400000, out=0x200000,
+             states=0x800000)
+    p[field] = at
+    lib = qsa.load()
+    lead = [_p(p[x]) for x in ("q", "k", "v", "la", "beta")]
+    if call == "extend":
+        h = (ctypes.c_int32 * 2)(0, 64)
+        r = lib.qsa_gated_deltanet_extend(*lead, _p(GOOD), h, 1, 2, 4, _p(p["states"]), 3, _p(GOOD),
+                                          _p(p["out"]), _p(0x4000000), 1 << 30, None)
+    else:
+        r = lib.qsa_gated_deltanet_step(*lead, 2, 32, None, 2, 4, _p(p["states"]), 3, _p(GOOD),
+                                        _p(p["out"]), None)
+    assert B.STATUS[r] == "QSA_ERR_INVALID_ARG"
+
+
 def _cache(batch=2, cap=64, k=GOOD, length=GOOD):
     return B.CacheDesc(k, GOOD, GOOD, GOOD, length, batch, cap)
 

@@ -187,6 +187,24 @@ def test_step_on_another_stream_in_a_graph():
     assert torch.equal(states, want) and torch.equal(out, ref)
 
 
+@pytest.mark.parametrize("lens", [[130, 3, 64], [20, 1], [9000]])
+def test_out_in_place_of_v(lens):
+    w, states = _draw(lens, 2, 1, len(lens), seed=38)
+    twin = states.clone()
+    want = qsa.gated_deltanet_extend(w.q, w.k, w.v, w.log_alpha, w.beta, w.cu_seqlens, states)
+    v = w.v.clone()
+    qsa.gated_deltanet_extend(w.q, w.k, v, w.log_alpha, w.beta, w.cu_seqlens, twin, out=v)
+    torch.cuda.synchronize()
+    assert torch.equal(v, want) and torch.equal(twin, states)
+    x = [y[:12].view(2, 6, *y.shape[1:]) for y in (w.q, w.k, w.v, w.log_alpha, w.beta)]
+    states, twin = states[:1].repeat(2, 1, 1, 1), twin[:1].repeat(2, 1, 1, 1)
+    want = qsa.gated_deltanet_step(*x, states)
+    x[2] = x[2].clone()
+    qsa.gated_deltanet_step(*x, twin, out=x[2])
+    torch.cuda.synchronize()
+    assert torch.equal(x[2], want) and torch.equal(twin, states)
+
+
 def test_extend_contexts_in_two_graphs():
     # two contexts, two captured graphs, replayed in turn and over again
     heads = 4
