@@ -185,8 +185,8 @@ __global__ void __launch_bounds__(kStepThreads) k_delta_step(DeltaArgs a) {
 // products a chunk (W S0^T, then U^T K) on the tcgen05 tensor cores.  Where the walks do not fill
 // the SMs, sequences are cut into segments: a segment is affine in the state it is entered with,
 // E -> E P + S, so a first pass of the scan finds S (from zero) and P (from the identity, without
-// writes) of all segments at once, k_delta_join takes the states through them, and a second pass
-// writes the outputs.
+// writes) of the inner segments while the first ones run whole, k_delta_join takes the states
+// through, and a second pass writes the other segments' outputs.
 //
 // q, k and v are bf16 and exact as operands; the fp32 operands go in as parts.  What a token
 // writes carries T and U straight into the state: three bf16 parts each, x = hi + mid + lo to
@@ -228,6 +228,7 @@ struct DeltaChunkArgs {
   unsigned char* rec;        // [records][nheads][kRecBytes]
   int64_t records;
   int32_t seg_chunks;        // chunks of a segment (a sequence is walked by one CTA a segment)
+  int32_t seg_first;         // and of a sequence's first segment, at most as many
   int64_t seg_slots;
   float* seg_state;          // [segment slots][nheads][128][128]: state at the segment's end
   float* seg_trans;          // the same shape: the segment's transition (P of S0 P + S)
@@ -783,8 +784,9 @@ constexpr int kScanSmemBytes = kScanBars + 8192;
 static_assert(kScanSmemBytes <= 232448, "shared memory per CTA");
 static_assert(kScanWBytes % 1024 == 0 && kScanQBytes % 1024 == 0, "tiles on 1 KB boundaries");
 
-// what a launch does: the whole walk; or, for a sequence cut into segments, their states from
-// zero and their transitions (pass 0), then the outputs from the joined states (pass 1)
+// what a launch does: the whole walk; or, where sequences are cut into segments, the first segments
+// whole and the inner ones' states from zero and transitions, then the outputs of all segments
+// behind the first from the joined states
 constexpr int kScanWhole = 0, kScanEnds = 1, kScanOutputs = 2;
 
 struct ScanBars {
@@ -859,19 +861,20 @@ __global__ void __launch_bounds__(kScanThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int hl = blockIdx.x, h = ca.head0 + hl, row = blockIdx.y;
   pdl_trigger();
-  // pass 0 has two CTAs a segment: states from zero, and transitions
+  // the first pass has two CTAs a segment: states, and transitions
   const bool trans = mode == kScanEnds && (blockIdx.z & 1);
-  const int seg = mode == kScanEnds ? blockIdx.z >> 1 : blockIdx.z;
+  const int seg = mode == kScanEnds ? blockIdx.z >> 1 : blockIdx.z + (mode == kScanOutputs);
   int64_t len;
   const int64_t begin = delta_row_tokens(a, row, &len);
   const int64_t chunks = (len + kGdnChunk - 1) / kGdnChunk;
-  const int64_t c0 = static_cast<int64_t>(seg) * ca.seg_chunks;
-  const int64_t c1 = c0 + ca.seg_chunks < chunks ? c0 + ca.seg_chunks : chunks;
+  const int64_t c0 = seg == 0 ? 0 : ca.seg_first + static_cast<int64_t>(seg - 1) * ca.seg_chunks;
+  const int64_t len_c = seg == 0 ? ca.seg_first : ca.seg_chunks;
+  const int64_t c1 = c0 + len_c < chunks ? c0 + len_c : chunks;
   const int nc = static_cast<int>(c1 - c0);
   const bool last = c1 == chunks;
   const int slot = a.slots != nullptr ? a.slots[row] : row;
   bool idle = nc <= 0 || len <= a.short_len || slot < 0 || slot >= a.num_slots ||
-              (mode == kScanEnds && (last || (trans && seg == 0)));
+              (mode == kScanEnds && (seg == 0 ? trans : last));
   if (!idle) idle = delta_slot_taken(a, row, slot);
   if (!idle && (smem_u32(smem) & 1023u) != 0) {   // the tiles need it; the runtime places them so
     if (tid == 0) report_error(ca.st, kErrDevice, 320);
@@ -881,18 +884,15 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     pdl_wait();   // every CTA waits: the kernels after this one count on all before it
     return;
   }
-  const bool outputs = mode != kScanEnds;
+  const bool outputs = mode != kScanEnds || seg == 0;
   const int64_t rec0 = delta_first_record(begin, row);
   const int64_t seg0 = rec0 / ca.seg_chunks + row;     // as records: segments never overlap
   const int64_t tile = static_cast<int64_t>(kGdnDim) * kGdnDim;
   float* state = a.states + (static_cast<int64_t>(slot) * a.heads + h) * tile;
   const int64_t seg_stride = static_cast<int64_t>(ca.nheads) * tile;
   float* ends = ca.seg_state + (seg0 + seg) * seg_stride + hl * tile;
-  // a cut sequence's start state waits in its last segment's place: the outputs pass reads it
-  // there, since that pass's last segment writes the pool
-  float* kept = ends + ((chunks - 1) / ca.seg_chunks - seg) * seg_stride;
-  const float* src = seg > 0 ? ends - seg_stride : mode == kScanOutputs && !last ? kept : state;
-  float* dst = mode != kScanEnds ? state : trans ? ca.seg_trans + (ends - ca.seg_state) : ends;
+  const float* src = seg > 0 ? ends - seg_stride : state;
+  float* dst = last ? state : trans ? ca.seg_trans + (ends - ca.seg_state) : ends;
   const int64_t t0 = begin + c0 * kGdnChunk;
   const int64_t ntok = (last ? len : c1 * kGdnChunk) - c0 * kGdnChunk;
 
@@ -957,7 +957,6 @@ __global__ void __launch_bounds__(kScanThreads, 1)
         s[4 * i + 1] = x.y;
         s[4 * i + 2] = x.z;
         s[4 * i + 3] = x.w;
-        if (mode == kScanEnds) reinterpret_cast<float4*>(kept + v * kGdnDim + 32 * quarter)[i] = x;
       }
     }
     auto signal = [&](uint64_t* bar) {
@@ -1355,7 +1354,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_delta_join(DeltaChunkArgs ca) 
   int64_t len;
   const int64_t begin = delta_row_tokens(a, row, &len);
   const int64_t chunks = (len + kGdnChunk - 1) / kGdnChunk;
-  const int64_t segs = (chunks + ca.seg_chunks - 1) / ca.seg_chunks;
+  const int64_t segs = 1 + (chunks - ca.seg_first + ca.seg_chunks - 1) / ca.seg_chunks;
   if (d == 0) {
     for (int i = 0; i < kStages; ++i) mbar_init(&full[i], 1);
     abort_flag = 0;

@@ -102,7 +102,7 @@ qsa_status extend_check_cu(const int32_t* h_cu, int32_t num_seqs) {
 // sequences cut into segments of seg_chunks chunks where that fills the SMs better.
 struct ExtendPlan {
   int64_t records = 0, max_chunks = 0, seg_slots = 0;
-  int32_t pass_heads = 1, seg_chunks = 1, segs = 1;
+  int32_t pass_heads = 1, seg_chunks = 1, seg_first = 1, segs = 1;
   int32_t short_len = 0;   // pieces of at most this many tokens go token by token
   size_t o_rec = 0, o_state = 0, o_trans = 0, total = 0;
 };
@@ -148,36 +148,48 @@ void extend_plan(const int32_t* h_cu, int32_t num_seqs, int32_t heads, ExtendPla
   }
   // Microseconds of the scan, uncut and cut into about k segments: the longest walk, or all walks
   // in waves over the SMs, at what a chunk was measured to take (2.65 with outputs, 2.4 without),
-  // and what a launch and a step of the join were.  Cut, all segments but the last run first
-  // without outputs (from zero, and their transitions), then all run with outputs.
+  // and what a launch and a step of the join were.  Cut, first segments run whole beside the inner
+  // ones' walks from zero and transitions, then all segments behind the first with outputs.  First
+  // ones an eighth shorter, as they write outputs beside walks that do not, or as long as the
+  // others, where that saves a shorter sequence a segment.
   const double sms = num_sms();
   // (a CTA takes 8 until its first chunk)
   auto waves_of = [&](double l, double all, double chunk) {
     return std::ceil(std::max(1.0, all / sms / l)) * (8 + chunk * l);
   };
   double best = 10 + 2.65 * std::max(double(p->max_chunks), double(total) * hp / sms);
-  int64_t L = std::max<int64_t>(1, p->max_chunks);
+  int64_t L = std::max<int64_t>(1, p->max_chunks), F = L;
   // where all walks together bound the uncut call, a cut only adds to them
   const int64_t cuts = double(total) * hp >= double(p->max_chunks) * sms ? 0 : 512;
-  for (int64_t k = 3; k <= cuts && k <= p->max_chunks / 2; k += 1 + k / 16) {
-    const int64_t l = (p->max_chunks + k - 1) / k;
-    double inner = 0;
+  auto consider = [&](int64_t l, int64_t f, int64_t k) {
+    double first = 0, rest = 0;   // chunks walked by the two passes
     for (int32_t i = 0; i < num_seqs; ++i) {
-      const int64_t nc = (int64_t(h_cu[i + 1]) - h_cu[i] + kGdnChunk - 1) / kGdnChunk;
-      const int64_t segs = (nc + l - 1) / l;
-      if (segs > 1) inner += double((2 * segs - 3) * l);
+      const int64_t len = int64_t(h_cu[i + 1]) - h_cu[i];
+      if (len <= p->short_len) continue;
+      const int64_t nc = (len + kGdnChunk - 1) / kGdnChunk;
+      const int64_t segs = nc <= f ? 1 : 1 + (nc - f + l - 1) / l;
+      first += segs > 1 ? double((2 * segs - 3) * l) : double(nc);
+      rest += double((segs - 1) * l);
     }
     const int rows = join_rows(int64_t(num_seqs) * hp);
     const double waves = std::ceil(double(num_seqs) * hp * (kGdnDim / rows) / sms);
-    const double t = waves_of(double(l), inner * hp, 2.4) + waves * (6 + double(k) * 0.9) + 8 +
-                     waves_of(double(l), double(total) * hp, 2.65);
+    const double t = waves_of(double(l), first * hp, 2.4) + (f == l ? 0.25 * double(l) : 0) +
+                     waves * (6 + double(k) * 0.9) + 8 + waves_of(double(l), rest * hp, 2.65);
     if (t < best) {
       best = t;
       L = l;
+      F = f;
     }
+  };
+  for (int64_t k = 3; k <= cuts && k <= p->max_chunks / 2; k += 1 + k / 16) {
+    const int64_t even = (p->max_chunks + k - 1) / k;
+    const int64_t l = (8 * p->max_chunks + 8 * k - 2) / (8 * k - 1);
+    consider(l, l - l / 8, k);
+    consider(even, even, k);
   }
   p->seg_chunks = static_cast<int32_t>(L);
-  p->segs = static_cast<int32_t>((p->max_chunks + L - 1) / L);
+  p->seg_first = static_cast<int32_t>(F);
+  p->segs = static_cast<int32_t>(p->max_chunks <= F ? 1 : 1 + (p->max_chunks - F + L - 1) / L);
   Carver cv;
   p->o_rec = cv.take(static_cast<size_t>(per_head * hp));
   if (p->segs > 1) {
@@ -232,6 +244,7 @@ extern "C" qsa_status qsa_gated_deltanet_extend(
   a.rec = ws + p.o_rec;
   a.records = p.records;
   a.seg_chunks = p.seg_chunks;
+  a.seg_first = p.seg_first;
   a.seg_slots = p.seg_slots;
   if (p.segs > 1) {
     a.seg_state = reinterpret_cast<float*>(ws + p.o_state);
@@ -268,8 +281,9 @@ extern "C" qsa_status qsa_gated_deltanet_extend(
                                  join_smem_bytes(rows), s, a));
       }
     }
-    QSA_CHECK_PDL(launch_pdl(k_delta_scan, dim3(a.nheads, num_seqs, p.segs), dim3(kScanThreads),
-                             kScanSmemBytes, s, maps, a, p.segs > 1 ? kScanOutputs : kScanWhole));
+    QSA_CHECK_PDL(launch_pdl(k_delta_scan, dim3(a.nheads, num_seqs, std::max(1, p.segs - 1)),
+                             dim3(kScanThreads), kScanSmemBytes, s, maps, a,
+                             p.segs > 1 ? kScanOutputs : kScanWhole));
   }
   return QSA_OK;
 }
