@@ -420,7 +420,8 @@ qsa_status evict_impl(const CacheView& view, float* mass, int32_t keep, int32_t 
   while (cluster > 1 && (int64_t(cluster) * c->batch > (cluster > 8 ? num_sms() / 2 : num_sms()) ||
                          a.cap_blocks / cluster < kEvThreads * kEvBatch))
     cluster /= 2;
-  if (cudaFuncSetAttribute(k_evict_select, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+  if (cluster > 8 &&
+      cudaFuncSetAttribute(k_evict_select, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
     return QSA_ERR_CUDA;
   QSA_CHECK_PDL(launch_cluster(k_evict_select, dim3(cluster, c->batch), dim3(kEvThreads), 0, cluster, s, a));
   if (g.tiles > 0)
