@@ -87,6 +87,8 @@ __global__ void __launch_bounds__(kStepThreads) k_delta_step(DeltaArgs a) {
   const int tid = threadIdx.x, l8 = tid & 7, grp = tid >> 3;   // 16 groups of 8 lanes
   const int h = blockIdx.x, r = blockIdx.y;
   const int v0 = (blockIdx.z * 16 + grp) * RV;
+  pdl_wait();      // launched as a programmatic dependent of the caller's last kernel, which is done
+  pdl_trigger();   // before any kernel behind this one starts
   int64_t n;
   const int64_t t0 = delta_row_tokens(a, r, &n);
   const int slot = a.slots != nullptr ? a.slots[r] : r;
@@ -401,6 +403,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) k_delta_prep(DeltaChunkArgs c
   const DeltaArgs& a = ca.d;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, tq = lane & 3;
   const int64_t r = blockIdx.x;
+  pdl_wait();      // the caller's last kernel
   pdl_trigger();   // the scan sets up while the last of these run
   // the last sequence whose first record is not past r, 256 candidates at a time
   int seq = 0;

@@ -91,6 +91,8 @@ __global__ void __launch_bounds__(kWtThreads) k_block_weights(WeightArgs a) {
   int32_t* at_sh = blk_sh + per;                      // its K rows / 4 (KV head 0); -1: reads as zeros
   float* mass_sh = reinterpret_cast<float*>(at_sh + per);   // fetched here, added to at the end
   float* mass = a.mass + static_cast<int64_t>(b) * a.cap_blocks;
+  pdl_wait();      // launched as a programmatic dependent of the caller's last kernel, which is done
+  pdl_trigger();   // before any kernel behind this one starts
   const int len = a.len[b];
   const int own = (len - 1) / kBlock;
   int n = a.cnt[b];
@@ -366,6 +368,8 @@ __global__ void __launch_bounds__(kEvThreads, 1) k_evict_select(EvictArgs a) {
   __shared__ int sh_first;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, b = blockIdx.y;
   const int C = gridDim.x, rank = blockIdx.x;
+  pdl_wait();      // the caller's last kernel
+  pdl_trigger();   // the move's first CTAs wait beside these
   const int len = a.len[b];
   const int nb = len / kBlock, tail = len % kBlock;
   const float* mass = a.mass + static_cast<int64_t>(b) * a.cap_blocks;

@@ -11,7 +11,7 @@
 #include "qsa_evict.cuh"
 
 namespace {
-// Launches a kernel in clusters of c CTAs along x.
+// Launches a kernel in clusters of c CTAs along x, as a programmatic dependent (launch_pdl).
 template <typename... KArgs, typename... Args>
 cudaError_t launch_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, int c,
                            cudaStream_t s, Args&&... args) {
@@ -20,13 +20,15 @@ cudaError_t launch_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, size
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = c;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 }  // namespace
@@ -86,8 +88,7 @@ bool delta_overlaps(const DeltaArgs& a) {
 }
 
 qsa_status launch_delta_step(const DeltaArgs& a, cudaStream_t s) {
-  k_delta_step<2><<<dim3(a.heads, a.rows, 4), kStepThreads, 0, s>>>(a);
-  QSA_CHECK_LAUNCH();
+  QSA_CHECK_PDL(launch_pdl(k_delta_step<2>, dim3(a.heads, a.rows, 4), dim3(kStepThreads), 0, s, a));
   return QSA_OK;
 }
 
@@ -268,9 +269,9 @@ extern "C" qsa_status qsa_gated_deltanet_extend(
   for (int32_t h0 = 0; h0 < heads; h0 += p.pass_heads) {
     a.head0 = h0;
     a.nheads = std::min(p.pass_heads, heads - h0);
-    k_delta_prep<<<dim3(static_cast<unsigned>(p.records), a.nheads), kPrepThreads, prep_smem, s>>>(a);
-    QSA_CHECK_LAUNCH();
-    // each of these sets up while the one before it finishes
+    // each launch sets up while the one before it finishes
+    QSA_CHECK_PDL(launch_pdl(k_delta_prep, dim3(static_cast<unsigned>(p.records), a.nheads),
+                             dim3(kPrepThreads), prep_smem, s, a));
     if (p.segs > 1) {
       QSA_CHECK_PDL(launch_pdl(k_delta_scan, dim3(a.nheads, num_seqs, 2 * (p.segs - 1)),
                                dim3(kScanThreads), kScanSmemBytes, s, maps, a, kScanEnds));
