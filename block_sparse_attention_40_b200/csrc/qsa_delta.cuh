@@ -79,7 +79,7 @@ __device__ __forceinline__ void unpack_bf16x2(uint32_t w, float* f) {
 // pass, and the reductions are three shuffles.  A token's inputs are fetched while the one before
 // it is taken.  Bound by the state's bytes: 128 KB per (row, head) against about 4.5 KB of
 // everything else at one token.  64 rows x 32 heads x 1 token: 45 us, 6.0 TB/s, 92% of the measured
-// copy rate; 24 rows of up to 5 tokens x 16 heads: 10.3 us (its states' bytes take 6.9).
+// copy rate; 24 rows of up to 5 tokens x 16 heads: 9.8 us a call (its states' bytes take 6.9).
 constexpr int kStepThreads = 128;
 
 template <int RV>

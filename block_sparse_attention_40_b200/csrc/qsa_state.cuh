@@ -5,6 +5,7 @@
 
 #pragma once
 
+#include <atomic>
 #include <cmath>
 
 #include "qsa_delta.cuh"
@@ -30,6 +31,32 @@ cudaError_t launch_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, size
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+// How many clusters of c CTAs of a kernel run at a time, for kernels whose CTAs fill an SM (a GPC's
+// SMs hold whole clusters only: 16 clusters of 8 do not fit into 148 SMs).  Asked once a size, since
+// the GPUs of a process are alike; `memo` has an entry a size.
+template <typename... KArgs>
+int active_clusters(void (*kernel)(KArgs...), int threads, size_t smem, int c, std::atomic<int>* memo) {
+  int n = memo[c].load(std::memory_order_relaxed);
+  if (n > 0) return n;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(c);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = c;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
+    cudaGetLastError();   // a size that cannot run here
+    return 0;
+  }
+  memo[c].store(n, std::memory_order_relaxed);
+  return n;
 }
 }  // namespace
 
@@ -339,18 +366,26 @@ qsa_status weights_impl(const void* q, const CacheView& view, const int32_t* sel
   a.mass = mass;
   a.pg = view.pg;
   a.st = dev_status(workspace);
-  // As many CTAs to a sequence, up to eight, as keep the grid within two CTAs an SM.  Where clusters
-  // of eight take half the SMs at most, CTAs of 512 threads halve the tiles of a warp (one to four
-  // sequences of 60K tokens 10.3 us against 12.3 with 256 threads); beyond, one such CTA fills an SM
-  // and its cluster waits for a whole GPC (16 sequences: 20.5 us against 14.4).  Clusters of 16
-  // took 24.6 us there.
+  // CTAs of 512 threads, one to an SM, in the largest clusters that all run at once: 16 sequences of
+  // 60K tokens in clusters of 6 take 10.2 us, 11.9 of 4 and 18.0 of 8 (in turns), 32 of 4 12.2, 64 of
+  // 2 17.8.  Sequences beyond clusters of two: CTAs of 256 threads, two to an SM, in as large clusters
+  // as keep to that (64 so, of 4: 18.7, and one wide CTA a sequence 28.3).
+  static std::atomic<int> memo[kWtMaxCluster + 1];
+  const int most = wt_smem_bytes(QSA_MAX_TOPK, 1);
+  if (!set_smem(k_block_weights<512>, most) || !set_smem(k_block_weights<256>, most)) return QSA_ERR_CUDA;
   int cluster = kWtMaxCluster;
-  while (cluster > 1 && (int64_t(cluster) * c->batch > 2 * num_sms() || wt_tiles_per_cta(topk, cluster) < 4))
-    cluster /= 2;
-  const bool wide = cluster == kWtMaxCluster && 2 * cluster * c->batch <= num_sms();
+  while (cluster > 1 && (wt_tiles_per_cta(topk, cluster) < 4 ||
+                         active_clusters(k_block_weights<512>, 512, wt_smem_bytes(QSA_MAX_TOPK, cluster),
+                                         cluster, memo) < c->batch))
+    --cluster;
+  const bool wide = cluster > 1;
+  if (!wide) {
+    cluster = kWtMaxCluster;
+    while (cluster > 1 && (int64_t(cluster) * c->batch > 2 * num_sms() || wt_tiles_per_cta(topk, cluster) < 4))
+      cluster /= 2;
+  }
   const auto kernel = wide ? k_block_weights<512> : k_block_weights<256>;
   const int smem = wt_smem_bytes(topk, cluster);
-  if (!set_smem(kernel, smem)) return QSA_ERR_CUDA;
   QSA_CHECK_PDL(launch_cluster(kernel, dim3(cluster, c->batch), dim3(wide ? 512 : 256), smem, cluster,
                                reinterpret_cast<cudaStream_t>(stream), a));
   return QSA_OK;
@@ -413,17 +448,18 @@ qsa_status evict_impl(const CacheView& view, float* mass, int32_t keep, int32_t 
   a.loaded = reinterpret_cast<int32_t*>(ws + g.o_loaded);
   a.before = reinterpret_cast<int32_t*>(ws + g.o_before);
   a.ticket = reinterpret_cast<int32_t*>(ws + g.o_ticket);
-  // As many CTAs to a sequence as the SMs hold, with at least 4,096 weights each (four a thread):
-  // below that the cluster's barriers cost more than its reads.  A CTA fills an SM, and a GPC has
-  // room for one cluster of 16, so those are for few sequences (four of 262,140 tokens cut to almost
-  // all: 112 us against 117 with eight; eight: 213 against 199).
+  // The largest clusters that all run at once (a CTA fills an SM), with at least 4,096 weights a CTA
+  // (four a thread): below that the cluster's barriers cost more than its reads.  Four sequences of
+  // 262,140 tokens cut to almost all: 112 us in clusters of 16, 117 of 8; 16 of 65,535 cut to 64
+  // blocks: 26.7 of 4, 40.8 of 8 (in turns).
+  static std::atomic<int> memo[kEvMaxCluster + 1];
   int cluster = kEvMaxCluster;
-  while (cluster > 1 && (int64_t(cluster) * c->batch > (cluster > 8 ? num_sms() / 2 : num_sms()) ||
-                         a.cap_blocks / cluster < kEvThreads * kEvBatch))
-    cluster /= 2;
+  while (cluster > 1 && a.cap_blocks / cluster < kEvThreads * kEvBatch) cluster /= 2;
   if (cluster > 8 &&
       cudaFuncSetAttribute(k_evict_select, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
     return QSA_ERR_CUDA;
+  while (cluster > 1 && active_clusters(k_evict_select, kEvThreads, 0, cluster, memo) < c->batch)
+    cluster /= 2;
   QSA_CHECK_PDL(launch_cluster(k_evict_select, dim3(cluster, c->batch), dim3(kEvThreads), 0, cluster, s, a));
   if (g.tiles > 0)
     QSA_CHECK_PDL(launch_pdl(k_evict_move, dim3(static_cast<unsigned>(g.tiles) * c->batch),
