@@ -28,9 +28,9 @@ namespace qsa {
 // leaves one number, the log2 of the sum of its 4 exponentials, in shared memory; the heads'
 // totals are then joined over the CTA and the cluster (distributed shared memory) in a fixed
 // order, and each block's weight is the sum over heads of 2^(block's log-sum - head's total): one
-// pass over the keys and no second launch.  64 sequences of 32K tokens, 4,096-token pages: 17.9 us
-// a call, 3.8 TB/s (the keys would take 10.4); one sequence: 8.8 us, all latency (idx -> page ->
-// keys, two barriers of the cluster).
+// pass over the keys and no second launch.  64 sequences of 32K tokens, 4,096-token pages: 21.3 us
+// a call, 3.2 TB/s (the keys would take 10.4; 17.9 us where L2 holds them); one sequence: 8.8 us, all
+// latency (idx -> page -> keys, two barriers of the cluster).
 constexpr int kWtMaxCluster = 8;
 
 struct WeightArgs {
