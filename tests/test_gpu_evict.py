@@ -85,6 +85,21 @@ def test_weights(lens, topk, page):
     _check_weights(ev, lens, q, idx, cnt, before)
 
 
+@pytest.mark.parametrize("batch", [12, 16, 24, 31, 40, 74, 80])
+def test_weights_clusters_of_every_size(batch):
+    # from eight CTAs a sequence down to two, and the narrow ones beyond
+    lens = [600 - 7 * (b % 5) for b in range(batch)]
+    ev = qsa.Evictor(_cache(lens, 600, 0, seed=66), 8)
+    before = _np(ev.mass)
+    q = torch.randn((batch, 24, 128), generator=torch.Generator().manual_seed(67)) \
+        .to(torch.bfloat16).to(DEV)
+    idx, cnt = _selection(lens, 100, seed=68)
+    ev.accumulate(q, torch.from_numpy(idx).to(DEV), torch.from_numpy(cnt).to(DEV))
+    torch.cuda.synchronize()
+    assert ev.device_error() == ("QSA_OK", 0)
+    _check_weights(ev, lens, q, idx, cnt, before)
+
+
 def test_weights_twice_are_the_same_bits():
     lens = [1500, 700]
     ev = qsa.Evictor(_cache(lens, 2048, 0, seed=7), 8)
