@@ -36,7 +36,7 @@ EXPORTS = ("qsa_status_string", "qsa_version", "qsa_launch_count", "qsa_workspac
            "qsa_decode_shard_attend", "qsa_combine_partials", "qsa_gated_deltanet",
            "qsa_gated_deltanet_extend_workspace_size", "qsa_gated_deltanet_extend",
            "qsa_gated_deltanet_step", "qsa_accumulate_weights", "qsa_accumulate_weights_paged",
-           "qsa_evict_workspace_size", "qsa_evict", "qsa_evict_paged")
+           "qsa_evict_workspace_size", "qsa_evict", "qsa_evict_paged", "qsa_set_debug_fault")
 
 
 class QSAError(RuntimeError):
@@ -117,6 +117,7 @@ def load(build_if_needed: bool = True):
             "qsa_evict_workspace_size": ([P, I32, I32, I32], SZ),
             "qsa_evict": ([P, P, I32, I32, I32, P, P, SZ, P], st),
             "qsa_evict_paged": ([P, P, I32, I32, I32, P, P, SZ, P], st),
+            "qsa_set_debug_fault": ([I32], st),
         }
         for name, (args, res) in sig.items():
             fn = getattr(lib, name)

@@ -235,7 +235,10 @@ struct DeltaChunkArgs {
   float* seg_state;          // [segment slots][nheads][128][128]: state at the segment's end
   float* seg_trans;          // the same shape: the segment's transition (P of S0 P + S)
   DevStatus st;
+  uint32_t wait_ns;          // limit of every wait
+  int32_t fault;             // testing: a copy that block (0, 0, 0) does not issue (kFault..)
 };
+constexpr int32_t kFaultScan = 1, kFaultJoin = 2;
 
 // Instruction descriptor: kind::f16 with f16 A/B, fp32 D, dense.
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int a_mn_major, int b_mn_major) {
@@ -836,18 +839,24 @@ __device__ __forceinline__ void tmem_ld16_at(uint32_t taddr, float* f) {
   for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(r[i]);
 }
 
-// Bounded wait for the phase of the given parity.  Each try waits in hardware for a while; past
-// the limit (seconds) the site is noted for the CTA's other waits, which then give up too, and
-// for the status that the kernel reports at its end.  Small, since the kernel's loop has to stay
-// in the instruction cache.
-constexpr uint32_t kScanTries = 1u << 26;
+// Bounded wait for the phase of the given parity.  Past the limit (on the global timer's low word,
+// which wraps after 4.3 s) the site is noted for the CTA's other waits, which then give up too, and
+// for the status that the kernel reports at its end.  Small, since the kernel's loop has to stay in
+// the instruction cache.
+__device__ __forceinline__ uint32_t globaltimer_lo() {
+  uint32_t t;
+  asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+  return t;
+}
 __device__ __forceinline__ bool scan_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
-                                          int site) {
+                                          uint32_t limit_ns, int site) {
   if (mbar_try_wait(bar, parity)) return true;
+  const uint32_t t0 = globaltimer_lo();
 #pragma unroll 1
-  for (uint32_t i = 0; i < kScanTries && *abort == 0; ++i)
+  while (*abort == 0) {
     if (mbar_try_wait(bar, parity)) return true;
-  if (*abort == 0) *abort = site;
+    if (globaltimer_lo() - t0 > limit_ns) *abort = site;
+  }
   return false;
 }
 
@@ -971,7 +980,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     auto joined = [&](int phase) -> bool {   // the maxima of all quarters of the rows are in place
       __syncwarp();
       if (lane == 0) mbar_arrive(&B.rows[warp & 3]);
-      return __all_sync(0xffffffffu, scan_wait(&B.rows[warp & 3], phase & 1, abort, 337));
+      return __all_sync(0xffffffffu, scan_wait(&B.rows[warp & 3], phase & 1, abort, ca.wait_ns, 337));
     };
     auto row_max = [&](const float (*m)[kGdnDim]) -> float {
       return fmaxf(fmaxf(m[0][v], m[1][v]), fmaxf(m[2][v], m[3][v]));
@@ -998,13 +1007,13 @@ __global__ void __launch_bounds__(kScanThreads, 1)
 #pragma unroll
           for (int i = 0; i < 16; ++i) u[i] = 0.f;
         } else {
-          ok = scan_wait(&B.full_u[sg], (c >> 1) & 1, abort, 338);
+          ok = scan_wait(&B.full_u[sg], (c >> 1) & 1, abort, ca.wait_ns, 338);
           const float* tv = reinterpret_cast<const float*>(smem + kScanU + sg * kScanUBytes) + 16 * quarter * kGdnDim + v;
 #pragma unroll
           for (int i = 0; i < 16; ++i) u[i] = tv[i * kGdnDim];
         }
-        ok = ok && scan_wait(&B.full_w[sg], (c >> 1) & 1, abort, 330) &&
-             scan_wait(&B.d1, c & 1, abort, 331);
+        ok = ok && scan_wait(&B.full_w[sg], (c >> 1) & 1, abort, ca.wait_ns, 330) &&
+             scan_wait(&B.d1, c & 1, abort, ca.wait_ns, 331);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
         const float winv = inv * gate[kGateW];
@@ -1058,7 +1067,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
           tmem_st8(tU + lb + 8 * quarter, w);
           signal(&B.u_full);
         }
-        ok = scan_wait(&B.ds, c & 1, abort, 332);
+        ok = scan_wait(&B.ds, c & 1, abort, ca.wait_ns, 332);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
       } else {
@@ -1111,8 +1120,8 @@ __global__ void __launch_bounds__(kScanThreads, 1)
         const float* gate = reinterpret_cast<const float*>(smem + kScanQ + sg * kScanQBytes + 24576);
         const float4* eg = reinterpret_cast<const float4*>(gate + kGateQ + 32 * half);
         const float2* gm = reinterpret_cast<const float2*>(gate + kGateM + 32 * half);
-        bool ok = scan_wait(&B.full_q[sg], (c >> 1) & 1, abort, 333) &&
-                  scan_wait(&B.qs, c & 1, abort, 334);
+        bool ok = scan_wait(&B.full_q[sg], (c >> 1) & 1, abort, ca.wait_ns, 333) &&
+                  scan_wait(&B.qs, c & 1, abort, ca.wait_ns, 334);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
         const float inv = B.scale[sg][v];
@@ -1132,7 +1141,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&B.q_free);
-        ok = scan_wait(&B.o, c & 1, abort, 335);
+        ok = scan_wait(&B.o, c & 1, abort, ca.wait_ns, 335);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
         const float iu = B.uscale[sg][v];
@@ -1177,6 +1186,10 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     // warp alone would fill the instruction cache.
     const uint64_t dk = smem_desc_sw128(smem_u32(smem), 0, 1024);        // rows of 128 bytes
     const uint64_t dm = smem_desc_sw128(smem_u32(smem), 8192, 1024);     // two column panels
+    // (the lanes stay together, whatever each has seen)
+    auto wait = [&](uint64_t* bar, uint32_t parity, int site) {
+      return __all_sync(0xffffffffu, scan_wait(bar, parity, abort, ca.wait_ns, site)) != 0;
+    };
     bool ok = true;
 #pragma unroll 1
     for (int c = 0; c < nc; ++c) {
@@ -1184,11 +1197,11 @@ __global__ void __launch_bounds__(kScanThreads, 1)
       const uint32_t ph = (c >> 1) & 1;
       const uint64_t sw = (kScanW + sg * kScanWBytes) >> 4, sq = (kScanQ + sg * kScanQBytes) >> 4;
       {
-        if (!scan_wait(&B.full_w[sg], ph, abort, 342)) break;
+        if (!wait(&B.full_w[sg], ph, 342)) break;
         // D_W = -S0 W^T: (hi, hi and lo), (lo, hi) of 16 columns of each quarter at a time
 #pragma unroll 1
         for (int g = 0; g < 2; ++g) {
-          ok = scan_wait(&B.s_part[g], c & 1, abort, 341);
+          ok = wait(&B.s_part[g], c & 1, 341);
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
@@ -1208,8 +1221,8 @@ __global__ void __launch_bounds__(kScanThreads, 1)
         }
         if (!ok) break;
         if (outputs) {
-          if (!scan_wait(&B.full_q[sg], ph, abort, 343)) break;
-          if (c > 0 && !scan_wait(&B.o_free, (c - 1) & 1, abort, 344)) break;
+          if (!wait(&B.full_q[sg], ph, 343)) break;
+          if (c > 0 && !wait(&B.o_free, (c - 1) & 1, 344)) break;
           tc_fence_after();
           if (elect_one()) {
 #pragma unroll 1
@@ -1223,7 +1236,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
           __syncwarp();
         }
       }
-      if (!scan_wait(&B.uw_full, c & 1, abort, 345)) break;
+      if (!wait(&B.uw_full, c & 1, 345)) break;
       tc_fence_after();
       if (elect_one()) {
         // D_S = U'^T K: hi, mid, lo
@@ -1239,8 +1252,8 @@ __global__ void __launch_bounds__(kScanThreads, 1)
       }
       __syncwarp();
       if (outputs) {
-        if (!scan_wait(&B.q_free, c & 1, abort, 346)) break;
-        if (!scan_wait(&B.u_full, c & 1, abort, 348)) break;
+        if (!wait(&B.q_free, c & 1, 346)) break;
+        if (!wait(&B.u_full, c & 1, 348)) break;
         tc_fence_after();
         if (elect_one()) {
           // D_Q = U^T M^T
@@ -1262,13 +1275,14 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     const int who = warp - 25;
     uint64_t* full = who == 0 ? B.full_w : who == 1 ? B.full_u : B.full_q;
     uint64_t* empty = who == 0 ? B.empty_w : who == 1 ? B.empty_u : B.empty_q;
-    const bool on = who == 0 || (who == 1 ? !trans : outputs);
+    const bool on = who == 0 || (who == 1 ? !trans && !(ca.fault == kFaultScan && hl + row + blockIdx.z == 0)
+                                          : outputs);
     const int kh = h / (a.heads / a.key_heads);
     int issued = 0;
 #pragma unroll 1
     for (int c = 0; on && c < nc; ++c) {
       const int sg = c & 1;
-      const bool ok = c < 2 || scan_wait(&empty[sg], ((c >> 1) & 1) ^ 1, abort, 347);
+      const bool ok = c < 2 || scan_wait(&empty[sg], ((c >> 1) & 1) ^ 1, abort, ca.wait_ns, 347);
       if (!__all_sync(0xffffffffu, ok)) break;
       const int64_t at = t0 + static_cast<int64_t>(c) * kGdnChunk;
       const int64_t left = ntok - static_cast<int64_t>(c) * kGdnChunk;
@@ -1371,8 +1385,9 @@ __global__ void __launch_bounds__(kJoinThreads) k_delta_join(DeltaChunkArgs ca) 
   const int64_t at = ((delta_first_record(begin, row) / ca.seg_chunks + row) * ca.nheads + hl) * kTile;
   float* s = ca.seg_state + at + v0 * kGdnDim + d;
   const float* p = ca.seg_trans + at;
+  const int64_t absent = ca.fault == kFaultJoin && hl + row + blockIdx.z == 0 ? 1 : 0;
   auto fetch = [&](int64_t g) {   // segment g's transition
-    if (d == 0 && g + 1 < segs) {
+    if (d == 0 && g + 1 < segs && g != absent) {
       uint64_t* bar = &full[(g - 1) % kStages];
       mbar_arrive_expect_tx(bar, kTile * 4);
       bulk_load(join_sh + ((g - 1) % kStages) * kTile, p + g * stride, kTile * 4, bar);
@@ -1396,7 +1411,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_delta_join(DeltaChunkArgs ca) 
       own[i] = next[i];
       if (g + 2 < segs) next[i] = s[stride + i * kGdnDim];
     }
-    ok = scan_wait(&full[(g - 1) % kStages], ((g - 1) / kStages) & 1, abort, 350);
+    ok = scan_wait(&full[(g - 1) % kStages], ((g - 1) / kStages) & 1, abort, ca.wait_ns, 350);
     if (__syncthreads_or(!ok)) break;
     const float* pg = join_sh + ((g - 1) % kStages) * kTile + 32 * warp * kGdnDim + 4 * lane;
     float4 acc[kRows];
@@ -1433,7 +1448,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_delta_join(DeltaChunkArgs ca) 
   if (d == 0 && *abort) {   // no copy may land after the CTA is gone
     report_error(ca.st, kErrTimeout, 350);
     for (int64_t g = fetched > kStages ? fetched - kStages + 1 : 1; g <= fetched && g + 1 < segs; ++g)
-      mbar_drain(&full[(g - 1) % kStages], ((g - 1) / kStages) & 1);
+      if (g != absent) mbar_drain(&full[(g - 1) % kStages], ((g - 1) / kStages) & 1);
   }
 }
 

@@ -297,6 +297,8 @@ struct EvictArgs {
   uint4* kbar;
   Paging pg;
   DevStatus st;
+  uint64_t wait_ns;      // limit of the move's waits
+  int32_t fault;         // testing: sequence 0's first tile does not say that its blocks were read
 };
 
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -648,7 +650,8 @@ __global__ void __launch_bounds__(kMvThreads, 2) k_evict_move(EvictArgs a) {
   __syncthreads_or(fold == 0x5a5a5a5au);
   if (tid == 0) {
     sh_ok = 1;
-    asm volatile("st.release.gpu.global.s32 [%0], 1;" ::"l"(loaded + tile) : "memory");
+    if (a.fault == 0 || b + tile > 0)
+      asm volatile("st.release.gpu.global.s32 [%0], 1;" ::"l"(loaded + tile) : "memory");
     if (moves) {
       const uint64_t t0 = globaltimer();
       for (int t = dep0; t < dep1 && sh_ok; ++t) {
@@ -656,7 +659,7 @@ __global__ void __launch_bounds__(kMvThreads, 2) k_evict_move(EvictArgs a) {
         while (true) {
           asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(seen) : "l"(loaded + t) : "memory");
           if (seen) break;
-          if (globaltimer() - t0 > kWaitLimitNs) {
+          if (globaltimer() - t0 > a.wait_ns) {
             sh_ok = 0;
             report_error(a.st, kErrTimeout, 313);
             break;

@@ -12,6 +12,13 @@
 #include "qsa_evict.cuh"
 
 namespace {
+// The fault that this thread's next calls make (qsa_set_debug_fault), and the limit of their waits.
+thread_local int32_t debug_fault = 0;
+constexpr int32_t kFaultMove = 3;
+constexpr uint32_t kFaultWaitNs = 1000000;   // 1 ms
+uint32_t wait_limit(bool fault) { return fault ? kFaultWaitNs : static_cast<uint32_t>(kWaitLimitNs); }
+static_assert(kWaitLimitNs < 0xffffffffu, "32-bit limits");
+
 // Launches a kernel in clusters of c CTAs along x, as a programmatic dependent (launch_pdl).
 template <typename... KArgs, typename... Args>
 cudaError_t launch_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, int c,
@@ -279,6 +286,8 @@ extern "C" qsa_status qsa_gated_deltanet_extend(
     a.seg_trans = reinterpret_cast<float*>(ws + p.o_trans);
   }
   a.st = dev_status(workspace);
+  a.fault = debug_fault;
+  a.wait_ns = wait_limit(a.fault == kFaultScan || a.fault == kFaultJoin);
   ScanMaps maps;
   {
     const uint32_t box[3] = {64, 1, kGdnChunk};
@@ -444,6 +453,8 @@ qsa_status evict_impl(const CacheView& view, float* mass, int32_t keep, int32_t 
   a.kbar = static_cast<uint4*>(c->kbar);
   a.pg = view.pg;
   a.st = dev_status(workspace);
+  a.fault = debug_fault == kFaultMove;
+  a.wait_ns = wait_limit(a.fault);
   a.tiles = g.tiles;
   a.loaded = reinterpret_cast<int32_t*>(ws + g.o_loaded);
   a.before = reinterpret_cast<int32_t*>(ws + g.o_before);
@@ -469,6 +480,12 @@ qsa_status evict_impl(const CacheView& view, float* mass, int32_t keep, int32_t 
 }  // namespace
 
 extern "C" {
+
+qsa_status qsa_set_debug_fault(int32_t fault) {
+  if (fault < 0 || fault > kFaultMove) return QSA_ERR_INVALID_ARG;
+  debug_fault = fault;
+  return QSA_OK;
+}
 
 qsa_status qsa_accumulate_weights(const void* q, const qsa_cache* cache, const int32_t* sel_idx,
                                   const int32_t* sel_cnt, int32_t topk, float* mass,

@@ -38,7 +38,8 @@
  *   - bf16 means IEEE bfloat16 (raw 16-bit); fp32 is IEEE single.
  *   - Calls are re-entrant; the only global state is the cached driver entry point for
  *     tensor-map encoding, and, for qsa_decode_noalloc, its static scratch array and the
- *     per-device address of that array.  Concurrent calls must not share a workspace.
+ *     per-device address of that array (and a thread's qsa_set_debug_fault, 0 in normal use).
+ *     Concurrent calls must not share a workspace.
  */
 #ifndef QSA_H_
 #define QSA_H_
@@ -509,6 +510,15 @@ QSA_API qsa_status qsa_evict(const qsa_cache *cache, float *mass, int32_t keep_b
 QSA_API qsa_status qsa_evict_paged(const qsa_paged_cache *cache, float *mass, int32_t keep_blocks,
                                    int32_t sink_blocks, int32_t recent_blocks, int32_t *kept,
                                    void *workspace, size_t ws_bytes, qsa_stream_t stream);
+
+/* Testing only; 0 (no fault) in normal use.  Of the calling thread's next calls,
+ *   1: qsa_gated_deltanet_extend's first walk is short of a copy,
+ *   2: its first join of segments is (where a call has one),
+ *   3: qsa_evict's first tile of blocks does not say that it has been read,
+ * and the waits of such a call give up after 1 ms instead of 2 s: its device status reads
+ * QSA_ERR_TIMEOUT (sites 330 to 349, 350, 313) and what it wrote is undefined.  Any other call may
+ * follow at once.  Other values: QSA_ERR_INVALID_ARG. */
+QSA_API qsa_status qsa_set_debug_fault(int32_t fault);
 
 #ifdef __cplusplus
 }
