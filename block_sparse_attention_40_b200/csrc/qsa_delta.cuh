@@ -190,33 +190,41 @@ __global__ void __launch_bounds__(kStepThreads) k_delta_step(DeltaArgs a) {
 // writes) of the inner segments while the first ones run whole, k_delta_join takes the states
 // through, and a second pass writes the other segments' outputs.
 //
-// q, k and v are bf16 and exact as operands; the fp32 operands go in as parts.  What a token
-// writes carries T and U straight into the state: three bf16 parts each, x = hi + mid + lo to
-// 2^-24 of x.  W and S meet in a sum over 128 columns: two fp16 parts each (hi + lo to 2^-22 of
-// x), scaled by powers of two (a row of S, all of W) so that fp16 holds them; the product lo lo
-// (2^-24) is left out.  What only the bf16 output sees, S in Q S^T and M and U, is rounded to
-// fp16 once, scaled by rows as well.  Sums are fp32 throughout, running log gates fp64 (a reset
-// adds -87, after which fp32 differences would be off by 2^-11).
+// q, k and v are bf16 and exact as operands; the fp32 operands go in as parts.  T, U and M: three
+// bf16 parts each, x = hi + mid + lo to 2^-24 of x (of M U, the products of at least 2^-16).  W and
+// S: two fp16 parts each (hi + lo to 2^-22 of x), scaled by powers of two (a row of S, all of W) so
+// that fp16 holds them; the product lo lo (2^-24) of W S is left out.  So an output is rounded to
+// fewer than 22 bits once, to bf16 at its end.  Sums are fp32 throughout, running log gates fp64 (a
+// reset adds -87, after which fp32 differences would be off by 2^-11).
 
 // A record: operand tiles in the layout that the tensor core reads (rows of 128 bytes, 16-byte
 // words exchanged within 8 rows), then the gates.
 constexpr int kRecW = 0;                    // -W [64 t][128 d] fp16, two 64-column panels: hi, lo each
 constexpr int kRecU = 32768;                // T V [64 t][128 v] fp32
-constexpr int kRecM = 65536;                // M [64 t][64 j] fp16, rows scaled
-constexpr int kRecQ = 73728;                // Q [64 t][128 d] fp16, rows scaled (two panels)
-constexpr int kRecGate = 90112;             // fp32 [256], as follows
-constexpr int kRecBytes = 91136;
+constexpr int kRecM = 65536;                // M bf16, hi, mid, lo: its lower triangle by 16 columns j
+constexpr int kRecQ = 80896;                // Q [64 t][128 d] fp16, rows scaled (two panels)
+constexpr int kRecGate = 97280;             // fp32 [256], as follows
+constexpr int kRecBytes = 98304;
 constexpr int kGateQ = 0;                   // [64] e^g over the scale of the Q row
 constexpr int kGateU = 64;                  // [64] e^(g_C - g)
 constexpr int kGateC = 128;                 // e^(g_C)
 constexpr int kGateK = 129;                 // the largest |K|, times that of e^(g_C - g) where above 1
 constexpr int kGateW = 130;                 // 1 over the scale of W
-constexpr int kGateM = 192;                 // [64] 1 over the scale of the M row
 
 // Byte of element (r, c) of a [rows][64] bf16 tile.
 __host__ __device__ constexpr uint32_t tile_byte(uint32_t r, uint32_t c) {
   return r * 128 + (((c >> 3) ^ (r & 7)) << 4) + (c & 7) * 2;
 }
+
+// Columns 16 k .. of M, rows t >= 16 k: rows of 32 bytes whose two 16-byte words change places every
+// 4 rows, the four panels one behind the other.
+constexpr int kMPart = 5120;
+__host__ __device__ constexpr uint32_t m_panel(uint32_t k) { return 2048 * k - 256 * k * (k - 1); }
+__host__ __device__ constexpr uint32_t m_byte(uint32_t t, uint32_t j) {
+  const uint32_t r = t - (j & ~15u);
+  return m_panel(j >> 4) + r * 32 + ((((j >> 3) ^ (r >> 2)) & 1) << 4) + (j & 7) * 2;
+}
+static_assert(m_panel(4) == kMPart && 3 * kMPart <= kRecQ - kRecM, "M's parts");
 
 // First record of sequence s whose tokens start at `begin`: sequences never overlap, since
 // floor(end / 64) - floor(begin / 64) + 1 >= ceil((end - begin) / 64).
@@ -245,6 +253,13 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int a_mn_majo
   return idesc_bf16_f32(M, N, a_mn_major, b_mn_major) & ~((1u << 7) | (1u << 10));
 }
 
+// Shared-memory descriptor of a K-major tile with rows of 32 bytes, 8-row atoms `sbo_bytes` apart,
+// words exchanged as m_byte has them (the 32-byte swizzle).
+__device__ __forceinline__ uint64_t smem_desc_sw32(uint32_t saddr, uint32_t sbo_bytes) {
+  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) |
+         static_cast<uint64_t>((sbo_bytes >> 4) & 0x3FFFu) << 32 | 1ull << 46 | 6ull << 61;
+}
+
 // x -= lo(h), y -= hi(h): one mixed-precision instruction each
 __device__ __forceinline__ void take_bf16x2(uint32_t h, float* x, float* y) {
   asm("{\n\t.reg .b16 l, h, m;\n\tmov.b32 {l, h}, %2;\n\tmov.b16 m, 0xBF80;\n\t"
@@ -262,13 +277,14 @@ __device__ __forceinline__ uint32_t pack_f16x2(float x, float y) {
   const __half2 h = __floats2half2_rn(x, y);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+// x = hi + mid + lo, 8 bits each, the upper ones cut off: exact, in fewer cycles than rounded parts
 __device__ __forceinline__ void split3_bf16x2(float x, float y, uint32_t* hi, uint32_t* mid,
                                               uint32_t* lo) {
-  *hi = pack_bf16x2(x, y);
+  *hi = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
   take_bf16x2(*hi, &x, &y);
-  *mid = pack_bf16x2(x, y);
+  *mid = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
   take_bf16x2(*mid, &x, &y);
-  *lo = pack_bf16x2(x, y);
+  *lo = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
 }
 __device__ __forceinline__ void split_f16x2(float x, float y, uint32_t* hi, uint32_t* lo) {
   *hi = pack_f16x2(x, y);
@@ -352,7 +368,7 @@ __device__ __forceinline__ void bulk_store_wait() {
 // that is done with: Q becomes the scaled fp16 Q in place, then holds M, then V; K and Tu become W.
 // 16,384 chunks (8 x 8,192 tokens x 16 heads): 580 us, 5.2 us of an SM a chunk, bound by shared
 // memory (68% of its cycles; instructions issue in 54%; three CTAs an SM take as long); the bytes
-// (48 KB in, 89 KB out) would take 343 us.
+// (48 KB in, 96 KB out) would take 360 us.
 constexpr int kPrepThreads = 256;
 constexpr int kPrepLdA = kGdnChunk + 8;   // fp32 row stride of L / Tu: 8 rows x 4 pairs without conflicts
 struct PrepSmem {
@@ -424,6 +440,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) k_delta_prep(DeltaChunkArgs c
   const int n = static_cast<int>(len - c * kGdnChunk < kGdnChunk ? len - c * kGdnChunk : kGdnChunk);
   const int h = ca.head0 + blockIdx.y, kh = h / (a.heads / a.key_heads);
   unsigned char* rec = ca.rec + (r * ca.nheads + blockIdx.y) * static_cast<int64_t>(kRecBytes);
+  asm volatile("" : "+l"(rec));   // one register pair, not what it is computed from (spills cost 50 us)
   float la[2] = {0.f, 0.f}, bt[2] = {0.f, 0.f};
   if (warp == 0) {   // two tokens a lane
 #pragma unroll
@@ -538,7 +555,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) k_delta_prep(DeltaChunkArgs c
     const int t = (tid - 128) >> 1, half = tid & 1;
     unsigned char* p = S.q + 8192 * half;
     uint32_t m2 = 0u;
-#pragma unroll
+#pragma unroll 2
     for (int i = 0; i < 8; ++i) {
       // the two panels' words of a row lie in the same banks: the halves take them in turn
       const uint4 x = *reinterpret_cast<const uint4*>(p + tile_byte(t, 8 * (i ^ (4 * half))));
@@ -549,7 +566,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) k_delta_prep(DeltaChunkArgs c
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
     float inv;
     const uint16_t sc = static_cast<uint16_t>(__float_as_uint(row_scale(m, &inv)) >> 16);
-#pragma unroll
+#pragma unroll 2
     for (int i = 0; i < 8; ++i) {
       uint4* at = reinterpret_cast<uint4*>(p + tile_byte(t, 8 * (i ^ (4 * half))));
       const uint4 x = *at;
@@ -564,33 +581,25 @@ __global__ void __launch_bounds__(kPrepThreads, 4) k_delta_prep(DeltaChunkArgs c
       bulk_store_wait();
     }
     named_barrier_sync(1, 128);
-    float ma = 0.f, mb = 0.f;
 #pragma unroll
     for (int nt = 0; nt < 8; ++nt) {
-      ma = fmaxf(ma, fmaxf(fabsf(acc[nt][0]), fabsf(acc[nt][1])));
-      mb = fmaxf(mb, fmaxf(fabsf(acc[nt][2]), fabsf(acc[nt][3])));
-    }
+      if (nt < 2 * (rb + 1)) {
+        const int j = 8 * nt + 2 * tq;
+        const float* x = acc[nt];
 #pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-      ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, o));
-      mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, o));
-    }
-    float ia, ib;
-    const float sa = row_scale(ma, &ia), sb = row_scale(mb, &ib);
-    if (tq == 0) {
-      gate[kGateM + ta] = ia;
-      gate[kGateM + tb] = ib;
-    }
+        for (int i = 0; i < 2; ++i) {
+          uint32_t part[3];
+          split3_bf16x2(x[2 * i], x[2 * i + 1], &part[0], &part[1], &part[2]);
+          unsigned char* at = S.q + m_byte(i ? tb : ta, j);
 #pragma unroll
-    for (int nt = 0; nt < 8; ++nt) {
-      const int j = 8 * nt + 2 * tq;
-      *reinterpret_cast<uint32_t*>(S.q + tile_byte(ta, j)) = pack_f16x2(sa * acc[nt][0], sa * acc[nt][1]);
-      *reinterpret_cast<uint32_t*>(S.q + tile_byte(tb, j)) = pack_f16x2(sb * acc[nt][2], sb * acc[nt][3]);
+          for (int e = 0; e < 3; ++e) *reinterpret_cast<uint32_t*>(at + e * kMPart) = part[e];
+        }
+      }
     }
     fence_proxy_async_smem();
     named_barrier_sync(1, 128);
     if (tid == 128) {
-      bulk_store(rec + kRecM, S.q, 8192);
+      bulk_store(rec + kRecM, S.q, 3 * kMPart);
       bulk_store_wait();
     }
     __syncwarp();
@@ -762,7 +771,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) k_delta_prep(DeltaChunkArgs c
 // operand in tensor memory, written there by the threads that computed it, and no result goes
 // back to shared memory:
 //     D_W [v][t] = -S0 W^T          A = S0 (fp16 parts); S0 hi W hi^T and S0 hi W lo^T side by side
-//     D_Q [v][t] = S0 Q^T, then U^T M^T
+//     D_Q [v][t] = S0 Q^T, then U^T M^T (by 16 columns j of M, whose rows t >= j count)
 //     D_S [v][d] = U'^T K,  U' = diag(e^(g_C - g)) U,  U = (T V)^T + D_W
 // Four warpgroups hold the fp32 state in registers (a lane has one v, 32 of its d's), form U and
 // U' and then S; two write the outputs; one warp issues the products and three load, each its own
@@ -781,14 +790,16 @@ __global__ void __launch_bounds__(kPrepThreads, 4) k_delta_prep(DeltaChunkArgs c
 constexpr int kScanThreads = 896;
 constexpr int kScanW = 0;                               // [2] W, K, gates
 constexpr int kScanWBytes = 32768 + 16384 + 1024;
-constexpr int kScanQ = kScanW + 2 * kScanWBytes;        // [2] Q, M, the gates again (the outputs' warps read them late)
-constexpr int kScanQBytes = 16384 + 8192 + 1024;
-constexpr int kScanU = kScanQ + 2 * kScanQBytes;        // [2] T V
+constexpr int kScanQ = kScanW + 2 * kScanWBytes;        // [2] Q, the gates again (the outputs' warps read them late)
+constexpr int kScanQBytes = 16384 + 1024;
+constexpr int kScanM = kScanQ + 2 * kScanQBytes;        // M, once: asked for a chunk ahead of its product
+constexpr int kScanMBytes = 3 * kMPart;
+constexpr int kScanU = kScanM + kScanMBytes;            // [2] T V
 constexpr int kScanUBytes = 32768;
 constexpr int kScanBars = kScanU + 2 * kScanUBytes;
-constexpr int kScanSmemBytes = kScanBars + 8192;
+constexpr int kScanSmemBytes = kScanBars + 6144;
 static_assert(kScanSmemBytes <= 232448, "shared memory per CTA");
-static_assert(kScanWBytes % 1024 == 0 && kScanQBytes % 1024 == 0, "tiles on 1 KB boundaries");
+static_assert(kScanWBytes % 1024 == 0 && kScanQBytes % 1024 == 0 && kScanMBytes % 1024 == 0, "tiles on 1 KB boundaries");
 
 // what a launch does: the whole walk; or, where sequences are cut into segments, the first segments
 // whole and the inner ones' states from zero and transitions, then the outputs of all segments
@@ -796,17 +807,17 @@ static_assert(kScanWBytes % 1024 == 0 && kScanQBytes % 1024 == 0, "tiles on 1 KB
 constexpr int kScanWhole = 0, kScanEnds = 1, kScanOutputs = 2;
 
 struct ScanBars {
-  uint64_t full_w[2], empty_w[2], full_u[2], empty_u[2], full_q[2], empty_q[2];
+  uint64_t full_w[2], empty_w[2], full_u[2], empty_u[2], full_q[2], empty_q[2], full_m, empty_m;
   uint64_t s_part[2];           // 16 columns of S of every quarter
   uint64_t d1, uw_full, u_full, ds, qs, q_free, o, o_free, mma_done;
   uint64_t rows[4];             // the four warps of 32 rows have their maxima in place
   uint32_t tmem;
   int abort;
-  // by row: 1 over the scales of S and U (by the parity of the chunk); the quarters' largest |S|, |U|
-  float scale[2][kGdnDim], uscale[2][kGdnDim];
+  // by row: 1 over the scale of S (by the parity of the chunk); the quarters' largest |S|, |U|
+  float scale[2][kGdnDim];
   float smax[4][kGdnDim], umax[4][kGdnDim];
 };
-static_assert(sizeof(ScanBars) <= 8192, "barriers");
+static_assert(sizeof(ScanBars) <= 6144, "barriers");
 
 // 32 lanes x 32 bit, 8 (4) consecutive columns per thread
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
@@ -917,7 +928,8 @@ __global__ void __launch_bounds__(kScanThreads, 1)
       mbar_init(&B.full_q[i], 1);
       mbar_init(&B.empty_q[i], 1 + 8);
     }
-
+    mbar_init(&B.full_m, 1);
+    mbar_init(&B.empty_m, 1);
     for (int i = 0; i < 2; ++i) mbar_init(&B.s_part[i], 16);
     mbar_init(&B.uw_full, 16);
     mbar_init(&B.d1, 1);
@@ -942,8 +954,9 @@ __global__ void __launch_bounds__(kScanThreads, 1)
   pdl_wait();
   // all 512 columns are this CTA's, so they start at 0: addresses are known to the compiler
   constexpr uint32_t tm = 0;
-  // columns: S hi 64, S lo 64, D_S 128, D_W 64, its (hi, lo) part 64 (then U' mid and lo, each
-  // quarter of the threads in the columns that it has read), D_Q 64, U' hi 32, U 32
+  // columns: S hi 64, S lo 64, D_S 128, D_W 64, its (hi, lo) part 64 (then, each quarter of the
+  // threads in the 16 columns that it has read, U' mid and lo, 8 each, and U mid and lo behind
+  // them), D_Q 64, U' hi 32, U hi 32
   constexpr uint32_t tS = tm, tDS = tm + 128, tDW = tm + 256, tDQ = tm + 384, tUw = tm + 448,
                      tU = tm + 480;
   volatile int* abort = &B.abort;
@@ -1058,13 +1071,16 @@ __global__ void __launch_bounds__(kScanThreads, 1)
         umax = row_max(B.umax);
         sc = row_scale(fmaf(gc, row_max(B.smax), 64.f * kmax * umax), &inv);
         if (outputs) {
-          float iu;
-          const float su = row_scale(umax, &iu);
-          uint32_t w[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) w[i] = pack_f16x2(su * u[2 * i], su * u[2 * i + 1]);
-          if (quarter == 0) B.uscale[sg][v] = iu;
-          tmem_st8(tU + lb + 8 * quarter, w);
+          for (int b = 0; b < 2; ++b) {
+            uint32_t vh[4], vm[4], vl[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              split3_bf16x2(u[8 * b + 2 * i], u[8 * b + 2 * i + 1], &vh[i], &vm[i], &vl[i]);
+            tmem_st4(tU + lb + 8 * quarter + 4 * b, vh);
+            tmem_st4(tDW + 8 + lb + 16 * quarter + 4 * b, vm);
+            tmem_st4(tDW + 72 + lb + 16 * quarter + 4 * b, vl);
+          }
           signal(&B.u_full);
         }
         ok = scan_wait(&B.ds, c & 1, abort, ca.wait_ns, 332);
@@ -1117,9 +1133,8 @@ __global__ void __launch_bounds__(kScanThreads, 1)
 #pragma unroll 1
       for (int c = 0; c < nc; ++c) {
         const int sg = c & 1;
-        const float* gate = reinterpret_cast<const float*>(smem + kScanQ + sg * kScanQBytes + 24576);
+        const float* gate = reinterpret_cast<const float*>(smem + kScanQ + sg * kScanQBytes + 16384);
         const float4* eg = reinterpret_cast<const float4*>(gate + kGateQ + 32 * half);
-        const float2* gm = reinterpret_cast<const float2*>(gate + kGateM + 32 * half);
         bool ok = scan_wait(&B.full_q[sg], (c >> 1) & 1, abort, ca.wait_ns, 333) &&
                   scan_wait(&B.qs, c & 1, abort, ca.wait_ns, 334);
         if (!__all_sync(0xffffffffu, ok)) break;
@@ -1140,11 +1155,13 @@ __global__ void __launch_bounds__(kScanThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&B.q_free);
+        if (lane == 0) {
+          mbar_arrive(&B.q_free);
+          mbar_arrive(&B.empty_q[sg]);   // the gates have been read
+        }
         ok = scan_wait(&B.o, c & 1, abort, ca.wait_ns, 335);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
-        const float iu = B.uscale[sg][v];
         const int64_t left = ntok - static_cast<int64_t>(c) * kGdnChunk - 32 * half - (lane & 1);
         const int n = static_cast<int>(left < kGdnChunk ? left : kGdnChunk);   // mine: tokens i < n
         // lanes in pairs: the even one stores both its own and its neighbour's value of token t,
@@ -1162,17 +1179,13 @@ __global__ void __launch_bounds__(kScanThreads, 1)
           }
 #pragma unroll
           for (int i = 0; i < 16; i += 2) {
-            const float2 e = gm[(i0 + i) / 2];
-            const uint32_t w = pack_bf16x2(fmaf(iu * e.x, x[i], y[i0 + i]),
-                                           fmaf(iu * e.y, x[i + 1], y[i0 + i + 1]));
+            const uint32_t w = pack_bf16x2(x[i] + y[i0 + i], x[i + 1] + y[i0 + i + 1]);
             const uint32_t z = __shfl_xor_sync(0xffffffffu, w, 1);
             const uint32_t both = __byte_perm(w, z, sel);
             if (i0 + i < n) *reinterpret_cast<uint32_t*>(op) = both;
             op += 2 * step;
           }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&B.empty_q[sg]);
       }
     }
   } else {
@@ -1186,6 +1199,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     // warp alone would fill the instruction cache.
     const uint64_t dk = smem_desc_sw128(smem_u32(smem), 0, 1024);        // rows of 128 bytes
     const uint64_t dm = smem_desc_sw128(smem_u32(smem), 8192, 1024);     // two column panels
+    const uint64_t dmm = smem_desc_sw32(smem_u32(smem) + kScanM, 256);   // M: rows of 32 bytes
     // (the lanes stay together, whatever each has seen)
     auto wait = [&](uint64_t* bar, uint32_t parity, int site) {
       return __all_sync(0xffffffffu, scan_wait(bar, parity, abort, ca.wait_ns, site)) != 0;
@@ -1228,10 +1242,13 @@ __global__ void __launch_bounds__(kScanThreads, 1)
 #pragma unroll 1
             for (int k = 0; k < 4; ++k)
 #pragma unroll
-              for (int kh = 0; kh < 2; ++kh)
-                umma_ts(tDQ, tS + 32 * kh + 8 * k, dk + sq + 512 * kh + 2 * k, kIdF16,
-                        k + kh > 0 ? 1u : 0u);
+              for (int kh = 0; kh < 2; ++kh) {
+                const uint64_t dq = dk + sq + 512 * kh + 2 * k;
+                umma_ts(tDQ, tS + 32 * kh + 8 * k, dq, kIdF16, k + kh > 0 ? 1u : 0u);
+                umma_ts(tDQ, tS + 64 + 32 * kh + 8 * k, dq, kIdF16, 1u);
+              }
             umma_commit(&B.qs);
+            umma_commit(&B.empty_q[sg]);
           }
           __syncwarp();
         }
@@ -1253,15 +1270,25 @@ __global__ void __launch_bounds__(kScanThreads, 1)
       __syncwarp();
       if (outputs) {
         if (!wait(&B.q_free, c & 1, 346)) break;
+        if (!wait(&B.full_m, c & 1, 349)) break;
         if (!wait(&B.u_full, c & 1, 348)) break;
         tc_fence_after();
         if (elect_one()) {
-          // D_Q = U^T M^T
+          // D_Q = U^T M^T: hi (hi, mid, lo), mid (hi, mid), lo hi; M is zero above its diagonal, so
+          // that columns j = 16 k .. take part in tokens t >= 16 k only
 #pragma unroll 1
-          for (int k = 0; k < 4; ++k)
-            umma_ts(tDQ, tU + 8 * k, dk + sq + 1024 + 2 * k, kIdF16, k > 0 ? 1u : 0u);
+          for (int k = 0; k < 4; ++k) {
+            const uint64_t d = dmm + (m_panel(k) >> 4);
+            const uint32_t to = tDQ + 16 * k, id = idesc_bf16_f32(128, 64 - 16 * k, 0, 0);
+            umma_ts(to, tU + 8 * k, d, id, k > 0 ? 1u : 0u);
+            umma_ts(to, tU + 8 * k, d + (kMPart >> 4), id, 1u);
+            umma_ts(to, tU + 8 * k, d + 2 * (kMPart >> 4), id, 1u);
+            umma_ts(to, tDW + 8 + 16 * k, d, id, 1u);
+            umma_ts(to, tDW + 8 + 16 * k, d + (kMPart >> 4), id, 1u);
+            umma_ts(to, tDW + 72 + 16 * k, d, id, 1u);
+          }
           umma_commit(&B.o);
-          umma_commit(&B.empty_q[sg]);
+          umma_commit(&B.empty_m);
         }
         __syncwarp();
       }
@@ -1271,33 +1298,33 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     mbar_drain(&B.mma_done, 0);
     __syncwarp();
   } else {
-    // ---- loads: warp 25: W, K and the gates; 26: T V; 27: Q, M and the gates -------------------
+    // ---- loads: warp 25: W, K and the gates; 26: T V; 27: Q and the gates, M -------------------
     const int who = warp - 25;
     uint64_t* full = who == 0 ? B.full_w : who == 1 ? B.full_u : B.full_q;
     uint64_t* empty = who == 0 ? B.empty_w : who == 1 ? B.empty_u : B.empty_q;
     const bool on = who == 0 || (who == 1 ? !trans && !(ca.fault == kFaultScan && hl + row + blockIdx.z == 0)
                                           : outputs);
     const int kh = h / (a.heads / a.key_heads);
-    int issued = 0;
+    int issued = 0, issued_m = 0;
+    const unsigned char* rec = ca.rec + ((rec0 + c0) * ca.nheads + hl) * static_cast<int64_t>(kRecBytes);
 #pragma unroll 1
-    for (int c = 0; on && c < nc; ++c) {
+    for (int c = 0; on && c < nc; ++c, rec += ca.nheads * static_cast<int64_t>(kRecBytes)) {
       const int sg = c & 1;
       const bool ok = c < 2 || scan_wait(&empty[sg], ((c >> 1) & 1) ^ 1, abort, ca.wait_ns, 347);
       if (!__all_sync(0xffffffffu, ok)) break;
-      const int64_t at = t0 + static_cast<int64_t>(c) * kGdnChunk;
-      const int64_t left = ntok - static_cast<int64_t>(c) * kGdnChunk;
-      const int n = static_cast<int>(left < kGdnChunk ? left : kGdnChunk);
+      const int at = static_cast<int>(t0) + c * kGdnChunk;
+      const int left = static_cast<int>(ntok) - c * kGdnChunk;
+      const int n = left < kGdnChunk ? left : kGdnChunk;
       const bool whole = n == kGdnChunk;
       unsigned char* stage = smem + (who == 0 ? kScanW + sg * kScanWBytes : who == 1 ? kScanU + sg * kScanUBytes : kScanQ + sg * kScanQBytes);
       if (lane == 0) {
-        const unsigned char* rec = ca.rec + ((rec0 + c0 + c) * ca.nheads + hl) * static_cast<int64_t>(kRecBytes);
         if (who == 0) {
           mbar_arrive_expect_tx(&full[sg], 32768 + 1024 + (whole ? 16384 : 0));
           bulk_load(stage, rec + kRecW, 32768, &full[sg]);
           bulk_load(stage + 49152, rec + kRecGate, 1024, &full[sg]);
           if (whole) {
-            tma_load_3d(stage + 32768, &maps.k, 0, kh, static_cast<int>(at), &full[sg]);
-            tma_load_3d(stage + 32768 + 8192, &maps.k, 64, kh, static_cast<int>(at), &full[sg]);
+            tma_load_3d(stage + 32768, &maps.k, 0, kh, at, &full[sg]);
+            tma_load_3d(stage + 32768 + 8192, &maps.k, 64, kh, at, &full[sg]);
           }
         } else if (who == 1) {
           mbar_arrive_expect_tx(&full[sg], kScanUBytes);
@@ -1305,8 +1332,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
         } else {
           mbar_arrive_expect_tx(&full[sg], kScanQBytes);
           bulk_load(stage, rec + kRecQ, 16384, &full[sg]);
-          bulk_load(stage + 16384, rec + kRecM, 8192, &full[sg]);
-          bulk_load(stage + 24576, rec + kRecGate, 1024, &full[sg]);
+          bulk_load(stage + 16384, rec + kRecGate, 1024, &full[sg]);
         }
       }
       __syncwarp();
@@ -1314,7 +1340,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
       if (who == 0) {
         if (!whole) {   // the rows behind the sequence's last token must be zero
           const uint32_t to = smem_u32(stage + 32768);
-          const __nv_bfloat16* from = a.k + (at * a.key_heads + kh) * kGdnDim;
+          const __nv_bfloat16* from = a.k + (static_cast<int64_t>(at) * a.key_heads + kh) * kGdnDim;
           const int64_t step = static_cast<int64_t>(a.key_heads) * kGdnDim;
 #pragma unroll 1
           for (int e = lane; e < kGdnChunk * 16; e += 32) {
@@ -1327,10 +1353,21 @@ __global__ void __launch_bounds__(kScanThreads, 1)
           __syncwarp();
         }
         if (lane == 0) mbar_arrive(&full[sg]);
+      } else if (who == 2) {
+        const bool free = c == 0 || scan_wait(&B.empty_m, (c - 1) & 1, abort, ca.wait_ns, 336);
+        if (!__all_sync(0xffffffffu, free)) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&B.full_m, kScanMBytes);
+          bulk_load(smem + kScanM, rec + kRecM, kScanMBytes, &B.full_m);
+        }
+        __syncwarp();
+        ++issued_m;
       }
     }
-    if (lane == 0 && *abort)   // no copy may land after the CTA is gone
+    if (lane == 0 && *abort) {   // no copy may land after the CTA is gone
       for (int c = issued > 2 ? issued - 2 : 0; c < issued; ++c) mbar_drain(&full[c & 1], (c >> 1) & 1);
+      if (issued_m > 0) mbar_drain(&B.full_m, (issued_m - 1) & 1);
+    }
     }
   }
   tc_fence_before();

@@ -1,0 +1,64 @@
+"""GPU tests of how exactly the delta rule's chunked form computes: cases whose result is known to the
+bit, and cases whose magnitudes differ by many orders, against the fp64 oracle.
+
+Tolerances.  Token by token in fp32 a step is off by at most 21 half steps (2^-24) of the largest
+row norm R_t of the state it leaves (two roundings of the update, 19 of the dot S k), and what it is
+off by goes on through the later gates (|I - beta k k^T| <= 1 for unit-norm keys).  So a state is off by
+    E_T = 21 * 2^-24 * sum_t R_t prod_{t < s <= T} a_s
+and an output, rounded once to bf16 (half a step: 2^-8 of the value), by 2^-8 |o_t| + E_t +
+21 * 2^-24 R_t.  The chunked form is held to the same.
+"""
+import numpy as np
+import pytest
+import torch
+
+import block_sparse_attention_40_b200 as qsa
+from oracle.gated_deltanet import gated_delta_rule
+from tests.gpu_helpers import needs_gpu
+from tests.test_gpu_delta import DEV, STATE_TOL, _compare, _draw, _np
+
+pytestmark = [pytest.mark.gpu, needs_gpu]
+FINE = 1 + 2.0 ** -8 + 2.0 ** -13      # just above half way from 1 to the next bf16, 1 + 2^-7
+
+
+def _blank(T, heads):
+    """No decay, nothing written, all vectors zero."""
+    x = torch.zeros((T, heads, 128), dtype=torch.bfloat16, device=DEV)
+    g = torch.zeros((T, heads), device=DEV)
+    return x, x.clone(), x.clone(), g, g.clone()
+
+
+def test_out_is_rounded_once_from_the_state():
+    # one-hot queries of a state that stays: every output is one of its entries
+    T, heads = 100, 2
+    q, k, v, la, beta = _blank(T, heads)
+    g = torch.Generator().manual_seed(1)
+    t = torch.arange(T)
+    q[t, :, (7 * t) % 128] = 1.0
+    k[:, :, 3] = 1.0
+    i = torch.arange(128)
+    sign = torch.where(torch.rand((heads, 128, 128), generator=g) < 0.5, -1.0, 1.0)
+    states = (sign * FINE * 2.0 ** ((i[:, None] + i) % 5)).to(DEV)[None].contiguous()
+    want = states[0][:, :, (7 * t) % 128].permute(2, 0, 1).to(torch.bfloat16)
+    out = qsa.gated_deltanet_extend(q, k, v, la, beta, [0, T], states)
+    assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("fine", ["key product", "write"])
+def test_out_is_rounded_once_from_the_writes(fine):
+    # one token writes, all read it: the product q.k (1 + 2^-8 + 2^-13), or what is written
+    T, heads = 100, 2
+    q, k, v, la, beta = _blank(T, heads)
+    states = torch.zeros((1, heads, 128, 128), device=DEV)
+    sign = torch.where(torch.arange(128) % 3 == 0, -1.0, 1.0).to(DEV)
+    v[0] = sign.to(torch.bfloat16)
+    if fine == "write":
+        k[0, :, 9] = 1.0
+        q[:, :, 9] = 1.0
+        beta[0] = FINE
+    else:
+        k[0, :, :3] = 1.0
+        q[:, :, 0], q[:, :, 1], q[:, :, 2] = 1.0, 2.0 ** -8, 2.0 ** -13
+        beta[0] = 1.0
+    out = qsa.gated_deltanet_extend(q, k, v, la, beta, [0, T], states)
+    assert torch.all(out == (sign * (1 + 2.0 ** -7)).to(torch.bfloat16))
