@@ -208,7 +208,7 @@ constexpr int kRecBytes = 98304;
 constexpr int kGateQ = 0;                   // [64] e^g over the scale of the Q row
 constexpr int kGateU = 64;                  // [64] e^(g_C - g)
 constexpr int kGateC = 128;                 // e^(g_C)
-constexpr int kGateK = 129;                 // the largest |K|, times that of e^(g_C - g) where above 1
+constexpr int kGateK = 129;                 // the largest |K|
 constexpr int kGateW = 130;                 // 1 over the scale of W
 
 // Byte of element (r, c) of a [rows][64] bf16 tile.
@@ -378,7 +378,7 @@ struct PrepSmem {
   float gate[256];
   float g_hi[kGdnChunk], g_lo[kGdnChunk]; // running log gate in base 2, as a sum
   float beta[kGdnChunk], eg[kGdnChunk], beg[kGdnChunk];   // beta, e^g, their product
-  float wmax[8], kmax[4], umax;
+  float wmax[8], kmax[4];
 };
 static_assert(16384 + 4 * kGdnChunk * kPrepLdA >= 32768, "W fits");
 static_assert(sizeof(PrepSmem) <= 55 * 1024, "four CTAs an SM");
@@ -482,14 +482,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) k_delta_prep(DeltaChunkArgs c
       S.beg[t] = bt[i] * S.eg[t];
       gate[kGateU + t] = exp2f(static_cast<float>(gc - g2[i]));
     }
-    // gates above one make U' larger than U
-    float grow = fmaxf(gate[kGateU + 2 * lane], gate[kGateU + 2 * lane + 1]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) grow = fmaxf(grow, __shfl_xor_sync(0xffffffffu, grow, o));
-    if (lane == 0) {
-      gate[kGateC] = exp2f(static_cast<float>(gc));
-      S.umax = fmaxf(grow, 1.f);
-    }
+    if (lane == 0) gate[kGateC] = exp2f(static_cast<float>(gc));
   }
   cp_async_wait_all();
   __syncthreads();
@@ -742,7 +735,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) k_delta_prep(DeltaChunkArgs c
   float inv_w;
   const float sw = -row_scale(m, &inv_w);
   if (tid == 0) {
-    gate[kGateK] = S.umax * fmaxf(fmaxf(S.kmax[0], S.kmax[1]), fmaxf(S.kmax[2], S.kmax[3]));
+    gate[kGateK] = fmaxf(fmaxf(S.kmax[0], S.kmax[1]), fmaxf(S.kmax[2], S.kmax[3]));
     gate[kGateW] = inv_w;
   }
   unsigned char* w = S.k + 16384 * (warp >> 2);   // on into Tu's space
@@ -782,7 +775,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) k_delta_prep(DeltaChunkArgs c
 // x 16), 1,600 for S, most of whose conversion is instruction issue (two products' parts, 5 to 9
 // instructions an element).  S goes over in two parts, so that the products of one run while the
 // other is converted; S is scaled before it is known, by a bound on its rows,
-// |S| <= e^(g_C) max|S0| + 64 max|U| max|K| max(1, e^(g_C - g)); what only the outputs need (D_Q)
+// |S| <= e^(g_C) max|S0| + 64 max|U'| max|K|; what only the outputs need (D_Q)
 // runs in the gaps.  A form without W (X = V - e^g K S0^T, U = T X) would read 32 KB less a chunk
 // and have one more product and conversion in the chain.  8 x 8,192 tokens x 16 heads: 387 us on 128
 // SMs (121 KB a chunk: 5.1 TB/s); the same walk with fp32 state in shared memory and warp MMAs
@@ -813,7 +806,7 @@ struct ScanBars {
   uint64_t rows[4];             // the four warps of 32 rows have their maxima in place
   uint32_t tmem;
   int abort;
-  // by row: 1 over the scale of S (by the parity of the chunk); the quarters' largest |S|, |U|
+  // by row: 1 over the scale of S (by the parity of the chunk); the quarters' largest |S|, |U'|
   float scale[2][kGdnDim];
   float smax[4][kGdnDim], umax[4][kGdnDim];
 };
@@ -1055,9 +1048,13 @@ __global__ void __launch_bounds__(kScanThreads, 1)
           tmem_st4(tDW + 64 + lb + 16 * quarter + 4 * b, vl);
         }
         signal(&B.uw_full);
-        float umax = 0.f;
+        float umax = 0.f;   // of U', not of U: what a later gate takes back does not count
 #pragma unroll
-        for (int i = 0; i < 16; ++i) umax = fmaxf(umax, fabsf(u[i]));
+        for (int i = 0; i < 4; ++i) {
+          const float4 w = wk[i];
+          umax = fmaxf(fmaxf(umax, fabsf(w.x * u[4 * i])), fabsf(w.y * u[4 * i + 1]));
+          umax = fmaxf(fmaxf(umax, fabsf(w.z * u[4 * i + 2])), fabsf(w.w * u[4 * i + 3]));
+        }
         B.smax[quarter][v] = smax;
         B.umax[quarter][v] = umax;
         gc = gate[kGateC];

@@ -62,3 +62,40 @@ def test_out_is_rounded_once_from_the_writes(fine):
         beta[0] = 1.0
     out = qsa.gated_deltanet_extend(q, k, v, la, beta, [0, T], states)
     assert torch.all(out == (sign * (1 + 2.0 ** -7)).to(torch.bfloat16))
+
+
+def _carried(w, start):
+    """fp64 outputs, final state, E_t and R_t (see above) of one sequence, per token and head."""
+    x = [_np(y) for y in (w.q, w.k, w.v, w.log_alpha, w.beta)]
+    S, outs, E, R = _np(start), [], [], []
+    e = np.zeros(S.shape[0])
+    for t in range(x[0].shape[0]):
+        before = np.linalg.norm(S, axis=-1).max(axis=-1)
+        o, S = gated_delta_rule(*(y[t:t + 1] for y in x), S)
+        a = np.exp(np.maximum(x[3][t], -87.0))
+        r = np.maximum(np.linalg.norm(S, axis=-1).max(axis=-1), a * before)
+        e = a * e + 21 * 2.0 ** -24 * r
+        outs.append(o[0])
+        E.append(e)
+        R.append(r)
+    return np.stack(outs), S, np.stack(E), np.stack(R)
+
+
+def _check_carried(w, states):
+    start = states[0].clone()
+    ref, ref_state, E, R = _carried(w, start)
+    out = qsa.gated_deltanet_extend(w.q, w.k, w.v, w.log_alpha, w.beta, w.cu_seqlens, states)
+    torch.cuda.synchronize()
+    err = np.abs(_np(states[0]) - ref_state).max(axis=(1, 2))
+    assert np.all(err <= E[-1]), (err, E[-1])
+    tol = 2.0 ** -8 * np.abs(ref) + (E + 21 * 2.0 ** -24 * R)[..., None]
+    assert np.all(np.abs(_np(out) - ref) <= tol), (np.abs(_np(out) - ref) - tol).max()
+
+
+@pytest.mark.parametrize("big", [1e3, 1e6, 1e8])
+def test_a_large_write_before_a_reset_leaves_nothing(big):
+    # what token 5 wrote is gone at token 29, in the middle of its chunk
+    w, states = _draw([150], 2, 1, 1, seed=60, state=0.0)
+    w.v[5] *= big
+    w.log_alpha[29] = float("-inf")
+    _check_carried(w, states)
