@@ -192,14 +192,14 @@ __global__ void __launch_bounds__(kStepThreads) k_delta_step(DeltaArgs a) {
 //
 // q, k and v are bf16 and exact as operands; the fp32 operands go in as parts.  T, U and M: three
 // bf16 parts each, x = hi + mid + lo to 2^-24 of x (of M U, the products of at least 2^-16).  W and
-// S: two fp16 parts each (hi + lo to 2^-22 of x), scaled by powers of two (a row of S, all of W) so
+// S: two fp16 parts each (hi + lo to 2^-22 of x), scaled by powers of two (a row of S, a row of W) so
 // that fp16 holds them; the product lo lo (2^-24) of W S is left out.  So an output is rounded to
 // fewer than 22 bits once, to bf16 at its end.  Sums are fp32 throughout, running log gates fp64 (a
 // reset adds -87, after which fp32 differences would be off by 2^-11).
 
 // A record: operand tiles in the layout that the tensor core reads (rows of 128 bytes, 16-byte
 // words exchanged within 8 rows), then the gates.
-constexpr int kRecW = 0;                    // -W [64 t][128 d] fp16, two 64-column panels: hi, lo each
+constexpr int kRecW = 0;                    // -W [64 t][128 d] fp16, rows scaled, two 64-column panels: hi, lo each
 constexpr int kRecU = 32768;                // T V [64 t][128 v] fp32
 constexpr int kRecM = 65536;                // M bf16, hi, mid, lo: its lower triangle by 16 columns j
 constexpr int kRecQ = 80896;                // Q [64 t][128 d] fp16, rows scaled (two panels)
@@ -207,9 +207,9 @@ constexpr int kRecGate = 97280;             // fp32 [256], as follows
 constexpr int kRecBytes = 98304;
 constexpr int kGateQ = 0;                   // [64] e^g over the scale of the Q row
 constexpr int kGateU = 64;                  // [64] e^(g_C - g)
-constexpr int kGateC = 128;                 // e^(g_C)
-constexpr int kGateK = 129;                 // the largest |K|
-constexpr int kGateW = 130;                 // 1 over the scale of W
+constexpr int kGateW = 128;                 // [64] 1 over the scale of the W row
+constexpr int kGateC = 192;                 // e^(g_C)
+constexpr int kGateK = 193;                 // the largest |K|
 
 // Byte of element (r, c) of a [rows][64] bf16 tile.
 __host__ __device__ constexpr uint32_t tile_byte(uint32_t r, uint32_t c) {
@@ -378,7 +378,7 @@ struct PrepSmem {
   float gate[256];
   float g_hi[kGdnChunk], g_lo[kGdnChunk]; // running log gate in base 2, as a sum
   float beta[kGdnChunk], eg[kGdnChunk], beg[kGdnChunk];   // beta, e^g, their product
-  float wmax[8], kmax[4];
+  float wmax[2][kGdnChunk], kmax[4];
 };
 static_assert(16384 + 4 * kGdnChunk * kPrepLdA >= 32768, "W fits");
 static_assert(sizeof(PrepSmem) <= 55 * 1024, "four CTAs an SM");
@@ -721,32 +721,40 @@ __global__ void __launch_bounds__(kPrepThreads, 4) k_delta_prep(DeltaChunkArgs c
       }
     }
   }
-  float m = 0.f;
+  // a row's largest |W|, each half of the columns by another warp
+  float ma = 0.f, mb = 0.f;
 #pragma unroll
-  for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) m = fmaxf(m, fabsf(acc[nt][e]));
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (lane == 0) S.wmax[warp] = m;
-  __syncthreads();   // also: K and Tu have been read
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = fmaxf(m, S.wmax[i]);
-  float inv_w;
-  const float sw = -row_scale(m, &inv_w);
-  if (tid == 0) {
-    gate[kGateK] = fmaxf(fmaxf(S.kmax[0], S.kmax[1]), fmaxf(S.kmax[2], S.kmax[3]));
-    gate[kGateW] = inv_w;
+  for (int nt = 0; nt < 8; ++nt) {
+    ma = fmaxf(ma, fmaxf(fabsf(acc[nt][0]), fabsf(acc[nt][1])));
+    mb = fmaxf(mb, fmaxf(fabsf(acc[nt][2]), fabsf(acc[nt][3])));
   }
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1) {
+    ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, o));
+    mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, o));
+  }
+  if (tq == 0) {
+    S.wmax[warp >> 2][ta] = ma;
+    S.wmax[warp >> 2][tb] = mb;
+  }
+  __syncthreads();   // also: K and Tu have been read
+  float ia, ib;
+  const float sa = -row_scale(fmaxf(S.wmax[0][ta], S.wmax[1][ta]), &ia);
+  const float sb = -row_scale(fmaxf(S.wmax[0][tb], S.wmax[1][tb]), &ib);
+  if (warp < 4 && tq == 0) {
+    gate[kGateW + ta] = ia;
+    gate[kGateW + tb] = ib;
+  }
+  if (tid == 0) gate[kGateK] = fmaxf(fmaxf(S.kmax[0], S.kmax[1]), fmaxf(S.kmax[2], S.kmax[3]));
   unsigned char* w = S.k + 16384 * (warp >> 2);   // on into Tu's space
 #pragma unroll
   for (int nt = 0; nt < 8; ++nt) {
     uint32_t vh, vl;
     const int d = 8 * nt + 2 * tq;
-    split_f16x2(sw * acc[nt][0], sw * acc[nt][1], &vh, &vl);
+    split_f16x2(sa * acc[nt][0], sa * acc[nt][1], &vh, &vl);
     *reinterpret_cast<uint32_t*>(w + tile_byte(ta, d)) = vh;
     *reinterpret_cast<uint32_t*>(w + 8192 + tile_byte(ta, d)) = vl;
-    split_f16x2(sw * acc[nt][2], sw * acc[nt][3], &vh, &vl);
+    split_f16x2(sb * acc[nt][2], sb * acc[nt][3], &vh, &vl);
     *reinterpret_cast<uint32_t*>(w + tile_byte(tb, d)) = vh;
     *reinterpret_cast<uint32_t*>(w + 8192 + tile_byte(tb, d)) = vl;
   }
@@ -910,7 +918,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
   const float* src = seg > 0 ? ends - seg_stride : state;
   float* dst = last ? state : trans ? ca.seg_trans + (ends - ca.seg_state) : ends;
   const int64_t t0 = begin + c0 * kGdnChunk;
-  const int64_t ntok = (last ? len : c1 * kGdnChunk) - c0 * kGdnChunk;
+  const int ntok = static_cast<int>((last ? len : c1 * kGdnChunk) - c0 * kGdnChunk);
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -1022,8 +1030,8 @@ __global__ void __launch_bounds__(kScanThreads, 1)
              scan_wait(&B.d1, c & 1, abort, ca.wait_ns, 331);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
-        const float winv = inv * gate[kGateW];
         const float4* wk = reinterpret_cast<const float4*>(gate + kGateU + 16 * quarter);
+        const float4* wi = reinterpret_cast<const float4*>(gate + kGateW + 16 * quarter);
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           uint32_t x[8], y[8], vh[4], vm[4], vl[4];
@@ -1034,11 +1042,12 @@ __global__ void __launch_bounds__(kScanThreads, 1)
           reg_fence8(y);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float4 w = wk[2 * b + i];
+            const float4 w = wk[2 * b + i], z = wi[2 * b + i];
+            const float r[4] = {inv * z.x, inv * z.y, inv * z.z, inv * z.w};
             float* p = u + 8 * b + 4 * i;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              p[e] = fmaf(winv, __uint_as_float(y[4 * i + e]) + __uint_as_float(x[4 * i + e]), p[e]);
+              p[e] = fmaf(r[e], __uint_as_float(y[4 * i + e]) + __uint_as_float(x[4 * i + e]), p[e]);
             split3_bf16x2(w.x * p[0], w.y * p[1], &vh[2 * i], &vm[2 * i], &vl[2 * i]);
             split3_bf16x2(w.z * p[2], w.w * p[3], &vh[2 * i + 1], &vm[2 * i + 1], &vl[2 * i + 1]);
           }
@@ -1159,8 +1168,8 @@ __global__ void __launch_bounds__(kScanThreads, 1)
         ok = scan_wait(&B.o, c & 1, abort, ca.wait_ns, 335);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
-        const int64_t left = ntok - static_cast<int64_t>(c) * kGdnChunk - 32 * half - (lane & 1);
-        const int n = static_cast<int>(left < kGdnChunk ? left : kGdnChunk);   // mine: tokens i < n
+        const int left = ntok - c * kGdnChunk - 32 * half - (lane & 1);
+        const int n = left < kGdnChunk ? left : kGdnChunk;   // mine: tokens i < n
         // lanes in pairs: the even one stores both its own and its neighbour's value of token t,
         // the odd one of token t + 1
         __nv_bfloat16* op = a.out + ((t0 + static_cast<int64_t>(c) * kGdnChunk + 32 * half + (lane & 1)) * a.heads + h) * kGdnDim +
@@ -1310,7 +1319,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
       const bool ok = c < 2 || scan_wait(&empty[sg], ((c >> 1) & 1) ^ 1, abort, ca.wait_ns, 347);
       if (!__all_sync(0xffffffffu, ok)) break;
       const int at = static_cast<int>(t0) + c * kGdnChunk;
-      const int left = static_cast<int>(ntok) - c * kGdnChunk;
+      const int left = ntok - c * kGdnChunk;
       const int n = left < kGdnChunk ? left : kGdnChunk;
       const bool whole = n == kGdnChunk;
       unsigned char* stage = smem + (who == 0 ? kScanW + sg * kScanWBytes : who == 1 ? kScanU + sg * kScanUBytes : kScanQ + sg * kScanQBytes);

@@ -99,3 +99,15 @@ def test_a_large_write_before_a_reset_leaves_nothing(big):
     w.v[5] *= big
     w.log_alpha[29] = float("-inf")
     _check_carried(w, states)
+
+
+@pytest.mark.parametrize("size", [1e3, 1e6])
+def test_a_large_start_that_decays(size):
+    w, states = _draw([150], 2, 2, 1, seed=61, gate=(0.5, 1.0), state=0.3 * size)
+    _check_carried(w, states)
+
+
+def test_a_large_start_that_is_reset():
+    w, states = _draw([100], 2, 2, 1, seed=62, state=3e7)
+    w.log_alpha[40] = float("-inf")
+    _check_carried(w, states)
