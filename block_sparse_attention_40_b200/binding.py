@@ -763,7 +763,8 @@ class DeltaExtend:
         """q, k bf16 [T, key_heads, 128], v bf16 [T, heads, 128], log_alpha and beta fp32
         [T, heads]; states fp32 [slots, heads, 128 (v), 128 (k)] is updated in place: sequence s
         continues states[slots[s]] (int32 on the device; None: states[s]).  Returns out bf16
-        [T, heads, 128]."""
+        [T, heads, 128]; the rows of a sequence that is skipped (its slot outside the pool, or named
+        before) are left as they were (zero in a new tensor)."""
         index = self.device.index
         Hk, H = _delta_shapes(q, k, v, log_alpha, beta, states, slots, out, (self.T,),
                               self.num_seqs, index)
@@ -771,7 +772,7 @@ class DeltaExtend:
             raise ValueError(f"{Hk} key heads and {H} heads, the context has {self.key_heads} and "
                              f"{self.heads}")
         if out is None:
-            out = torch.empty_like(v)
+            out = torch.empty_like(v) if slots is None else torch.zeros_like(v)
         if self.T == 0:
             return out
         _call("qsa_gated_deltanet_extend", index, q.data_ptr(), k.data_ptr(), v.data_ptr(),

@@ -111,3 +111,17 @@ def test_a_large_start_that_is_reset():
     w, states = _draw([100], 2, 2, 1, seed=62, state=3e7)
     w.log_alpha[40] = float("-inf")
     _check_carried(w, states)
+
+
+# ---- rows that are skipped, gates that are no number ---------------------------------------------
+def test_extend_out_of_skipped_rows_is_zero():
+    lens = [70, 40, 65, 33]
+    w, states = _draw(lens, 2, 2, 3, seed=63)
+    slots = torch.tensor([1, -1, 1, 0], dtype=torch.int32, device=DEV)
+    junk = torch.full_like(w.v, float("nan"))
+    del junk      # its memory is the next tensor's of this size
+    out = qsa.gated_deltanet_extend(w.q, w.k, w.v, w.log_alpha, w.beta, w.cu_seqlens, states,
+                                    slots=slots)
+    torch.cuda.synchronize()
+    assert torch.count_nonzero(out[70:175]).item() == 0
+    assert torch.all(torch.isfinite(out)) and torch.count_nonzero(out[:70]).item() > 0
