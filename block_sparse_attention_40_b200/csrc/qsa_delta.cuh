@@ -65,6 +65,11 @@ __device__ __forceinline__ bool delta_slot_taken(const DeltaArgs& a, int r, int 
   return __syncthreads_or(hit) != 0;
 }
 
+// A log gate, no smaller than the reset's; NaN stays (fmaxf would make a reset of it).
+__device__ __forceinline__ float delta_gate(float la) {
+  return la < kGdnMinLogAlpha ? kGdnMinLogAlpha : la;
+}
+
 __device__ __forceinline__ void unpack_bf16x2(uint32_t w, float* f) {
   f[0] = __uint_as_float(w << 16);
   f[1] = __uint_as_float(w & 0xffff0000u);
@@ -123,7 +128,7 @@ __global__ void __launch_bounds__(kStepThreads) k_delta_step(DeltaArgs a) {
   fetch(t0);
   if (delta_slot_taken(a, r, slot)) return;
   for (int64_t t = t0; t < t0 + n; ++t) {
-    const float al = expf(fmaxf(la, kGdnMinLogAlpha));
+    const float al = expf(delta_gate(la));
     const float bt = beta;
     float q[16], k[16], x[RV];
 #pragma unroll
@@ -447,7 +452,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) k_delta_prep(DeltaChunkArgs c
     for (int i = 0; i < 2; ++i) {
       const int t = 2 * lane + i;
       if (t < n) {
-        la[i] = fmaxf(a.log_alpha[(t0 + t) * a.heads + h], kGdnMinLogAlpha);
+        la[i] = delta_gate(a.log_alpha[(t0 + t) * a.heads + h]);
         bt[i] = a.beta[(t0 + t) * a.heads + h];
       }
     }

@@ -428,6 +428,8 @@ QSA_API qsa_status qsa_gated_deltanet(const void *q, const void *k, const void *
  *   log_alpha, beta  fp32 [tokens][heads]
  * heads 1..256, a multiple of key_heads: value head h reads key head h / (heads / key_heads).
  * The arithmetic keeps about fp32 accuracy in the states; out is rounded once to bf16.
+ * A NaN in log_alpha is carried on (qsa_gated_deltanet takes it for a reset).  What is not finite
+ * stays within its sequence and head; in chunks it may reach outputs up to 63 tokens before it.
  * out may be v itself; otherwise neither out nor states overlaps an input or the other
  * (QSA_ERR_INVALID_ARG).
  *

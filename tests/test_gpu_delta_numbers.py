@@ -125,3 +125,29 @@ def test_extend_out_of_skipped_rows_is_zero():
     torch.cuda.synchronize()
     assert torch.count_nonzero(out[70:175]).item() == 0
     assert torch.all(torch.isfinite(out)) and torch.count_nonzero(out[:70]).item() > 0
+
+
+@pytest.mark.parametrize("lens,at", [([100, 70], 40), ([20, 9], 11)])
+def test_extend_a_gate_that_is_no_number_is_carried_on(lens, at):
+    # in chunks and token by token: not taken for a reset; other heads and sequences do not see it
+    w, states = _draw(lens, 3, 3, 2, seed=64)
+    clean = states.clone()
+    want = qsa.gated_deltanet_extend(w.q, w.k, w.v, w.log_alpha, w.beta, w.cu_seqlens, clean)
+    w.log_alpha[at, 1] = float("nan")
+    out = qsa.gated_deltanet_extend(w.q, w.k, w.v, w.log_alpha, w.beta, w.cu_seqlens, states)
+    torch.cuda.synchronize()
+    assert torch.all(torch.isnan(states[0, 1])) and torch.all(torch.isnan(out[at:lens[0], 1]))
+    assert torch.equal(states[1], clean[1]) and torch.equal(out[lens[0]:], want[lens[0]:])
+    for h in (0, 2):
+        assert torch.equal(states[0, h], clean[0, h]) and torch.equal(out[:, h], want[:, h])
+
+
+def test_step_a_gate_that_is_no_number_is_carried_on():
+    w, states = _draw([3, 3], 2, 1, 2, seed=65)
+    x = [y.view(2, 3, *y.shape[1:]) for y in (w.q, w.k, w.v, w.log_alpha, w.beta)]
+    x[3][0, 1, 0] = float("nan")
+    out = qsa.gated_deltanet_step(*x, states)
+    torch.cuda.synchronize()
+    assert torch.all(torch.isnan(states[0, 0])) and torch.all(torch.isnan(out[0, 1:, 0]))
+    assert torch.all(torch.isfinite(out[0, 0])) and torch.all(torch.isfinite(states[0, 1]))
+    assert torch.all(torch.isfinite(out[1])) and torch.all(torch.isfinite(states[1]))
