@@ -237,11 +237,20 @@ __host__ __device__ constexpr int64_t delta_first_record(int64_t begin, int s) {
   return begin / kGdnChunk + s;
 }
 
+// Segments of a sequence of nc chunks.
+__host__ __device__ constexpr int64_t delta_segments(int64_t nc, int64_t seg_first, int64_t seg_chunks) {
+  return nc <= seg_first ? 1 : 1 + (nc - seg_first + seg_chunks - 1) / seg_chunks;
+}
+
 struct DeltaChunkArgs {
   DeltaArgs d;
   int32_t head0, nheads;     // the heads of this pass
-  unsigned char* rec;        // [records][nheads][kRecBytes]
+  // The sequences that go in chunks: {row, first record, first segment slot, 0}, row -1 for none; or
+  // null where all do.
+  int4* list;
+  int32_t listed;            // as the host counts them
   int64_t records;
+  unsigned char* rec;        // [records][nheads][kRecBytes]
   int32_t seg_chunks;        // chunks of a segment (a sequence is walked by one CTA a segment)
   int32_t seg_first;         // and of a sequence's first segment, at most as many
   int64_t seg_slots;
@@ -252,6 +261,80 @@ struct DeltaChunkArgs {
   int32_t fault;             // testing: a copy that block (0, 0, 0) does not issue (kFault..)
 };
 constexpr int32_t kFaultScan = 1, kFaultJoin = 2;
+
+// The i-th sequence that goes in chunks.
+struct DeltaPiece {
+  int row;            // -1: none
+  int64_t begin, len;
+  int64_t record, segment;   // its first record and segment slot
+};
+__device__ __forceinline__ DeltaPiece delta_piece(const DeltaChunkArgs& ca, int i) {
+  DeltaPiece p;
+  p.row = i;
+  p.begin = p.len = p.record = p.segment = 0;
+  if (ca.list != nullptr) {
+    const int4 x = __ldcg(ca.list + i);
+    p.row = x.x;
+    p.record = x.y;
+    p.segment = x.z;
+    if (p.row < 0) return p;
+  }
+  p.begin = delta_row_tokens(ca.d, p.row, &p.len);
+  if (ca.list == nullptr) {
+    p.record = delta_first_record(p.begin, p.row);
+    p.segment = p.record / ca.seg_chunks + p.row;     // as records: segments never overlap
+  }
+  return p;
+}
+
+// ---- k_delta_index: one CTA that lists the sequences in chunks --------------------------------
+// Where a call has sequences that go token by token, or empty ones: without the list each would
+// hold a record a head (96 KB) and a CTA in every launch.  It runs beside the former (`beside`: the
+// launch before is theirs, and has itself waited for all before it).
+constexpr int kIndexThreads = 1024;
+
+__global__ void __launch_bounds__(kIndexThreads) k_delta_index(DeltaChunkArgs ca, bool beside) {
+  __shared__ int3 part[32];
+  const DeltaArgs& a = ca.d;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (!beside) pdl_wait();
+  int3 done = make_int3(0, 0, 0);   // sequences, records and segment slots before this turn's
+  for (int r0 = 0; r0 < a.rows; r0 += kIndexThreads) {
+    const int r = r0 + tid;
+    int64_t len = 0;
+    if (r < a.rows) delta_row_tokens(a, r, &len);
+    int3 own = make_int3(0, 0, 0);
+    if (len > a.short_len) {
+      const int64_t nc = (len + kGdnChunk - 1) / kGdnChunk;
+      own = make_int3(1, static_cast<int>(nc),
+                      static_cast<int>(delta_segments(nc, ca.seg_first, ca.seg_chunks) - 1));
+    }
+    int3 x = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int3 y = make_int3(__shfl_up_sync(0xffffffffu, x.x, o), __shfl_up_sync(0xffffffffu, x.y, o),
+                               __shfl_up_sync(0xffffffffu, x.z, o));
+      if (lane >= o) x = make_int3(x.x + y.x, x.y + y.y, x.z + y.z);
+    }
+    if (lane == 31) part[warp] = x;
+    __syncthreads();
+    int3 at = make_int3(done.x + x.x - own.x, done.y + x.y - own.y, done.z + x.z - own.z);
+    for (int w = 0; w < 32; ++w) {
+      const int3 y = part[w];
+      done = make_int3(done.x + y.x, done.y + y.y, done.z + y.z);
+      if (w < warp) at = make_int3(at.x + y.x, at.y + y.y, at.z + y.z);
+    }
+    if (own.x) {   // (lengths that disagree with the host's: what has no space is left out)
+      const bool fits = at.x < ca.listed && at.y + own.y <= ca.records && at.z + own.z <= ca.seg_slots;
+      if (!fits) report_error(ca.st, kErrDevice, 321);
+      if (at.x < ca.listed) ca.list[at.x] = make_int4(fits ? r : -1, fits ? at.y : 0x7fffffff, at.z, 0);
+    }
+    __syncthreads();
+  }
+  for (int i = done.x + tid; i < ca.listed; i += kIndexThreads)
+    ca.list[i] = make_int4(-1, 0x7fffffff, 0, 0);
+  if (beside) pdl_wait();   // the launches after this one count on all before it
+}
 
 // Instruction descriptor: kind::f16 with f16 A/B, fp32 D, dense.
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int a_mn_major, int b_mn_major) {
@@ -431,15 +514,15 @@ __global__ void __launch_bounds__(kPrepThreads, 4) k_delta_prep(DeltaChunkArgs c
   pdl_trigger();   // the scan sets up while the last of these run
   // the last sequence whose first record is not past r, 256 candidates at a time
   int seq = 0;
-  for (int step = a.rows > kPrepThreads ? kPrepThreads : 1; step > 0; step = step > 1 ? 1 : 0) {
+  for (int step = ca.listed > kPrepThreads ? kPrepThreads : 1; step > 0; step = step > 1 ? 1 : 0) {
     const int64_t s = seq + static_cast<int64_t>(tid) * step;
-    const bool in = s < a.rows && delta_first_record(a.cu[s], static_cast<int>(s)) <= r;
+    const bool in = s < ca.listed &&
+                    (ca.list != nullptr ? __ldcg(&ca.list[s].y) : delta_first_record(a.cu[s], static_cast<int>(s))) <= r;
     const int m = __syncthreads_count(in);
     seq += (m > 0 ? m - 1 : 0) * step;
   }
-  int64_t len;
-  const int64_t begin = delta_row_tokens(a, seq, &len);
-  const int64_t c = r - delta_first_record(begin, seq);
+  const DeltaPiece piece = delta_piece(ca, seq);
+  const int64_t begin = piece.begin, len = piece.len, c = r - piece.record;
   if (c < 0 || c * kGdnChunk >= len || len <= a.short_len) return;
   const int64_t t0 = begin + c * kGdnChunk;
   const int n = static_cast<int>(len - c * kGdnChunk < kGdnChunk ? len - c * kGdnChunk : kGdnChunk);
@@ -888,20 +971,20 @@ __global__ void __launch_bounds__(kScanThreads, 1)
   ScanBars& B = *reinterpret_cast<ScanBars*>(smem + kScanBars);
   const DeltaArgs& a = ca.d;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int hl = blockIdx.x, h = ca.head0 + hl, row = blockIdx.y;
+  const int hl = blockIdx.x, h = ca.head0 + hl;
   pdl_trigger();
   // the first pass has two CTAs a segment: states, and transitions
   const bool trans = mode == kScanEnds && (blockIdx.z & 1);
   const int seg = mode == kScanEnds ? blockIdx.z >> 1 : blockIdx.z + (mode == kScanOutputs);
-  int64_t len;
-  const int64_t begin = delta_row_tokens(a, row, &len);
-  const int64_t chunks = (len + kGdnChunk - 1) / kGdnChunk;
+  const DeltaPiece piece = delta_piece(ca, blockIdx.y);
+  const int row = piece.row;
+  const int64_t begin = piece.begin, len = piece.len, chunks = (len + kGdnChunk - 1) / kGdnChunk;
   const int64_t c0 = seg == 0 ? 0 : ca.seg_first + static_cast<int64_t>(seg - 1) * ca.seg_chunks;
   const int64_t len_c = seg == 0 ? ca.seg_first : ca.seg_chunks;
   const int64_t c1 = c0 + len_c < chunks ? c0 + len_c : chunks;
   const int nc = static_cast<int>(c1 - c0);
   const bool last = c1 == chunks;
-  const int slot = a.slots != nullptr ? a.slots[row] : row;
+  const int slot = a.slots != nullptr && row >= 0 ? a.slots[row] : row;
   bool idle = nc <= 0 || len <= a.short_len || slot < 0 || slot >= a.num_slots ||
               (mode == kScanEnds && (seg == 0 ? trans : last));
   if (!idle) idle = delta_slot_taken(a, row, slot);
@@ -914,8 +997,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     return;
   }
   const bool outputs = mode != kScanEnds || seg == 0;
-  const int64_t rec0 = delta_first_record(begin, row);
-  const int64_t seg0 = rec0 / ca.seg_chunks + row;     // as records: segments never overlap
+  const int64_t rec0 = piece.record, seg0 = piece.segment;
   const int64_t tile = static_cast<int64_t>(kGdnDim) * kGdnDim;
   float* state = a.states + (static_cast<int64_t>(slot) * a.heads + h) * tile;
   const int64_t seg_stride = static_cast<int64_t>(ca.nheads) * tile;
@@ -1313,7 +1395,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     const int who = warp - 25;
     uint64_t* full = who == 0 ? B.full_w : who == 1 ? B.full_u : B.full_q;
     uint64_t* empty = who == 0 ? B.empty_w : who == 1 ? B.empty_u : B.empty_q;
-    const bool on = who == 0 || (who == 1 ? !trans && !(ca.fault == kFaultScan && hl + row + blockIdx.z == 0)
+    const bool on = who == 0 || (who == 1 ? !trans && !(ca.fault == kFaultScan && hl + blockIdx.y + blockIdx.z == 0)
                                           : outputs);
     const int kh = h / (a.heads / a.key_heads);
     int issued = 0, issued_m = 0;
@@ -1412,14 +1494,11 @@ __global__ void __launch_bounds__(kJoinThreads) k_delta_join(DeltaChunkArgs ca) 
   __shared__ int abort_flag;
   float* e = join_sh + kStages * kTile;               // [rows][128]
   float* part = e + kRows * kGdnDim;                  // [4][rows][128]
-  const DeltaArgs& a = ca.d;
-  const int row = blockIdx.y, hl = blockIdx.x, d = threadIdx.x, v0 = blockIdx.z * kRows;
+  const int hl = blockIdx.x, d = threadIdx.x, v0 = blockIdx.z * kRows;
   const int warp = d >> 5, lane = d & 31;
   pdl_trigger();
-  int64_t len;
-  const int64_t begin = delta_row_tokens(a, row, &len);
-  const int64_t chunks = (len + kGdnChunk - 1) / kGdnChunk;
-  const int64_t segs = 1 + (chunks - ca.seg_first + ca.seg_chunks - 1) / ca.seg_chunks;
+  const DeltaPiece piece = delta_piece(ca, blockIdx.y);
+  const int64_t segs = delta_segments((piece.len + kGdnChunk - 1) / kGdnChunk, ca.seg_first, ca.seg_chunks);
   if (d == 0) {
     for (int i = 0; i < kStages; ++i) mbar_init(&full[i], 1);
     abort_flag = 0;
@@ -1430,10 +1509,10 @@ __global__ void __launch_bounds__(kJoinThreads) k_delta_join(DeltaChunkArgs ca) 
   if (segs < 3) return;
   volatile int* abort = &abort_flag;
   const int64_t stride = static_cast<int64_t>(ca.nheads) * kTile;
-  const int64_t at = ((delta_first_record(begin, row) / ca.seg_chunks + row) * ca.nheads + hl) * kTile;
+  const int64_t at = (piece.segment * ca.nheads + hl) * kTile;
   float* s = ca.seg_state + at + v0 * kGdnDim + d;
   const float* p = ca.seg_trans + at;
-  const int64_t absent = ca.fault == kFaultJoin && hl + row + blockIdx.z == 0 ? 1 : 0;
+  const int64_t absent = ca.fault == kFaultJoin && hl + blockIdx.y + blockIdx.z == 0 ? 1 : 0;
   auto fetch = [&](int64_t g) {   // segment g's transition
     if (d == 0 && g + 1 < segs && g != absent) {
       uint64_t* bar = &full[(g - 1) % kStages];

@@ -7,6 +7,9 @@
 
 #include <atomic>
 #include <cmath>
+#include <new>
+#include <utility>
+#include <vector>
 
 #include "qsa_delta.cuh"
 #include "qsa_evict.cuh"
@@ -133,13 +136,15 @@ qsa_status extend_check_cu(const int32_t* h_cu, int32_t num_seqs) {
   return QSA_OK;
 }
 
-// How a call of extend runs: heads in passes that keep the records within a budget, and long
-// sequences cut into segments of seg_chunks chunks where that fills the SMs better.
+// How a call of extend runs: heads in passes that keep records and segments within a budget, and
+// long sequences cut into segments of seg_chunks chunks where that fills the SMs better.
 struct ExtendPlan {
   int64_t records = 0, max_chunks = 0, seg_slots = 0;
   int32_t pass_heads = 1, seg_chunks = 1, seg_first = 1, segs = 1;
   int32_t short_len = 0;   // pieces of at most this many tokens go token by token
-  size_t o_rec = 0, o_state = 0, o_trans = 0, total = 0;
+  int32_t listed = 0;      // the others: sequences that go in chunks
+  bool index = false;      // not all do: they are listed on the device
+  size_t o_list = 0, o_rec = 0, o_state = 0, o_trans = 0, total = 0;
 };
 
 // Where a call has no longer pieces than 32 tokens, all go token by token (a piece of 30 tokens x 4
@@ -148,7 +153,7 @@ struct ExtendPlan {
 // 1 to 64 tokens x 16 heads: 95 us against 132); fewer ride along (7 pieces, one of 1 token, x 4
 // heads: 65.6 us against 69.7 with a launch more).
 constexpr int32_t kShortAll = 32, kShortMany = 16;
-constexpr int64_t kRecordBudget = int64_t(1) << 32;
+constexpr int64_t kExtendBudget = int64_t(1) << 32;   // bytes of scratch, above which heads run in passes
 
 // Rows of a state that a CTA of the join takes: as few as leave the grid in one wave.
 int join_rows(int64_t heads_seqs) {
@@ -157,30 +162,10 @@ int join_rows(int64_t heads_seqs) {
   return rows;
 }
 
-void extend_plan(const int32_t* h_cu, int32_t num_seqs, int32_t heads, ExtendPlan* p) {
-  const int64_t tokens = h_cu[num_seqs];
-  p->records = tokens / kGdnChunk + num_seqs;
-  const int64_t per_head = p->records * kRecBytes;
-  int64_t hp = std::max<int64_t>(1, std::min<int64_t>(heads, kRecordBudget / per_head));
-  const int64_t passes = (heads + hp - 1) / hp;
-  hp = (heads + passes - 1) / passes;
-  p->pass_heads = static_cast<int32_t>(hp);
-  int64_t short_rows = 0, longest = 0;
-  for (int32_t i = 0; i < num_seqs; ++i) {
-    const int64_t len = int64_t(h_cu[i + 1]) - h_cu[i];
-    longest = std::max(longest, len);
-    short_rows += len > 0 && len <= kShortMany;
-  }
-  p->short_len = longest <= kShortAll ? kShortAll
-                 : short_rows * heads >= num_sms() ? kShortMany : 0;
-  int64_t total = 0;
-  for (int32_t i = 0; i < num_seqs; ++i) {
-    const int64_t len = int64_t(h_cu[i + 1]) - h_cu[i];
-    if (len <= p->short_len) continue;
-    const int64_t nc = (len + kGdnChunk - 1) / kGdnChunk;
-    p->max_chunks = std::max(p->max_chunks, nc);
-    total += nc;
-  }
+// Into how long segments sequences are cut, hp heads at a time.  chunks: the lengths of those that
+// a cut may split, and how many there are of each; flat: chunks of the others together.
+void extend_cuts(const std::vector<std::pair<int64_t, int64_t>>& chunks, int64_t flat, int64_t cuts,
+                 int64_t total, int64_t hp, ExtendPlan* p) {
   // Microseconds of the scan, uncut and cut into about k segments: the longest walk, or all walks
   // in waves over the SMs, at what a chunk was measured to take (2.65 with outputs, 2.4 without),
   // and what a launch and a step of the join were.  Cut, first segments run whole beside the inner
@@ -194,20 +179,15 @@ void extend_plan(const int32_t* h_cu, int32_t num_seqs, int32_t heads, ExtendPla
   };
   double best = 10 + 2.65 * std::max(double(p->max_chunks), double(total) * hp / sms);
   int64_t L = std::max<int64_t>(1, p->max_chunks), F = L;
-  // where all walks together bound the uncut call, a cut only adds to them
-  const int64_t cuts = double(total) * hp >= double(p->max_chunks) * sms ? 0 : 512;
+  const int rows = join_rows(int64_t(p->listed) * hp);
+  const double waves = std::ceil(double(p->listed) * hp * (kGdnDim / rows) / sms);
   auto consider = [&](int64_t l, int64_t f, int64_t k) {
-    double first = 0, rest = 0;   // chunks walked by the two passes
-    for (int32_t i = 0; i < num_seqs; ++i) {
-      const int64_t len = int64_t(h_cu[i + 1]) - h_cu[i];
-      if (len <= p->short_len) continue;
-      const int64_t nc = (len + kGdnChunk - 1) / kGdnChunk;
-      const int64_t segs = nc <= f ? 1 : 1 + (nc - f + l - 1) / l;
-      first += segs > 1 ? double((2 * segs - 3) * l) : double(nc);
-      rest += double((segs - 1) * l);
+    double first = double(flat), rest = 0;   // chunks walked by the two passes
+    for (const auto& c : chunks) {
+      const int64_t segs = delta_segments(c.first, f, l);
+      first += double(c.second) * (segs > 1 ? double((2 * segs - 3) * l) : double(c.first));
+      rest += double(c.second) * double((segs - 1) * l);
     }
-    const int rows = join_rows(int64_t(num_seqs) * hp);
-    const double waves = std::ceil(double(num_seqs) * hp * (kGdnDim / rows) / sms);
     const double t = waves_of(double(l), first * hp, 2.4) + (f == l ? 0.25 * double(l) : 0) +
                      waves * (6 + double(k) * 0.9) + 8 + waves_of(double(l), rest * hp, 2.65);
     if (t < best) {
@@ -216,24 +196,83 @@ void extend_plan(const int32_t* h_cu, int32_t num_seqs, int32_t heads, ExtendPla
       F = f;
     }
   };
-  for (int64_t k = 3; k <= cuts && k <= p->max_chunks / 2; k += 1 + k / 16) {
-    const int64_t even = (p->max_chunks + k - 1) / k;
-    const int64_t l = (8 * p->max_chunks + 8 * k - 2) / (8 * k - 1);
-    consider(l, l - l / 8, k);
-    consider(even, even, k);
-  }
+  // where all walks together bound the uncut call, a cut only adds to them
+  if (double(total) * hp < double(p->max_chunks) * sms)
+    for (int64_t k = 3; k <= cuts; k += 1 + k / 16) {
+      const int64_t even = (p->max_chunks + k - 1) / k;
+      const int64_t l = (8 * p->max_chunks + 8 * k - 2) / (8 * k - 1);
+      consider(l, l - l / 8, k);
+      consider(even, even, k);
+    }
   p->seg_chunks = static_cast<int32_t>(L);
   p->seg_first = static_cast<int32_t>(F);
-  p->segs = static_cast<int32_t>(p->max_chunks <= F ? 1 : 1 + (p->max_chunks - F + L - 1) / L);
+  p->segs = static_cast<int32_t>(delta_segments(p->max_chunks, F, L));
+}
+
+// False where the host has no memory for it.
+bool extend_plan(const int32_t* h_cu, int32_t num_seqs, int32_t heads, ExtendPlan* p) try {
+  int64_t short_rows = 0, longest = 0;
+  for (int32_t i = 0; i < num_seqs; ++i) {
+    const int64_t len = int64_t(h_cu[i + 1]) - h_cu[i];
+    longest = std::max(longest, len);
+    short_rows += len > 0 && len <= kShortMany;
+  }
+  p->short_len = longest <= kShortAll ? kShortAll
+                 : short_rows * heads >= num_sms() ? kShortMany : 0;
+  p->max_chunks = longest > p->short_len ? (longest + kGdnChunk - 1) / kGdnChunk : 0;
   Carver cv;
-  p->o_rec = cv.take(static_cast<size_t>(per_head * hp));
+  p->total = cv.off;
+  if (p->max_chunks == 0) return true;
+  // the most cuts that are considered, and the longest sequence that no cut splits
+  const int64_t cuts = std::min<int64_t>(512, p->max_chunks / 2);
+  const int64_t shortest = cuts < 3 ? p->max_chunks : (p->max_chunks + cuts - 1) / cuts * 7 / 8;
+  std::vector<std::pair<int64_t, int64_t>> chunks;
+  int64_t total = 0, flat = 0;
+  for (int32_t i = 0; i < num_seqs; ++i) {
+    const int64_t len = int64_t(h_cu[i + 1]) - h_cu[i];
+    if (len <= p->short_len) continue;
+    const int64_t nc = (len + kGdnChunk - 1) / kGdnChunk;
+    ++p->listed;
+    total += nc;
+    if (nc > shortest) chunks.emplace_back(nc, 1);
+    else flat += nc;
+  }
+  std::sort(chunks.begin(), chunks.end());
+  size_t n = 0;   // one entry a length
+  for (size_t i = 1; i < chunks.size(); ++i) {
+    if (chunks[i].first == chunks[n].first) ++chunks[n].second;
+    else chunks[++n] = chunks[i];
+  }
+  if (!chunks.empty()) chunks.resize(n + 1);
+  p->index = p->listed < num_seqs;
+  p->records = p->index ? total : h_cu[num_seqs] / kGdnChunk + num_seqs;
+  const int64_t tile = int64_t(kGdnDim) * kGdnDim * 4;
+  // heads in passes of equal size, the first that fits
+  for (int64_t passes = 1;; ) {
+    const int64_t hp = (heads + passes - 1) / passes;
+    p->pass_heads = static_cast<int32_t>(hp);
+    extend_cuts(chunks, flat, cuts, total, hp, p);
+    p->seg_slots = 0;
+    if (p->segs > 1 && !p->index) p->seg_slots = p->records / p->seg_chunks + num_seqs;
+    if (p->segs > 1 && p->index)   // (a sequence that no cut splits is one segment)
+      for (const auto& c : chunks)
+        p->seg_slots += c.second * (delta_segments(c.first, p->seg_first, p->seg_chunks) - 1);
+    const int64_t per_head = p->records * kRecBytes + 2 * p->seg_slots * tile;
+    if (hp == 1 || per_head * hp <= kExtendBudget) break;
+    const int64_t fit = std::max<int64_t>(1, std::min(hp - 1, kExtendBudget / per_head));
+    passes = std::max(passes + 1, (heads + fit - 1) / fit);
+  }
+  if (p->index) p->o_list = cv.take(static_cast<size_t>(p->listed) * sizeof(int4));
+  p->o_rec = cv.take(static_cast<size_t>(p->records * kRecBytes * p->pass_heads));
   if (p->segs > 1) {
-    p->seg_slots = p->records / L + num_seqs;
-    const size_t bytes = static_cast<size_t>(p->seg_slots) * hp * kGdnDim * kGdnDim * 4;
+    const size_t bytes = static_cast<size_t>(p->seg_slots * p->pass_heads * tile);
     p->o_state = cv.take(bytes);
     p->o_trans = cv.take(bytes);
   }
   p->total = cv.off;
+  return true;
+} catch (const std::bad_alloc&) {
+  return false;
 }
 }  // namespace
 
@@ -244,8 +283,7 @@ extern "C" size_t qsa_gated_deltanet_extend_workspace_size(const int32_t* h_cu_s
       key_heads < 1 || heads % key_heads != 0)
     return 0;
   ExtendPlan p;
-  extend_plan(h_cu_seqlens, num_seqs, heads, &p);
-  return p.total;
+  return extend_plan(h_cu_seqlens, num_seqs, heads, &p) ? p.total : 0;
 }
 
 extern "C" qsa_status qsa_gated_deltanet_extend(
@@ -263,7 +301,7 @@ extern "C" qsa_status qsa_gated_deltanet_extend(
   if (!aligned16(workspace) || reinterpret_cast<uintptr_t>(d_cu_seqlens) % 4 != 0)
     return QSA_ERR_ALIGNMENT;
   ExtendPlan p;
-  extend_plan(h_cu_seqlens, num_seqs, heads, &p);
+  if (!extend_plan(h_cu_seqlens, num_seqs, heads, &p)) return QSA_ERR_CUDA;
   if (ws_bytes < p.total) return QSA_ERR_WORKSPACE;
   a.d.cu = d_cu_seqlens;
   a.d.tokens = h_cu_seqlens[num_seqs];
@@ -278,6 +316,8 @@ extern "C" qsa_status qsa_gated_deltanet_extend(
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   a.rec = ws + p.o_rec;
   a.records = p.records;
+  a.listed = p.listed;
+  if (p.index) a.list = reinterpret_cast<int4*>(ws + p.o_list);
   a.seg_chunks = p.seg_chunks;
   a.seg_first = p.seg_first;
   a.seg_slots = p.seg_slots;
@@ -297,11 +337,11 @@ extern "C" qsa_status qsa_gated_deltanet_extend(
     if (!make_tmap(&maps.k, k, 3, kd, ks, box)) return QSA_ERR_CUDA;
   }
   const int prep_smem = static_cast<int>(sizeof(PrepSmem));
-  if (!set_smem(k_delta_prep, prep_smem) || !set_smem(k_delta_scan, kScanSmemBytes) ||
-      !set_smem(k_delta_join<4>, join_smem_bytes(4)) || !set_smem(k_delta_join<8>, join_smem_bytes(8)) ||
-      !set_smem(k_delta_join<16>, join_smem_bytes(16)))
-    return QSA_ERR_CUDA;
+  if (!set_smem(k_delta_prep, prep_smem) || !set_smem(k_delta_scan, kScanSmemBytes)) return QSA_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const unsigned listed = static_cast<unsigned>(p.listed);
+  if (p.index)
+    QSA_CHECK_PDL(launch_pdl(k_delta_index, dim3(1), dim3(kIndexThreads), 0, s, a, p.short_len > 0));
   for (int32_t h0 = 0; h0 < heads; h0 += p.pass_heads) {
     a.head0 = h0;
     a.nheads = std::min(p.pass_heads, heads - h0);
@@ -309,16 +349,17 @@ extern "C" qsa_status qsa_gated_deltanet_extend(
     QSA_CHECK_PDL(launch_pdl(k_delta_prep, dim3(static_cast<unsigned>(p.records), a.nheads),
                              dim3(kPrepThreads), prep_smem, s, a));
     if (p.segs > 1) {
-      QSA_CHECK_PDL(launch_pdl(k_delta_scan, dim3(a.nheads, num_seqs, 2 * (p.segs - 1)),
+      QSA_CHECK_PDL(launch_pdl(k_delta_scan, dim3(a.nheads, listed, 2 * (p.segs - 1)),
                                dim3(kScanThreads), kScanSmemBytes, s, maps, a, kScanEnds));
       if (p.segs > 2) {
-        const int rows = join_rows(int64_t(a.nheads) * num_seqs);
-        QSA_CHECK_PDL(launch_pdl(rows == 4 ? k_delta_join<4> : rows == 8 ? k_delta_join<8> : k_delta_join<16>,
-                                 dim3(a.nheads, num_seqs, kGdnDim / rows), dim3(kJoinThreads),
+        const int rows = join_rows(int64_t(a.nheads) * p.listed);
+        const auto join = rows == 4 ? k_delta_join<4> : rows == 8 ? k_delta_join<8> : k_delta_join<16>;
+        if (!set_smem(join, join_smem_bytes(rows))) return QSA_ERR_CUDA;
+        QSA_CHECK_PDL(launch_pdl(join, dim3(a.nheads, listed, kGdnDim / rows), dim3(kJoinThreads),
                                  join_smem_bytes(rows), s, a));
       }
     }
-    QSA_CHECK_PDL(launch_pdl(k_delta_scan, dim3(a.nheads, num_seqs, std::max(1, p.segs - 1)),
+    QSA_CHECK_PDL(launch_pdl(k_delta_scan, dim3(a.nheads, listed, std::max(1, p.segs - 1)),
                              dim3(kScanThreads), kScanSmemBytes, s, maps, a,
                              p.segs > 1 ? kScanOutputs : kScanWhole));
   }

@@ -1,0 +1,85 @@
+"""GPU tests of extend calls that mix sequences in chunks with short ones (token by token) and empty
+ones, which are listed on the device (tolerances of tests/test_gpu_delta.py)."""
+import pytest
+import torch
+
+import block_sparse_attention_40_b200 as qsa
+from tests.gpu_helpers import needs_gpu
+from tests.test_gpu_delta import DEV, STATE_TOL, _check_extend, _draw
+
+pytestmark = [pytest.mark.gpu, needs_gpu]
+
+
+@pytest.mark.parametrize("lens,heads,key_heads", [
+    ([0, 100, 0], 2, 1), ([0, 0, 70, 64, 0, 129, 0], 2, 2),
+    ([1] * 80 + [300, 17, 16] + [0] * 5 + [65, 3] * 6, 2, 2),
+    ([5000, 1, 0, 2100] + [2] * 160 + [700], 1, 1),              # cut into segments, of some one only
+    ([0, 3000, 0, 40, 1400], 4, 2),
+    ([3] * 1100 + [90], 1, 1)])                                  # more rows than one turn of the list
+def test_extend_mixed(lens, heads, key_heads):
+    _check_extend(lens, heads, key_heads, seed=90, gate=(0.95, 1.0))
+
+
+def test_extend_mixed_slots():
+    # a short row names the slot of a later long one and has it; a long one lies outside the pool
+    lens = [9, 200, 70, 0, 300, 64] + [2] * 100
+    slots = [2, 2, 900, 1, 0, 1] + [10 + i for i in range(100)]
+    _check_extend(lens, 2, 1, seed=91, slots=slots, num_slots=120)
+
+
+def test_extend_mixed_equals_its_parts():
+    # 4,000 and 900 tokens beside 60 short pieces, against calls of their own
+    lens, heads = [7] * 30 + [4000] + [1] * 30 + [0, 900], 4
+    w, states = _draw(lens, heads, 2, len(lens), seed=92)
+    args = (w.q, w.k, w.v, w.log_alpha, w.beta)
+    got = states.clone()
+    out = qsa.gated_deltanet_extend(*args, w.cu_seqlens, got)
+    cu = [int(x) for x in w.cu_seqlens]
+    norm = max(got.norm(dim=-1).max().item(), states.norm(dim=-1).max().item())
+    for s in (0, 30, 31, 62):
+        one = states[s:s + 1].clone()
+        a = qsa.gated_deltanet_extend(*[x[cu[s]:cu[s + 1]] for x in args], [0, lens[s]], one)
+        assert (one[0] - got[s]).abs().max().item() <= 2 * STATE_TOL * norm
+        tol = 2.0 ** -7 * a.float().abs() + 4 * STATE_TOL * norm
+        assert torch.all((a.float() - out[cu[s]:cu[s + 1]].float()).abs() <= tol)
+    assert torch.equal(got[61], states[61])      # the empty one
+
+
+def test_extend_mixed_in_a_graph():
+    # the list is made anew in every replay, beside the short rows' launch
+    for lens in ([3000] + [4] * 80, [500, 0, 0, 2000]):
+        w, states = _draw(lens, 2, 2, len(lens), seed=93)
+        args = (w.q, w.k, w.v, w.log_alpha, w.beta)
+        ctx = qsa.DeltaExtend(w.cu_seqlens, 2, DEV)
+        want = states.clone()
+        ref = [ctx.run(*args, want).clone() for _ in range(3)][-1]
+        torch.cuda.synchronize()
+        out = torch.empty_like(w.v)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            ctx.run(*args, states, out=out)
+        for _ in range(3):
+            g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(states, want) and torch.equal(out, ref)
+        assert ctx.device_error() == ("QSA_OK", 0)
+
+
+def test_extend_mixed_in_passes():
+    # records of more than the budget, short pieces and an index: heads in two passes
+    lens, heads = [60000, 1, 70000, 60001] + [2] * 20, 16
+    w, states = _draw(lens, heads, heads, len(lens), seed=94, gate=(0.95, 1.0))
+    ctx = qsa.DeltaExtend(w.cu_seqlens, heads, DEV)
+    got = states.clone()
+    out = ctx.run(w.q, w.k, w.v, w.log_alpha, w.beta, got)
+    torch.cuda.synchronize()
+    assert ctx.device_error() == ("QSA_OK", 0) and ctx.ws.numel() <= (1 << 32) + 4096
+    norm = got.norm(dim=-1).max().item()
+    for h in (0, 8, 15):
+        one = states[:, h:h + 1].contiguous()
+        x = [y[:, h:h + 1].contiguous() for y in (w.q, w.k, w.v, w.log_alpha, w.beta)]
+        alone = qsa.gated_deltanet_extend(*x, w.cu_seqlens, one)
+        assert (one - got[:, h:h + 1]).abs().max().item() <= 2 * STATE_TOL * norm
+        a = alone[:, 0].float()
+        tol = 2.0 ** -7 * a.abs() + 4 * STATE_TOL * norm
+        assert torch.all((a - out[:, h].float()).abs() <= tol)
