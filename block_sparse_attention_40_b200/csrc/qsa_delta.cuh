@@ -77,8 +77,8 @@ __device__ __forceinline__ void unpack_bf16x2(uint32_t w, float* f) {
 
 // ---------------------------------------------------------------------------------------
 // Token by token.  Eight lanes hold one value row of S (16 key columns each, in four groups of
-// four so that a row's loads are 128-byte segments), RV rows a thread, so a block of 128
-// threads holds 16 * RV rows and the grid (heads, rows, 128 / (16 RV)) covers S.  The state
+// four so that a row's loads are 128-byte segments), two rows a thread, so a block of 128 threads
+// holds 32 rows and the grid (heads, rows, 4) covers S.  The state
 // stays in registers over a row's tokens: it is read once and written once.  With
 // o = a S q + u (k.q), u = beta (v - a S k), both dots of a token come from the old state in one
 // pass, and the reductions are three shuffles.  A token's inputs are fetched while the one before
@@ -86,12 +86,12 @@ __device__ __forceinline__ void unpack_bf16x2(uint32_t w, float* f) {
 // everything else at one token.  64 rows x 32 heads x 1 token: 45 us, 6.0 TB/s, 92% of the measured
 // copy rate; 24 rows of up to 5 tokens x 16 heads: 9.8 us a call (its states' bytes take 6.9).
 constexpr int kStepThreads = 128;
+constexpr int kStepRows = 2;
 
-template <int RV>
 __global__ void __launch_bounds__(kStepThreads) k_delta_step(DeltaArgs a) {
   const int tid = threadIdx.x, l8 = tid & 7, grp = tid >> 3;   // 16 groups of 8 lanes
   const int h = blockIdx.x, r = blockIdx.y;
-  const int v0 = (blockIdx.z * 16 + grp) * RV;
+  const int v0 = (blockIdx.z * 16 + grp) * kStepRows;
   pdl_wait();      // launched as a programmatic dependent of the caller's last kernel, which is done
   pdl_trigger();   // before any kernel behind this one starts
   int64_t n;
@@ -101,16 +101,16 @@ __global__ void __launch_bounds__(kStepThreads) k_delta_step(DeltaArgs a) {
   const int kh = h / (a.heads / a.key_heads);
   float* st = a.states +
               ((static_cast<int64_t>(slot) * a.heads + h) * kGdnDim + v0) * kGdnDim + 4 * l8;
-  float4 S[RV][4];
+  float4 S[kStepRows][4];
 #pragma unroll
-  for (int i = 0; i < RV; ++i)
+  for (int i = 0; i < kStepRows; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       S[i][j] = __ldcs(reinterpret_cast<const float4*>(st + i * kGdnDim + 32 * j));
   // a token's inputs, on their way while the one before it is taken
   uint2 wq[4], wk[4];
   float la, beta;
-  __nv_bfloat16 wv[RV];
+  __nv_bfloat16 wv[kStepRows];
   auto fetch = [&](int64_t t) {
     const uint2* qp = reinterpret_cast<const uint2*>(a.q + (t * a.key_heads + kh) * kGdnDim) + l8;
     const uint2* kp = reinterpret_cast<const uint2*>(a.k + (t * a.key_heads + kh) * kGdnDim) + l8;
@@ -123,14 +123,14 @@ __global__ void __launch_bounds__(kStepThreads) k_delta_step(DeltaArgs a) {
     beta = a.beta[t * a.heads + h];
     const __nv_bfloat16* vp = a.v + (t * a.heads + h) * kGdnDim + v0;
 #pragma unroll
-    for (int i = 0; i < RV; ++i) wv[i] = vp[i];
+    for (int i = 0; i < kStepRows; ++i) wv[i] = vp[i];
   };
   fetch(t0);
   if (delta_slot_taken(a, r, slot)) return;
   for (int64_t t = t0; t < t0 + n; ++t) {
     const float al = expf(delta_gate(la));
     const float bt = beta;
-    float q[16], k[16], x[RV];
+    float q[16], k[16], x[kStepRows];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       unpack_bf16x2(wq[j].x, q + 4 * j);
@@ -139,13 +139,13 @@ __global__ void __launch_bounds__(kStepThreads) k_delta_step(DeltaArgs a) {
       unpack_bf16x2(wk[j].y, k + 4 * j + 2);
     }
 #pragma unroll
-    for (int i = 0; i < RV; ++i) x[i] = __bfloat162float(wv[i]);
+    for (int i = 0; i < kStepRows; ++i) x[i] = __bfloat162float(wv[i]);
     if (t + 1 < t0 + n) fetch(t + 1);
-    float kq = 0.f, sk[RV], sq[RV];
+    float kq = 0.f, sk[kStepRows], sq[kStepRows];
 #pragma unroll
     for (int e = 0; e < 16; ++e) kq = fmaf(k[e], q[e], kq);
 #pragma unroll
-    for (int i = 0; i < RV; ++i) {
+    for (int i = 0; i < kStepRows; ++i) {
       const float* s = reinterpret_cast<const float*>(S[i]);
       sk[i] = sq[i] = 0.f;
 #pragma unroll
@@ -158,13 +158,13 @@ __global__ void __launch_bounds__(kStepThreads) k_delta_step(DeltaArgs a) {
     for (int o = 1; o < 8; o <<= 1) {
       kq += __shfl_xor_sync(0xffffffffu, kq, o);
 #pragma unroll
-      for (int i = 0; i < RV; ++i) {
+      for (int i = 0; i < kStepRows; ++i) {
         sk[i] += __shfl_xor_sync(0xffffffffu, sk[i], o);
         sq[i] += __shfl_xor_sync(0xffffffffu, sq[i], o);
       }
     }
 #pragma unroll
-    for (int i = 0; i < RV; ++i) {
+    for (int i = 0; i < kStepRows; ++i) {
       const float u = bt * (x[i] - al * sk[i]);
       float* s = reinterpret_cast<float*>(S[i]);
 #pragma unroll
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kStepThreads) k_delta_step(DeltaArgs a) {
     }
   }
 #pragma unroll
-  for (int i = 0; i < RV; ++i)
+  for (int i = 0; i < kStepRows; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       __stcs(reinterpret_cast<float4*>(st + i * kGdnDim + 32 * j), S[i][j]);

@@ -125,7 +125,7 @@ bool delta_overlaps(const DeltaArgs& a) {
 }
 
 qsa_status launch_delta_step(const DeltaArgs& a, cudaStream_t s) {
-  QSA_CHECK_PDL(launch_pdl(k_delta_step<2>, dim3(a.heads, a.rows, 4), dim3(kStepThreads), 0, s, a));
+  QSA_CHECK_PDL(launch_pdl(k_delta_step, dim3(a.heads, a.rows, kGdnDim / (16 * kStepRows)), dim3(kStepThreads), 0, s, a));
   return QSA_OK;
 }
 
