@@ -151,3 +151,59 @@ def test_step_a_gate_that_is_no_number_is_carried_on():
     assert torch.all(torch.isnan(states[0, 0])) and torch.all(torch.isnan(out[0, 1:, 0]))
     assert torch.all(torch.isfinite(out[0, 0])) and torch.all(torch.isfinite(states[0, 1]))
     assert torch.all(torch.isfinite(out[1])) and torch.all(torch.isfinite(states[1]))
+
+
+# ---- keys and queries of any length --------------------------------------------------------------
+@pytest.mark.parametrize("lens", [[200], [5000]])
+@pytest.mark.parametrize("m", [-20, -3, 3, 20])
+def test_keys_and_queries_of_any_length(lens, m):
+    # k 2^m, beta 2^-2m and S 2^-m, q 2^m leave the outputs as they were: powers of two, so that the
+    # unscaled run is the reference up to the roundings of the two runs
+    w, states = _draw(lens, 2, 1, 1, seed=66, gate=(0.95, 1.0))
+    s = 2.0 ** m
+    one, two = states.clone(), states / s
+    a = qsa.gated_deltanet_extend(w.q, w.k, w.v, w.log_alpha, w.beta, w.cu_seqlens, one)
+    b = qsa.gated_deltanet_extend((w.q.float() * s).to(torch.bfloat16),
+                                  (w.k.float() * s).to(torch.bfloat16), w.v, w.log_alpha,
+                                  w.beta / s ** 2, w.cu_seqlens, two)
+    torch.cuda.synchronize()
+    norm = max(one.norm(dim=-1).max().item(), states.norm(dim=-1).max().item())
+    assert (two * s - one).abs().max().item() <= 2 * STATE_TOL * norm
+    tol = 2.0 ** -7 * a.float().abs() + 4 * STATE_TOL * norm
+    assert torch.all((a.float() - b.float()).abs() <= tol)
+
+
+def test_keys_of_different_lengths():
+    # key rows of norm 2^-6 .. 2^3 (beta so that beta |k|^2 <= 1), queries of norm 2^-9 .. 2^9
+    w, states = _draw([300, 70], 2, 2, 2, seed=67)
+    g = torch.Generator().manual_seed(68)
+    e = torch.randint(-6, 4, (370, 2), generator=g).to(DEV).float()
+    f = torch.randint(-9, 10, (370, 2), generator=g).to(DEV).float()
+    w.k = (w.k.float() * (2.0 ** e)[..., None]).to(torch.bfloat16)
+    w.beta = w.beta * 2.0 ** (-2 * e).clamp_max(0.0)
+    plain = w.q
+    w.q = (w.q.float() * (2.0 ** f)[..., None]).to(torch.bfloat16)
+    before = states.clone()
+    out = qsa.gated_deltanet_extend(w.q, w.k, w.v, w.log_alpha, w.beta, w.cu_seqlens, states)
+    torch.cuda.synchronize()
+    out = (out.float() * (2.0 ** -f)[..., None]).to(torch.bfloat16)   # exact: as for unit queries
+    w.q = plain
+    # a write is at most beta |k| <= 2^6 times what it is with unit-norm keys, and so is R
+    for s, (a, b) in enumerate(((0, 300), (300, 370))):
+        _compare(out[a:b], states[s], w, a, b, before[s], True)
+
+
+# ---- joins ---------------------------------------------------------------------------------------
+@pytest.mark.parametrize("lens,heads", [([1000, 1000], 4), ([3000], 6), ([2000], 9)])
+def test_extend_cut_with_few_pairs_of_sequence_and_head(lens, heads):
+    # five to nine of them: joins of eight rows a block
+    w, states = _draw(lens, heads, heads, len(lens), seed=69, gate=(0.97, 1.0))
+    before = states.clone()
+    ctx = qsa.DeltaExtend(w.cu_seqlens, heads, DEV)
+    out = ctx.run(w.q, w.k, w.v, w.log_alpha, w.beta, states)
+    torch.cuda.synchronize()
+    assert ctx.device_error() == ("QSA_OK", 0)
+    cu = [int(x) for x in w.cu_seqlens]
+    for s in range(len(lens)):
+        a, b = cu[s], cu[s + 1]
+        _compare(out[a:b], states[s], w, a, b, before[s], True)
