@@ -862,7 +862,8 @@ class Evictor:
     def evict(self, with_kept: bool = False):
         """Cut every sequence of more than keep_blocks complete blocks to keep_blocks (in place;
         the cache's lengths follow).  With with_kept, returns the old indices of the blocks that
-        stay, int32 [B, keep_blocks] (-1 padded)."""
+        stay, int32 [B, keep_blocks] (-1 padded).  The host's lengths (cache.h_len) follow the call,
+        not the replays of a graph that captured it: set them from cache.len after a replay."""
         index = self.mass.get_device()
         kept = (torch.empty((self.cache.batch, self.keep), dtype=torch.int32,
                             device=self.mass.device) if with_kept else None)

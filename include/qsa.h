@@ -429,14 +429,17 @@ QSA_API qsa_status qsa_gated_deltanet(const void *q, const void *k, const void *
  * heads 1..256, a multiple of key_heads: value head h reads key head h / (heads / key_heads).
  * The arithmetic keeps about fp32 accuracy in the states; out is rounded once to bf16.
  * A NaN in log_alpha is carried on (qsa_gated_deltanet takes it for a reset).  What is not finite
- * stays within its sequence and head; in chunks it may reach outputs up to 63 tokens before it.
+ * stays within its sequence and head; in chunks it may reach outputs up to 15 tokens before it.
  * out may be v itself; otherwise neither out nor states overlaps an input or the other
  * (QSA_ERR_INVALID_ARG).
  *
  * qsa_gated_deltanet_extend takes packed sequences as qsa_gated_deltanet does (d_cu_seqlens,
  * h_cu_seqlens, num_seqs; sequences may be empty), in chunks, with scratch space of
- * qsa_gated_deltanet_extend_workspace_size bytes (0: bad arguments).  Calls that may run at the
- * same time need workspaces (and slots) of their own, and so do captured graphs. */
+ * qsa_gated_deltanet_extend_workspace_size bytes (0: bad arguments): 96 KB a chunk of 64 tokens and
+ * head, and 128 KB a segment and head where long sequences are cut, at most 4 GB unless one head
+ * alone needs more (else heads run in passes); calls whose longest sequence has at most 32 tokens
+ * need the header only.  Calls that may run at the same time need workspaces (and slots) of their
+ * own, and so do captured graphs. */
 QSA_API size_t qsa_gated_deltanet_extend_workspace_size(const int32_t *h_cu_seqlens,
                                                         int32_t num_seqs, int32_t key_heads,
                                                         int32_t heads);
@@ -477,6 +480,7 @@ QSA_API qsa_status qsa_gated_deltanet_step(const void *q, const void *k, const v
  * fixed order.  A selected block that is not above the one before it in its row, or not before
  * the own block, is left out and recorded as QSA_ERR_DEVICE, as are a count or a length out of
  * range (nothing is added for that sequence) and a bad page (its keys read as zeros).
+ * A weight is off by a few 2^-22 of itself and by what the fp32 rounding of its logits leaves.
  * workspace: at least QSA_WS_HEADER_BYTES (device status only). */
 QSA_API qsa_status qsa_accumulate_weights(const void *q, const qsa_cache *cache,
                                           const int32_t *sel_idx, const int32_t *sel_cnt,

@@ -207,3 +207,23 @@ def test_extend_cut_with_few_pairs_of_sequence_and_head(lens, heads):
     for s in range(len(lens)):
         a, b = cu[s], cu[s + 1]
         _compare(out[a:b], states[s], w, a, b, before[s], True)
+
+
+# ---- what is not finite --------------------------------------------------------------------------
+@pytest.mark.parametrize("which", ["q", "k", "v", "log_alpha", "beta"])
+def test_extend_not_finite_reaches_no_earlier_group_of_16(which):
+    # token 105 of 200: tokens before 96 come out as without it, and so does the other head
+    w, states = _draw([200], 2, 2, 1, seed=70)
+    clean = states.clone()
+    want = qsa.gated_deltanet_extend(w.q, w.k, w.v, w.log_alpha, w.beta, w.cu_seqlens, clean)
+    getattr(w, which)[105, 1] = float("nan")
+    out = qsa.gated_deltanet_extend(w.q, w.k, w.v, w.log_alpha, w.beta, w.cu_seqlens, states)
+    torch.cuda.synchronize()
+    assert torch.equal(out[:96], want[:96]) and torch.equal(out[:, 0], want[:, 0])
+    assert torch.equal(states[0, 0], clean[0, 0]) and torch.all(torch.isnan(out[105, 1]))
+    if which == "q":      # its own output only
+        assert torch.equal(states, clean)
+        rest = torch.arange(200, device=DEV) != 105
+        assert torch.equal(out[rest], want[rest])
+    else:
+        assert torch.all(torch.isnan(out[106:, 1])) and torch.all(torch.isnan(states[0, 1]))
