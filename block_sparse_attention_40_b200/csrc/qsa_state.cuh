@@ -167,17 +167,18 @@ int join_rows(int64_t heads_seqs) {
 void extend_cuts(const std::vector<std::pair<int64_t, int64_t>>& chunks, int64_t flat, int64_t cuts,
                  int64_t total, int64_t hp, ExtendPlan* p) {
   // Microseconds of the scan, uncut and cut into about k segments: the longest walk, or all walks
-  // in waves over the SMs, at what a chunk was measured to take (2.65 with outputs, 2.4 without),
+  // in waves over the SMs, at what a chunk was measured to take (2.87 with outputs, 2.45 without),
   // and what a launch and a step of the join were.  Cut, first segments run whole beside the inner
   // ones' walks from zero and transitions, then all segments behind the first with outputs.  First
   // ones an eighth shorter, as they write outputs beside walks that do not, or as long as the
   // others, where that saves a shorter sequence a segment.
+  constexpr double kOut = 2.87, kWalk = 2.45;
   const double sms = num_sms();
   // (a CTA takes 8 until its first chunk)
   auto waves_of = [&](double l, double all, double chunk) {
     return std::ceil(std::max(1.0, all / sms / l)) * (8 + chunk * l);
   };
-  double best = 10 + 2.65 * std::max(double(p->max_chunks), double(total) * hp / sms);
+  double best = 10 + kOut * std::max(double(p->max_chunks), double(total) * hp / sms);
   int64_t L = std::max<int64_t>(1, p->max_chunks), F = L;
   const int rows = join_rows(int64_t(p->listed) * hp);
   const double waves = std::ceil(double(p->listed) * hp * (kGdnDim / rows) / sms);
@@ -188,8 +189,9 @@ void extend_cuts(const std::vector<std::pair<int64_t, int64_t>>& chunks, int64_t
       first += double(c.second) * (segs > 1 ? double((2 * segs - 3) * l) : double(c.first));
       rest += double(c.second) * double((segs - 1) * l);
     }
-    const double t = waves_of(double(l), first * hp, 2.4) + (f == l ? 0.25 * double(l) : 0) +
-                     waves * (6 + double(k) * 0.9) + 8 + waves_of(double(l), rest * hp, 2.65);
+    const double t = waves_of(double(l), first * hp, kWalk) +
+                     (f == l ? (kOut - kWalk) * double(l) : 0) +
+                     waves * (6 + double(k) * 0.9) + 8 + waves_of(double(l), rest * hp, kOut);
     if (t < best) {
       best = t;
       L = l;
