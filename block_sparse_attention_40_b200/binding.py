@@ -750,7 +750,8 @@ class DeltaExtend:
         self.heads, self.key_heads = int(heads), int(heads if key_heads is None else key_heads)
         self.lib = load()
         with torch.cuda.device(self.device):
-            self.h_cu, self.d_cu = _cu_pair(cu_seqlens, self.device)
+            # (copies: the caller may fill its tensor with the next lengths)
+            self.h_cu, self.d_cu = (x.clone() for x in _cu_pair(cu_seqlens, self.device))
             self.num_seqs = self.h_cu.numel() - 1
             n = self.lib.qsa_gated_deltanet_extend_workspace_size(
                 ctypes.c_void_p(self.h_cu.data_ptr()), self.num_seqs, self.key_heads, self.heads)

@@ -83,3 +83,19 @@ def test_extend_mixed_in_passes():
         a = alone[:, 0].float()
         tol = 2.0 ** -7 * a.abs() + 4 * STATE_TOL * norm
         assert torch.all((a - out[:, h].float()).abs() <= tol)
+
+
+@pytest.mark.parametrize("where", ["cpu", DEV])
+def test_extend_context_keeps_its_own_lengths(where):
+    # the caller's tensor of lengths is filled with other ones after the context was made
+    w, states = _draw([130, 70], 2, 2, 2, seed=95)
+    twin = states.clone()
+    args = (w.q, w.k, w.v, w.log_alpha, w.beta)
+    want = qsa.gated_deltanet_extend(*args, [0, 130, 200], twin)
+    cu = torch.tensor([0, 130, 200], dtype=torch.int32, device=where)
+    ctx = qsa.DeltaExtend(cu, 2, DEV)
+    cu.copy_(torch.tensor([0, 3, 9], dtype=torch.int32))
+    out = ctx.run(*args, states)
+    torch.cuda.synchronize()
+    assert ctx.device_error() == ("QSA_OK", 0)
+    assert torch.equal(out, want) and torch.equal(states, twin)
