@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import block_sparse_attention_40_b200 as qsa
+from block_sparse_attention_40_b200 import workloads as W
 from tests.gpu_helpers import needs_gpu
 from tests.test_gpu_delta import DEV, STATE_TOL, _check_extend, _draw
 
@@ -99,3 +100,33 @@ def test_extend_context_keeps_its_own_lengths(where):
     torch.cuda.synchronize()
     assert ctx.device_error() == ("QSA_OK", 0)
     assert torch.equal(out, want) and torch.equal(states, twin)
+
+
+def test_extend_on_two_streams_at_once():
+    # two contexts and the prefill attention (which holds tensor memory too), each on a stream of its
+    # own, over and over without a wait between them
+    runs = []
+    for seed, lens, heads in ((96, [3000, 200], 4), (97, [5] * 40 + [1500, 700], 8)):
+        w, states = _draw(lens, heads, heads, len(lens), seed=seed)
+        runs.append((qsa.DeltaExtend(w.cu_seqlens, heads, DEV),
+                     (w.q, w.k, w.v, w.log_alpha, w.beta), states, states.clone()))
+    p = W.prefill("tiny")
+    d = p.to(DEV)
+    pre = qsa.Prefill(p.cu_seqlens, DEV, p.topk)
+    attention = lambda: pre.run(d.q, d.k, d.v, d.q_idx, d.k_idx, d.w)  # noqa: E731
+    want = [[ctx.run(*args, twin).clone() for _ in range(6)] for ctx, args, _, twin in runs]
+    ref = attention().clone()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    got, outs = [[], []], []
+    for _ in range(6):
+        for i, (ctx, args, states, _) in enumerate(runs):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(ctx.run(*args, states))
+        with torch.cuda.stream(streams[2]):
+            outs.append(attention())
+    torch.cuda.synchronize()
+    for i, (ctx, _, states, twin) in enumerate(runs):
+        assert ctx.device_error() == ("QSA_OK", 0) and torch.equal(states, twin)
+        assert all(torch.equal(a, b) for a, b in zip(got[i], want[i]))
+    assert pre.device_error() == ("QSA_OK", 0) and all(torch.equal(o, ref) for o in outs)
