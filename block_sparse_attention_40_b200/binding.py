@@ -35,6 +35,7 @@ EXPORTS = ("qsa_status_string", "qsa_version", "qsa_launch_count", "qsa_workspac
            "qsa_decode_shard_workspace_size", "qsa_decode_shard_select", "qsa_merge_candidates",
            "qsa_decode_shard_attend", "qsa_combine_partials", "qsa_gated_deltanet",
            "qsa_gated_deltanet_extend_workspace_size", "qsa_gated_deltanet_extend",
+           "qsa_gated_deltanet_extend_zeroed",
            "qsa_gated_deltanet_step", "qsa_accumulate_weights", "qsa_accumulate_weights_paged",
            "qsa_evict_workspace_size", "qsa_evict", "qsa_evict_paged", "qsa_set_debug_fault")
 
@@ -111,6 +112,8 @@ def load(build_if_needed: bool = True):
             "qsa_gated_deltanet_extend_workspace_size": ([P, I32, I32, I32], SZ),
             "qsa_gated_deltanet_extend": ([P, P, P, P, P, P, P, I32, I32, I32, P, I32, P, P, P, SZ,
                                            P], st),
+            "qsa_gated_deltanet_extend_zeroed": ([P, P, P, P, P, P, P, I32, I32, I32, P, I32, P, P, P,
+                                                  SZ, P], st),
             "qsa_gated_deltanet_step": ([P, P, P, P, P, I32, I32, P, I32, I32, P, I32, P, P, P], st),
             "qsa_accumulate_weights": ([P, P, P, P, I32, P, P, SZ, P], st),
             "qsa_accumulate_weights_paged": ([P, P, P, P, I32, P, P, SZ, P], st),
@@ -772,11 +775,14 @@ class DeltaExtend:
         if (Hk, H) != (self.key_heads, self.heads):
             raise ValueError(f"{Hk} key heads and {H} heads, the context has {self.key_heads} and "
                              f"{self.heads}")
+        name = "qsa_gated_deltanet_extend"
         if out is None:
-            out = torch.empty_like(v) if slots is None else torch.zeros_like(v)
+            out = torch.empty_like(v)
+            if slots is not None:
+                name = "qsa_gated_deltanet_extend_zeroed"
         if self.T == 0:
             return out
-        _call("qsa_gated_deltanet_extend", index, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+        _call(name, index, q.data_ptr(), k.data_ptr(), v.data_ptr(),
               log_alpha.data_ptr(), beta.data_ptr(), self.d_cu.data_ptr(), self.h_cu.data_ptr(),
               self.num_seqs, Hk, H, states.data_ptr(), states.shape[0], _addr(slots),
               out.data_ptr(), self.ws.data_ptr(), self.ws.numel())

@@ -7,9 +7,9 @@
 //     S <- a S + beta (v - a S k) k^T,   o = S q,      a = exp(max(log_alpha, -87)).
 // heads / key_heads value heads in a row share one key (and query) head.
 //
-// A row's slot is skipped (state and outputs untouched) when it lies outside the pool, which
-// is how rows of a padded batch are marked, or when an earlier row of the call names the same
-// slot: the first row owns it.
+// A row is skipped (state and outputs untouched, or outputs zeroed where zero_skipped says so) when
+// its slot lies outside the pool, which is how rows of a padded batch are marked, or when an earlier
+// row of the call names the same slot: the first row owns it.
 
 #pragma once
 
@@ -37,6 +37,7 @@ struct DeltaArgs {
   int32_t heads, key_heads;
   float* states;            // [num_slots][heads][128][128]
   __nv_bfloat16* out;       // [tokens][heads][128]
+  bool zero_skipped;        // rows of skipped sequences become zero in out
 };
 
 // Row r's first token and number of tokens.
@@ -97,7 +98,17 @@ __global__ void __launch_bounds__(kStepThreads) k_delta_step(DeltaArgs a) {
   int64_t n;
   const int64_t t0 = delta_row_tokens(a, r, &n);
   const int slot = a.slots != nullptr ? a.slots[r] : r;
-  if (n <= 0 || (a.cu != nullptr && n > a.short_len) || slot < 0 || slot >= a.num_slots) return;
+  if (n <= 0 || (a.cu != nullptr && n > a.short_len)) return;
+  auto skip = [&]() {
+    if (a.zero_skipped && l8 == 0)
+      for (int64_t t = t0; t < t0 + n; ++t)
+        for (int i = 0; i < kStepRows; ++i)
+          a.out[(t * a.heads + h) * kGdnDim + v0 + i] = __float2bfloat16(0.f);
+  };
+  if (slot < 0 || slot >= a.num_slots) {
+    skip();
+    return;
+  }
   const int kh = h / (a.heads / a.key_heads);
   float* st = a.states +
               ((static_cast<int64_t>(slot) * a.heads + h) * kGdnDim + v0) * kGdnDim + 4 * l8;
@@ -126,7 +137,10 @@ __global__ void __launch_bounds__(kStepThreads) k_delta_step(DeltaArgs a) {
     for (int i = 0; i < kStepRows; ++i) wv[i] = vp[i];
   };
   fetch(t0);
-  if (delta_slot_taken(a, r, slot)) return;
+  if (delta_slot_taken(a, r, slot)) {
+    skip();
+    return;
+  }
   for (int64_t t = t0; t < t0 + n; ++t) {
     const float al = expf(delta_gate(la));
     const float bt = beta;
@@ -985,9 +999,18 @@ __global__ void __launch_bounds__(kScanThreads, 1)
   const int nc = static_cast<int>(c1 - c0);
   const bool last = c1 == chunks;
   const int slot = a.slots != nullptr && row >= 0 ? a.slots[row] : row;
-  bool idle = nc <= 0 || len <= a.short_len || slot < 0 || slot >= a.num_slots ||
-              (mode == kScanEnds && (seg == 0 ? trans : last));
-  if (!idle) idle = delta_slot_taken(a, row, slot);
+  const bool outputs = mode != kScanEnds || seg == 0;
+  const int64_t t0 = begin + c0 * kGdnChunk;
+  const int ntok = static_cast<int>((last ? len : c1 * kGdnChunk) - c0 * kGdnChunk);
+  bool idle = nc <= 0 || len <= a.short_len || (mode == kScanEnds && (seg == 0 ? trans : last));
+  if (!idle && (slot < 0 || slot >= a.num_slots || delta_slot_taken(a, row, slot))) {
+    idle = true;
+    if (a.zero_skipped && outputs) {
+      pdl_wait();
+      for (int i = tid; i < ntok * 16; i += kScanThreads)
+        reinterpret_cast<uint4*>(a.out)[((t0 + (i >> 4)) * a.heads + h) * 16 + (i & 15)] = make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
   if (!idle && (smem_u32(smem) & 1023u) != 0) {   // the tiles need it; the runtime places them so
     if (tid == 0) report_error(ca.st, kErrDevice, 320);
     idle = true;
@@ -996,7 +1019,6 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     pdl_wait();   // every CTA waits: the kernels after this one count on all before it
     return;
   }
-  const bool outputs = mode != kScanEnds || seg == 0;
   const int64_t rec0 = piece.record, seg0 = piece.segment;
   const int64_t tile = static_cast<int64_t>(kGdnDim) * kGdnDim;
   float* state = a.states + (static_cast<int64_t>(slot) * a.heads + h) * tile;
@@ -1004,8 +1026,6 @@ __global__ void __launch_bounds__(kScanThreads, 1)
   float* ends = ca.seg_state + (seg0 + seg) * seg_stride + hl * tile;
   const float* src = seg > 0 ? ends - seg_stride : state;
   float* dst = last ? state : trans ? ca.seg_trans + (ends - ca.seg_state) : ends;
-  const int64_t t0 = begin + c0 * kGdnChunk;
-  const int ntok = static_cast<int>((last ? len : c1 * kGdnChunk) - c0 * kGdnChunk);
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {

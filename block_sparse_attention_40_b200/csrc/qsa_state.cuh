@@ -288,12 +288,14 @@ extern "C" size_t qsa_gated_deltanet_extend_workspace_size(const int32_t* h_cu_s
   return extend_plan(h_cu_seqlens, num_seqs, heads, &p) ? p.total : 0;
 }
 
-extern "C" qsa_status qsa_gated_deltanet_extend(
-    const void* q, const void* k, const void* v, const float* log_alpha, const float* beta,
-    const int32_t* d_cu_seqlens, const int32_t* h_cu_seqlens, int32_t num_seqs, int32_t key_heads,
-    int32_t heads, float* states, int32_t num_slots, const int32_t* slots, void* out,
-    void* workspace, size_t ws_bytes, qsa_stream_t stream) {
+namespace {
+qsa_status extend_impl(const void* q, const void* k, const void* v, const float* log_alpha,
+                       const float* beta, const int32_t* d_cu_seqlens, const int32_t* h_cu_seqlens,
+                       int32_t num_seqs, int32_t key_heads, int32_t heads, float* states,
+                       int32_t num_slots, const int32_t* slots, void* out, bool zero_skipped,
+                       void* workspace, size_t ws_bytes, qsa_stream_t stream) {
   DeltaChunkArgs a{};
+  a.d.zero_skipped = zero_skipped;
   qsa_status st = extend_check_cu(h_cu_seqlens, num_seqs);
   if (st == QSA_OK)
     st = delta_args(q, k, v, log_alpha, beta, num_seqs, key_heads, heads, states, num_slots, slots,
@@ -366,6 +368,25 @@ extern "C" qsa_status qsa_gated_deltanet_extend(
                              p.segs > 1 ? kScanOutputs : kScanWhole));
   }
   return QSA_OK;
+}
+}  // namespace
+
+extern "C" qsa_status qsa_gated_deltanet_extend(
+    const void* q, const void* k, const void* v, const float* log_alpha, const float* beta,
+    const int32_t* d_cu_seqlens, const int32_t* h_cu_seqlens, int32_t num_seqs, int32_t key_heads,
+    int32_t heads, float* states, int32_t num_slots, const int32_t* slots, void* out,
+    void* workspace, size_t ws_bytes, qsa_stream_t stream) {
+  return extend_impl(q, k, v, log_alpha, beta, d_cu_seqlens, h_cu_seqlens, num_seqs, key_heads, heads,
+                     states, num_slots, slots, out, false, workspace, ws_bytes, stream);
+}
+
+extern "C" qsa_status qsa_gated_deltanet_extend_zeroed(
+    const void* q, const void* k, const void* v, const float* log_alpha, const float* beta,
+    const int32_t* d_cu_seqlens, const int32_t* h_cu_seqlens, int32_t num_seqs, int32_t key_heads,
+    int32_t heads, float* states, int32_t num_slots, const int32_t* slots, void* out,
+    void* workspace, size_t ws_bytes, qsa_stream_t stream) {
+  return extend_impl(q, k, v, log_alpha, beta, d_cu_seqlens, h_cu_seqlens, num_seqs, key_heads, heads,
+                     states, num_slots, slots, out, true, workspace, ws_bytes, stream);
 }
 
 extern "C" qsa_status qsa_gated_deltanet_step(const void* q, const void* k, const void* v,

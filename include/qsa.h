@@ -453,6 +453,17 @@ QSA_API qsa_status qsa_gated_deltanet_extend(const void *q, const void *k, const
                                              void *workspace, size_t ws_bytes,
                                              qsa_stream_t stream);
 
+/* The same, into an out that nothing has written yet: the rows of skipped sequences become zero. */
+QSA_API qsa_status qsa_gated_deltanet_extend_zeroed(const void *q, const void *k, const void *v,
+                                                    const float *log_alpha, const float *beta,
+                                                    const int32_t *d_cu_seqlens,
+                                                    const int32_t *h_cu_seqlens, int32_t num_seqs,
+                                                    int32_t key_heads, int32_t heads,
+                                                    float *states, int32_t num_slots,
+                                                    const int32_t *slots, void *out,
+                                                    void *workspace, size_t ws_bytes,
+                                                    qsa_stream_t stream);
+
 /* qsa_gated_deltanet_step takes n_new tokens of each of batch rows ([batch][n_new] in place of
  * [tokens] above), token by token: one new token a row, or a short drafted run.  counts int32
  * [batch] on the device (each clamped to 0..n_new) or NULL: row b takes its first counts[b]

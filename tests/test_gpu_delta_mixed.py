@@ -130,3 +130,32 @@ def test_extend_on_two_streams_at_once():
         assert ctx.device_error() == ("QSA_OK", 0) and torch.equal(states, twin)
         assert all(torch.equal(a, b) for a, b in zip(got[i], want[i]))
     assert pre.device_error() == ("QSA_OK", 0) and all(torch.equal(o, ref) for o in outs)
+
+
+def test_extend_zeroes_the_rows_of_skipped_sequences_only():
+    # cut into segments, in chunks, token by token: a new out is zero where a slot is outside or was
+    # named before, also over memory that held something else; a given out keeps what it had
+    for lens, slots in (([3000, 2500, 70], [-1, 0, 0]), ([2] * 150 + [90, 40, 300], [0] * 151 + [1, 500]),
+                        ([9, 20, 3], [1, 1, -7])):
+        w, states = _draw(lens, 2, 1, 3, seed=98)
+        twin = states.clone()
+        sl = torch.tensor(slots, dtype=torch.int32, device=DEV)
+        args = (w.q, w.k, w.v, w.log_alpha, w.beta)
+        ctx = qsa.DeltaExtend(w.cu_seqlens, 2, DEV, 1)
+        given = torch.full_like(w.v, 7.0)
+        ctx.run(*args, twin, slots=sl, out=given)
+        junk = torch.full_like(w.v, float("nan"))
+        del junk
+        out = ctx.run(*args, states, slots=sl)
+        torch.cuda.synchronize()
+        assert ctx.device_error() == ("QSA_OK", 0) and torch.equal(states, twin)
+        t = 0
+        seen = set()
+        for n, slot in zip(lens, slots):
+            if 0 <= slot < 3 and slot not in seen:
+                assert torch.equal(out[t:t + n], given[t:t + n])
+            else:
+                assert torch.count_nonzero(out[t:t + n]).item() == 0
+                assert torch.all(given[t:t + n] == 7.0)
+            seen.add(slot)
+            t += n
