@@ -85,7 +85,7 @@ __device__ __forceinline__ void unpack_bf16x2(uint32_t w, float* f) {
 // pass, and the reductions are three shuffles.  A token's inputs are fetched while the one before
 // it is taken.  Bound by the state's bytes: 128 KB per (row, head) against about 4.5 KB of
 // everything else at one token.  64 rows x 32 heads x 1 token: 45 us, 6.0 TB/s, 92% of the measured
-// copy rate; 24 rows of up to 5 tokens x 16 heads: 9.8 us a call (its states' bytes take 6.9).
+// copy rate; 24 rows of up to 5 tokens x 16 heads: 10 us a call (its states' bytes take 6.9).
 constexpr int kStepThreads = 128;
 constexpr int kStepRows = 2;
 
@@ -468,8 +468,8 @@ __device__ __forceinline__ void bulk_store_wait() {
 // splits into parts) outweigh them and take registers, and since with four CTAs an SM the phases
 // of one fill the gaps of another.  The record leaves in pieces, out of the space of an operand
 // that is done with: Q becomes the scaled fp16 Q in place, then holds M, then V; K and Tu become W.
-// 16,384 chunks (8 x 8,192 tokens x 16 heads): 580 us, 5.2 us of an SM a chunk, bound by shared
-// memory (68% of its cycles; instructions issue in 54%; three CTAs an SM take as long); the bytes
+// 16,384 chunks (8 x 8,192 tokens x 16 heads): 570 us, 5.2 us of an SM a chunk, bound by shared
+// memory (68% of its cycles; instructions issue in 56%; three CTAs an SM take as long); the bytes
 // (48 KB in, 96 KB out) would take 360 us.
 constexpr int kPrepThreads = 256;
 constexpr int kPrepLdA = kGdnChunk + 8;   // fp32 row stride of L / Tu: 8 rows x 4 pairs without conflicts
@@ -880,15 +880,16 @@ __global__ void __launch_bounds__(kPrepThreads, 4) k_delta_prep(DeltaChunkArgs c
 // U' and then S; two write the outputs; one warp issues the products and three load, each its own
 // operands, whose space is free again as soon as their last product is done.
 //
-// Bound by the chain of a chunk, S -> D_W -> U' -> D_S -> S, 4,700 cycles (2.65 us): about 1,000
-// for D_W (16 products of 128 x 64 or 128 x 128 x 16), 1,150 for U', 1,000 for D_S (12 of 128 x 128
-// x 16), 1,600 for S, most of whose conversion is instruction issue (two products' parts, 5 to 9
-// instructions an element).  S goes over in two parts, so that the products of one run while the
-// other is converted; S is scaled before it is known, by a bound on its rows,
-// |S| <= e^(g_C) max|S0| + 64 max|U'| max|K|; what only the outputs need (D_Q)
-// runs in the gaps.  A form without W (X = V - e^g K S0^T, U = T X) would read 32 KB less a chunk
-// and have one more product and conversion in the chain.  8 x 8,192 tokens x 16 heads: 387 us on 128
-// SMs (121 KB a chunk: 5.1 TB/s); the same walk with fp32 state in shared memory and warp MMAs
+// Bound by the chain of a chunk, S -> D_W -> U' -> D_S -> S, 2.87 us (2.45 where no outputs are
+// written): about 1,000 cycles for D_W (16 products of 128 x 64 or 128 x 128 x 16), 1,250 for U',
+// 1,000 for D_S (12 of 128 x 128 x 16), 1,600 for S, most of whose conversion is instruction issue
+// (two products' parts, 5 to 9 instructions an element).  S goes over in two parts, so that the
+// products of one run while the other is converted; S is scaled before it is known, by a bound on
+// its rows, |S| <= e^(g_C) max|S0| + 64 max|U'| max|K|; what only the outputs need (D_Q) runs in the
+// gaps, but for 0.1 us that the next D_W waits for the 24 products of U^T M^T (12, of parts to 2^-17,
+// measured that much less).  A form without W (X = V - e^g K S0^T, U = T X) would read 32 KB less a
+// chunk and have one more product and conversion in the chain.  8 x 8,192 tokens x 16 heads: 432 us on
+// 128 SMs (129 KB a chunk: 4.9 TB/s); the same walk with fp32 state in shared memory and warp MMAs
 // (k_gated_deltanet, preparation included) takes 2.6 ms.
 constexpr int kScanThreads = 896;
 constexpr int kScanW = 0;                               // [2] W, K, gates
