@@ -148,10 +148,10 @@ struct ExtendPlan {
 };
 
 // Where a call has no longer pieces than 32 tokens, all go token by token (a piece of 30 tokens x 4
-// heads: 12.5 us against 26.6 by chunks).  Beside longer pieces, those of at most 16 do where
+// heads: 11.4 us against 24.6 by chunks).  Beside longer pieces, those of at most 16 do where
 // they would fill the SMs by themselves, since a walk by chunks holds an SM for 10 us (48 pieces of
-// 1 to 64 tokens x 16 heads: 95 us against 132); fewer ride along (7 pieces, one of 1 token, x 4
-// heads: 65.6 us against 69.7 with a launch more).
+// 1 to 64 tokens x 16 heads: 107 us against 128); fewer ride along (7 pieces, one of 1 token, x 4
+// heads: 71.1 us against 72.3 with their launch and the list's).
 constexpr int32_t kShortAll = 32, kShortMany = 16;
 constexpr int64_t kExtendBudget = int64_t(1) << 32;   // bytes of scratch, above which heads run in passes
 
